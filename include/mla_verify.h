@@ -72,6 +72,7 @@ typedef enum {
 #define MLA_DEV_BAD_SLOT 0x1u  /* a slot index outside [0, n_pool); pool row 0 was read instead */
 #define MLA_DEV_BAD_LEN 0x2u   /* a seq_len outside [q_len, slot_stride]; that stream was skipped */
 #define MLA_DEV_TIMEOUT 0x4u   /* a bounded device-side wait expired (or the pipeline could not start); the CTA gave up */
+#define MLA_DEV_BAD_DRAFT 0x8u /* a draft node with a bad parent or token (it was passed over), or a row without probability */
 
 /* Supported ranges. */
 #define MLA_D_QK 576           /* query / key width: 512 latent + 64 rope */
@@ -79,6 +80,7 @@ typedef enum {
 #define MLA_MAX_Q_LEN 64        /* drafts per stream: a draft tree of up to 64 nodes */
 #define MLA_MAX_HEADS 128
 #define MLA_MAX_NSPLIT 1024
+#define MLA_MAX_VOCAB (1 << 24)
 
 /*
  * Bytes of workspace that mla_verify_attn() needs for `nsplit` key splits
@@ -239,6 +241,104 @@ int mla_sparse_fp8_partials(const void* q, const uint8_t* kv_lat_e4m3, const flo
                             int64_t n_pool, const int32_t* topk_slots, int topk, int B, int H, float scale,
                             float* out, float* lse, int nsplit, void* workspace, size_t ws_bytes,
                             mla_stream_t stream);
+
+/*
+ * Norm and position rotation of a step's queries and new key rows, in one launch, as
+ * they come from their projections.  For every row x[0:576] of token t:
+ *     y[d] = w[d] * x[d] / sqrt(mean_{e<512} x[e]^2 + eps)        d < 512 (w NULL: y[d] = x[d])
+ *     y[a] = x[a] cos - x[b] sin,  y[b] = x[b] cos + x[a] sin     32 rope pairs (a, b)
+ * with the angle positions[t] * inv_freq[i] of pair i (reduced exactly, so far positions
+ * keep full precision), (a, b) = (512 + 2i, 512 + 2i + 1) when `interleaved`, else
+ * (512 + i, 544 + i).  Statistics and products are fp32, one rounding to bf16 at the end.
+ *   q          bf16 [n_tokens, H, 576] or NULL (no queries); q_out the same shape
+ *   kv         bf16 [n_tokens, 576] or NULL (no key rows); kv_out the same shape
+ *   q_weight   bf16 [512], shared by the heads, or NULL: the queries' latent dims pass
+ *              unchanged; kv_weight bf16 [512] or NULL likewise
+ *   positions  int32 [n_tokens] (any sign); inv_freq fp32 [32], radians a position
+ *   eps        finite, >= 0
+ * Every tensor but positions and inv_freq is 16-byte aligned.  An output may be its input
+ * (in place); other overlaps are not allowed.
+ * Limits: 1 <= H <= 128, 0 <= n_tokens <= 2^31 - 1 (0 is a no-op).
+ */
+int mla_qk_norm_rope(const void* q, const void* kv, const void* q_weight, const void* kv_weight,
+                     const int32_t* positions, const float* inv_freq, float eps, int interleaved, int64_t n_tokens,
+                     int H, void* q_out, void* kv_out, mla_stream_t stream);
+
+/*
+ * Quantising append to the fp8 cache: bf16 row i, rows[i, 0:576], goes to pool row slots[i] as
+ *     kv_scale = max_{d<512} |x[d]| / 448            (fp32, over the finite values)
+ *     kv_lat[d] = e4m3(x[d] / kv_scale)              (fp32 quotient, round to nearest even)
+ *     kv_rope   = x[512:576]                         (bf16, as it is)
+ * 448 is the largest e4m3 value.  An infinity saturates to +-448, a NaN becomes the NaN
+ * code, a row of zeros gets scale 0.
+ *   kv_lat uint8 [n_pool, 512], kv_scale fp32 [n_pool], kv_rope bf16 [n_pool, 64]: written
+ *   slots int32 [n_rows], distinct in one call (which of two rows lands in a shared slot is
+ *   unspecified, and its parts may come from both); rows bf16 [n_rows, 576]
+ * kv_lat, kv_rope and rows are 16-byte aligned.  A slot outside [0, n_pool) skips that row and
+ * sets MLA_DEV_BAD_SLOT.  n_rows == 0 is a no-op.
+ */
+int mla_kv_append_quant(uint8_t* kv_lat, float* kv_scale, void* kv_rope, int64_t n_pool, const int32_t* slots,
+                        const void* rows, int n_rows, mla_stream_t stream);
+
+/*
+ * Reads cached rows back: out[i] = [ bf16(kv_scale[s] * decode_e4m3(kv_lat[s])) | kv_rope[s] ]
+ * with s = slots[i] (duplicates allowed), one rounding.  out bf16 [n_rows, 576]; alignment
+ * as for mla_kv_append_quant().  A slot outside [0, n_pool) gives a row of zeros and sets
+ * MLA_DEV_BAD_SLOT.
+ */
+int mla_kv_read_fp8(const uint8_t* kv_lat, const float* kv_scale, const void* kv_rope, int64_t n_pool,
+                    const int32_t* slots, void* out, int n_rows, mla_stream_t stream);
+
+/*
+ * Verify attention over the fp8 latent cache: mla_verify_attn() with the keys
+ *     k_j = [ kv_scale[s_j] * decode_e4m3(kv_lat[s_j]) | kv_rope[s_j] ],  s_j = slot_table[b, j]
+ * and their first 512 dims as values.  The keys enter the scores without a rounding of their
+ * own; the probabilities are rounded once for the product with the values.
+ *   kv_lat uint8 [n_pool, 512], kv_scale fp32 [n_pool] (>= 0), kv_rope bf16 [n_pool, 64], as
+ *              mla_kv_append_quant() leaves them (lat / rope 16-byte aligned)
+ *   draft_mask / draft_mask_bits  the mask of mla_verify_attn() or of
+ *              mla_verify_attn_packed(); at most one of them, both NULL = causal chain
+ *   out        bf16 [B, q_len, H, 512], 16-byte aligned, each value rounded once from fp32
+ *   lse        fp32 [B, q_len, H]
+ * Every other argument, limit, workspace size and device status is that of mla_verify_attn().
+ * q_len = 1 is plain decode.
+ */
+int mla_verify_attn_fp8(const void* q, const uint8_t* kv_lat, const float* kv_scale, const void* kv_rope,
+                        int64_t n_pool, const int32_t* slot_table, int slot_stride, const int32_t* seq_lens,
+                        const uint8_t* draft_mask, const uint64_t* draft_mask_bits, int B, int q_len, int H,
+                        float scale, void* out, float* lse, int nsplit, void* workspace, size_t ws_bytes,
+                        mla_stream_t stream);
+
+/*
+ * Acceptance of drafted tokens from given random numbers, the step after a verify pass:
+ * rejection sampling down the draft chain or tree, so that the tokens that come out are
+ * distributed as the target's.  Node 0 is the stream's last committed token.  At the current
+ * node c (0 at first), with R = target_probs[c] and S = 1, the children are tried in index order:
+ *     child k with token x is accepted and becomes c   iff  u_accept[k] * q(x) * S < R(x)
+ *     otherwise  R <- max(R - S q, 0),  S <- sum R                    q = draft_probs[c]
+ * With no child left, the next token is the lowest i with R(0) + .. + R(i) > u_next * sum R
+ * (R = target_probs[c] again where nothing is left of R).
+ *   target_probs fp32 [B, q_len, vocab]: row t is the target's distribution after node t
+ *   draft_probs  fp32 [B, q_len, vocab]: row t is the distribution that node t's children were
+ *                drawn from; NULL: the drafts were chosen, not drawn (q is 1 at the token: it
+ *                is accepted iff u_accept * S < R(x), and taken out of R otherwise)
+ *   draft_tokens int32 [B, q_len] (node 0's is not read for anything)
+ *   parents      int32 [B, q_len], parents[i] < i; -1: the node is not there (a padded tree);
+ *                parents[0] is ignored; NULL = chain (parents[i] = i - 1)
+ *   u_accept     fp32 [B, q_len], u_next fp32 [B]: uniform in [0, 1)
+ *   n_accepted   int32 [B]: accepted drafts, 0..q_len-1
+ *   tokens       int32 [B, q_len]: the accepted drafts' tokens, the next token, then -1
+ *   path         int32 [B, q_len]: the accepted drafts' nodes, then -1
+ * Probabilities count as 0 where they are negative or NaN and as 1 above 1; rows need not
+ * sum to exactly 1.  Sums are integers of 2^-45, so results do not depend on the order of
+ * summation.  A node whose token is outside [0, vocab) or whose parent is outside [-1, i)
+ * is passed over and sets MLA_DEV_BAD_DRAFT; a current node without any probability gives the
+ * next token -1 and sets it too.  target_probs and draft_probs are 16-byte aligned.
+ * Limits: 1 <= q_len <= 64, 0 <= B <= 65535, 1 <= vocab <= MLA_MAX_VOCAB.
+ */
+int mla_draft_verify(const float* target_probs, const float* draft_probs, const int32_t* draft_tokens,
+                     const int32_t* parents, const float* u_accept, const float* u_next, int B, int q_len, int vocab,
+                     int32_t* n_accepted, int32_t* tokens, int32_t* path, mla_stream_t stream);
 
 /*
  * Verify attention without a caller-provided workspace, for callers that cannot

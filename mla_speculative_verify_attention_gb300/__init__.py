@@ -28,13 +28,14 @@ MLA_OK = 0
 STATUS_NAMES = {0: "MLA_OK", -1: "MLA_ERR_NULL", -2: "MLA_ERR_SHAPE", -3: "MLA_ERR_ALIGN",
                 -4: "MLA_ERR_WORKSPACE", -5: "MLA_ERR_NSPLIT", -6: "MLA_ERR_LAUNCH",
                 -7: "MLA_ERR_DEVICE", -8: "MLA_ERR_ARG"}
-DEV_BAD_SLOT, DEV_BAD_LEN, DEV_TIMEOUT = 0x1, 0x2, 0x4
+DEV_BAD_SLOT, DEV_BAD_LEN, DEV_TIMEOUT, DEV_BAD_DRAFT = 0x1, 0x2, 0x4, 0x8
 
 EXPORTS = ("mla_verify_workspace_bytes", "mla_verify_auto_nsplit", "mla_verify_attn",
            "mla_verify_partials", "mla_verify_combine", "mla_verify_status",
            "mla_status_string", "mla_verify_version", "mla_verify_attn_static_scratch",
            "mla_sparse_fp8_decode", "mla_sparse_fp8_partials", "mla_verify_attn_packed", "mla_kv_append", "mla_kv_append_fp8",
-           "mla_debug_stall_next_launch", "mla_debug_rescale_count")
+           "mla_debug_stall_next_launch", "mla_debug_rescale_count", "mla_qk_norm_rope", "mla_kv_append_quant",
+           "mla_kv_read_fp8", "mla_verify_attn_fp8", "mla_draft_verify")
 STATIC_SCRATCH_BYTES = 64 << 20
 
 _lib = None
@@ -79,6 +80,16 @@ def load():
     L.mla_kv_append.restype = I
     L.mla_kv_append_fp8.argtypes = [P, P, P, I64, P, P, P, P, I, P]
     L.mla_kv_append_fp8.restype = I
+    L.mla_qk_norm_rope.argtypes = [P, P, P, P, P, P, F, I, I64, I, P, P, P]
+    L.mla_qk_norm_rope.restype = I
+    L.mla_kv_append_quant.argtypes = [P, P, P, I64, P, P, I, P]
+    L.mla_kv_append_quant.restype = I
+    L.mla_kv_read_fp8.argtypes = [P, P, P, I64, P, P, I, P]
+    L.mla_kv_read_fp8.restype = I
+    L.mla_verify_attn_fp8.argtypes = [P, P, P, P, I64, P, I, P, P, P, I, I, I, F, P, P, I, P, SZ, P]
+    L.mla_verify_attn_fp8.restype = I
+    L.mla_draft_verify.argtypes = [P, P, P, P, P, P, I, I, I, P, P, P, P]
+    L.mla_draft_verify.restype = I
     L.mla_verify_combine.argtypes = [P, P, I, I, I, I, P, P, P]
     L.mla_verify_combine.restype = I
     L.mla_verify_status.argtypes = [P, ctypes.POINTER(ctypes.c_uint32), I]
@@ -328,6 +339,214 @@ def verify_combine(part_out: torch.Tensor, part_lse: torch.Tensor, B: int, q_len
     rc = L.mla_verify_combine(_ptr(part_out), _ptr(part_lse), B, q_len, H, S, _ptr(out), _ptr(lse), _stream(stream))
     _check("mla_verify_combine", rc)
     return out, lse
+
+
+class _Launch:
+    """Context of one call of the operators below: every tensor is a contiguous CUDA tensor of
+    one device, that device is the current one inside, and `stream` (default: the device's
+    current stream) is where the call is enqueued and what its own outputs and workspace are
+    allocated for, so that their memory is not handed out again before the call has run."""
+
+    def __init__(self, stream, *tensors):
+        self.device = None
+        for t in tensors:
+            if t is None:
+                continue
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError("all tensors must be contiguous CUDA tensors")
+            if self.device is None:
+                self.device = t.device
+            elif t.device != self.device:
+                raise ValueError("all tensors must be on the same device")
+        if stream is not None and stream.device != self.device:
+            raise ValueError("the stream must belong to the tensors' device")
+        self.given = stream
+
+    def __enter__(self):
+        self.guard = None
+        if self.device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        self.stream = self.given if self.given is not None else torch.cuda.current_stream()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    @property
+    def ptr(self):
+        return self.stream.cuda_stream
+
+    def empty(self, shape, dtype):
+        if self.given is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.given):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+
+def _want(name, t, dtype, shape):
+    """`t` has this dtype and shape (None: any size)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {str(dtype).replace('torch.', '')}, not {str(t.dtype).replace('torch.', '')}")
+    if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {list(shape)}, not {list(t.shape)}")
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def qk_norm_rope(q: Optional[torch.Tensor], kv: Optional[torch.Tensor], positions: torch.Tensor,
+                 inv_freq: torch.Tensor, *, q_weight: Optional[torch.Tensor] = None,
+                 kv_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = True,
+                 q_out: Optional[torch.Tensor] = None, kv_out: Optional[torch.Tensor] = None, stream=None):
+    """mla_qk_norm_rope: RMS norm of the 512 latent dims (where a weight [512] is given) and
+    position rotation of the 64 rope dims of the queries q [..., H, 576] and the key rows
+    kv [..., 576] (bf16; either may be None), for positions int32 [...] and inv_freq fp32
+    [32].  Returns (q_out, kv_out); an output may be its input."""
+    if q is None and kv is None:
+        raise ValueError("qk_norm_rope needs q or kv")
+    lead = tuple(positions.shape)
+    _want("positions", positions, torch.int32, lead)
+    _want("inv_freq", inv_freq, torch.float32, (32,))
+    H = 1
+    if q is not None:
+        _want("q", q, torch.bfloat16, lead + (None, D_QK))
+        H = q.shape[-2]
+    if kv is not None:
+        _want("kv", kv, torch.bfloat16, lead + (D_QK,))
+    for name, w in (("q_weight", q_weight), ("kv_weight", kv_weight)):
+        if w is not None:
+            _want(name, w, torch.bfloat16, (D_V,))
+    for name, o, x in (("q_out", q_out, q), ("kv_out", kv_out, kv)):
+        if o is not None:
+            if x is None:
+                raise ValueError(f"{name} without its input")
+            _want(name, o, torch.bfloat16, tuple(x.shape))
+    with _Launch(stream, q, kv, positions, inv_freq, q_weight, kv_weight, q_out, kv_out) as at:
+        if q is not None and q_out is None:
+            q_out = at.empty(q.shape, torch.bfloat16)
+        if kv is not None and kv_out is None:
+            kv_out = at.empty(kv.shape, torch.bfloat16)
+        _check("mla_qk_norm_rope", load().mla_qk_norm_rope(
+            _addr(q), _addr(kv), _addr(q_weight), _addr(kv_weight), positions.data_ptr(), inv_freq.data_ptr(),
+            float(eps), 1 if interleaved else 0, positions.numel(), H, _addr(q_out), _addr(kv_out), at.ptr))
+    return q_out, kv_out
+
+
+def _want_fp8_cache(kv_lat, kv_scale, kv_rope):
+    _want("kv_lat", kv_lat, torch.uint8, (None, D_V))
+    _want("kv_scale", kv_scale, torch.float32, (kv_lat.shape[0],))
+    _want("kv_rope", kv_rope, torch.bfloat16, (kv_lat.shape[0], D_QK - D_V))
+
+
+def kv_append_quant(kv_lat: torch.Tensor, kv_scale: torch.Tensor, kv_rope: torch.Tensor, slots: torch.Tensor,
+                    rows: torch.Tensor, stream=None) -> None:
+    """mla_kv_append_quant: quantises rows [n, 576] (bf16) into the fp8 cache (kv_lat uint8
+    [n_pool, 512], kv_scale fp32 [n_pool], kv_rope bf16 [n_pool, 64]) at pool rows slots [n]
+    (int32, distinct)."""
+    _want_fp8_cache(kv_lat, kv_scale, kv_rope)
+    _want("slots", slots, torch.int32, (None,))
+    _want("rows", rows, torch.bfloat16, (slots.shape[0], D_QK))
+    with _Launch(stream, kv_lat, kv_scale, kv_rope, slots, rows) as at:
+        _check("mla_kv_append_quant", load().mla_kv_append_quant(
+            kv_lat.data_ptr(), kv_scale.data_ptr(), kv_rope.data_ptr(), kv_lat.shape[0], slots.data_ptr(),
+            rows.data_ptr(), slots.shape[0], at.ptr))
+
+
+def kv_read_fp8(kv_lat: torch.Tensor, kv_scale: torch.Tensor, kv_rope: torch.Tensor, slots: torch.Tensor, *,
+                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """mla_kv_read_fp8: the cached rows slots [n] as bf16 [n, 576], bf16(scale * code) | rope."""
+    _want_fp8_cache(kv_lat, kv_scale, kv_rope)
+    _want("slots", slots, torch.int32, (None,))
+    if out is not None:
+        _want("out", out, torch.bfloat16, (slots.shape[0], D_QK))
+    with _Launch(stream, kv_lat, kv_scale, kv_rope, slots, out) as at:
+        if out is None:
+            out = at.empty((slots.shape[0], D_QK), torch.bfloat16)
+        _check("mla_kv_read_fp8", load().mla_kv_read_fp8(
+            kv_lat.data_ptr(), kv_scale.data_ptr(), kv_rope.data_ptr(), kv_lat.shape[0], slots.data_ptr(),
+            out.data_ptr(), slots.shape[0], at.ptr))
+    return out
+
+
+def verify_attn_fp8(q: torch.Tensor, kv_lat: torch.Tensor, kv_scale: torch.Tensor, kv_rope: torch.Tensor,
+                    slot_table: torch.Tensor, seq_lens: torch.Tensor, draft_mask: Optional[torch.Tensor],
+                    scale: float, *, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    nsplit: int = 0, workspace: Optional[torch.Tensor] = None,
+                    stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """mla_verify_attn_fp8: verify_attn over the fp8 cache of kv_append_quant; out bf16
+    [B, q_len, H, 512] and lse fp32 [B, q_len, H].  ``draft_mask`` is uint8 [B, q_len, q_len],
+    bit-packed int64 [B, q_len], or None (causal chain); ``workspace`` as for verify_attn."""
+    _want("q", q, torch.bfloat16, (None, None, None, D_QK))
+    B, q_len, H, _ = q.shape
+    _want_fp8_cache(kv_lat, kv_scale, kv_rope)
+    _want("slot_table", slot_table, torch.int32, (B, None))
+    _want("seq_lens", seq_lens, torch.int32, (B,))
+    mask = bits = None
+    if draft_mask is not None:
+        if draft_mask.dtype == torch.int64:
+            _want("draft_mask", draft_mask, torch.int64, (B, q_len))
+            bits = draft_mask.data_ptr()
+        else:
+            _want("draft_mask", draft_mask, torch.uint8, (B, q_len, q_len))
+            mask = draft_mask.data_ptr()
+    if out is not None:
+        _want("out", out, torch.bfloat16, (B, q_len, H, D_V))
+    if lse is not None:
+        _want("lse", lse, torch.float32, (B, q_len, H))
+    if workspace is not None:
+        _want("workspace", workspace, torch.uint8, (None,))
+    with _Launch(stream, q, kv_lat, kv_scale, kv_rope, slot_table, seq_lens, draft_mask, out, lse, workspace) as at:
+        if out is None:
+            out = at.empty((B, q_len, H, D_V), torch.bfloat16)
+        if lse is None:
+            lse = at.empty((B, q_len, H), torch.float32)
+        if workspace is None:
+            ns = nsplit if nsplit > 0 else auto_nsplit(B, q_len, H, slot_table.shape[1], num_sms(q.device), 1 << 62)
+            workspace = at.empty(max(workspace_bytes(B, q_len, H, ns), 256), torch.uint8)
+        _check("mla_verify_attn_fp8", load().mla_verify_attn_fp8(
+            q.data_ptr(), kv_lat.data_ptr(), kv_scale.data_ptr(), kv_rope.data_ptr(), kv_lat.shape[0],
+            slot_table.data_ptr(), slot_table.shape[1], seq_lens.data_ptr(), mask, bits, B, q_len, H, float(scale),
+            out.data_ptr(), lse.data_ptr(), nsplit, workspace.data_ptr(), workspace.numel(), at.ptr))
+    return out, lse
+
+
+def draft_verify(target_probs: torch.Tensor, draft_probs: Optional[torch.Tensor], draft_tokens: torch.Tensor,
+                 parents: Optional[torch.Tensor], u_accept: torch.Tensor, u_next: torch.Tensor, *,
+                 n_accepted: Optional[torch.Tensor] = None, tokens: Optional[torch.Tensor] = None,
+                 path: Optional[torch.Tensor] = None,
+                 stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """mla_draft_verify: rejection sampling down the draft chain (parents None) or tree.
+    target_probs and draft_probs (None: drafts chosen, not drawn) are fp32 [B, q_len, vocab],
+    draft_tokens and parents int32 [B, q_len], u_accept fp32 [B, q_len], u_next fp32 [B].
+    Returns (n_accepted [B], tokens [B, q_len], path [B, q_len]), int32: the accepted drafts'
+    tokens followed by the next token, and the accepted drafts' nodes, padded with -1."""
+    _want("target_probs", target_probs, torch.float32, (None, None, None))
+    B, q_len, vocab = target_probs.shape
+    if draft_probs is not None:
+        _want("draft_probs", draft_probs, torch.float32, (B, q_len, vocab))
+    _want("draft_tokens", draft_tokens, torch.int32, (B, q_len))
+    if parents is not None:
+        _want("parents", parents, torch.int32, (B, q_len))
+    _want("u_accept", u_accept, torch.float32, (B, q_len))
+    _want("u_next", u_next, torch.float32, (B,))
+    if n_accepted is not None:
+        _want("n_accepted", n_accepted, torch.int32, (B,))
+    for name, t in (("tokens", tokens), ("path", path)):
+        if t is not None:
+            _want(name, t, torch.int32, (B, q_len))
+    with _Launch(stream, target_probs, draft_probs, draft_tokens, parents, u_accept, u_next, n_accepted, tokens,
+                 path) as at:
+        n_accepted = at.empty((B,), torch.int32) if n_accepted is None else n_accepted
+        tokens = at.empty((B, q_len), torch.int32) if tokens is None else tokens
+        path = at.empty((B, q_len), torch.int32) if path is None else path
+        _check("mla_draft_verify", load().mla_draft_verify(
+            target_probs.data_ptr(), _addr(draft_probs), draft_tokens.data_ptr(), _addr(parents),
+            u_accept.data_ptr(), u_next.data_ptr(), B, q_len, vocab, n_accepted.data_ptr(), tokens.data_ptr(),
+            path.data_ptr(), at.ptr))
+    return n_accepted, tokens, path
 
 
 def device_status(stream=None, clear: bool = True) -> int:

@@ -14,6 +14,7 @@ constexpr int D_V = 512;
 constexpr unsigned DEV_BAD_SLOT = 0x1u;
 constexpr unsigned DEV_BAD_LEN = 0x2u;
 constexpr unsigned DEV_TIMEOUT = 0x4u;
+constexpr unsigned DEV_BAD_DRAFT = 0x8u;
 
 // One verify launch.  Row r of stream b is (t, h) with r = t * H + h, the
 // natural order of q [B, q_len, H, 576] and out [B, q_len, H, 512].
@@ -146,6 +147,31 @@ __device__ inline void balanced_stream(const BalancedPlan& P, int b, int* first,
 
 constexpr int BALANCED_MAX_STREAMS = 64;
 
+// Status word's device address and SM count of the current device (MLA_OK or
+// MLA_ERR_DEVICE: no sm_103 device, or a CUDA runtime error); any output may be null.
+int device_state(int* dev_out, unsigned** status, int* num_sms);
+
+inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// Launch as a programmatic dependent of the kernel before it on the stream: the kernel
+// starts with griddepcontrol.wait, which holds it until that kernel's writes are visible.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                             Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+
 // One-shot test hook, consumed by the next split-kernel launch on any device.
 bool take_debug_stall();
 
@@ -163,6 +189,9 @@ cudaError_t launch_kv_append_fp8(uint8_t* kv_lat, float* kv_scale, __nv_bfloat16
                                  const __nv_bfloat16* new_rope, int n_rows, unsigned* status, cudaStream_t stream);
 cudaError_t launch_combine(const float* part_out, const float* part_lse, long long n_rows, int S,
                            float* out, float* lse, cudaStream_t stream);
+// The same merge with the output rounded to bf16.
+cudaError_t launch_combine_bf16(const float* part_out, const float* part_lse, long long n_rows, int S,
+                                __nv_bfloat16* out, float* lse, cudaStream_t stream);
 // Combine of a balanced split (slot-major partials of VerifyArgs::balanced).
 cudaError_t launch_combine_balanced(const VerifyArgs& a, cudaStream_t stream);
 

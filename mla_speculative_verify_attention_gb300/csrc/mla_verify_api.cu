@@ -30,6 +30,8 @@ unsigned long long* g_rescales_ptr[MAX_DEVICES];
 int g_num_sms[MAX_DEVICES];
 int g_arch_ok[MAX_DEVICES];      // 0 unknown, 1 sm_103, -1 other
 
+}  // namespace
+
 // Device properties and the status word's device address for the current device.
 int device_state(int* dev_out, unsigned** status, int* num_sms) {
     int dev = 0;
@@ -55,8 +57,7 @@ int device_state(int* dev_out, unsigned** status, int* num_sms) {
     return MLA_OK;
 }
 
-inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+namespace {
 
 // ---------------------------------------------------------------------------
 // Combine.  A work item is (row, 128 output dims); Z warps (Z = 1, 2, 4 or 8, more for
@@ -85,10 +86,18 @@ struct CombineBalanced {
     int B, q_len, slot_stride, G, rows;
 };
 
-template <int Z>
+// The merged sums are fp32; a bf16 output rounds each of them once.
+__device__ __forceinline__ void store4(float* dst, const float4& v) { *reinterpret_cast<float4*>(dst) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* dst, const float4& v) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+template <int Z, typename Out>
 __global__ void __launch_bounds__(CB_THREADS) combine_kernel(const float* __restrict__ part_out,
                                                              const float* __restrict__ part_lse, int S_all,
-                                                             long long n_items, float* __restrict__ out,
+                                                             long long n_items, Out* __restrict__ out,
                                                              float* __restrict__ lse, const CombineBalanced bal) {
     __shared__ float4 red[CB_WARPS][32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, z = warp % Z;
@@ -178,37 +187,27 @@ __global__ void __launch_bounds__(CB_THREADS) combine_kernel(const float* __rest
             }
     }
     if (valid && z == 0) {
-        reinterpret_cast<float4*>(out + row * D_V + quarter * CB_DIMS)[lane] = acc;
+        store4(out + row * D_V + quarter * CB_DIMS + lane * 4, acc);
         if (quarter == 0 && lane == 0) lse[row] = bad ? __int_as_float(0x7fc00000) : (live ? L : -INFINITY);
     }
 }
 
-template <int Z>
-cudaError_t launch_combine_z(const float* part_out, const float* part_lse, long long n_rows, int S, float* out,
+template <int Z, typename Out>
+cudaError_t launch_combine_z(const float* part_out, const float* part_lse, long long n_rows, int S, Out* out,
                              float* lse, const CombineBalanced& bal, cudaStream_t stream) {
     const long long items = n_rows * (D_V / CB_DIMS);
     const long long per_cta = CB_WARPS / Z;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((items + per_cta - 1) / per_cta));
-    cfg.blockDim = dim3(CB_THREADS);
-    cfg.dynamicSmemBytes = 0;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, combine_kernel<Z>, part_out, part_lse, S, items, out, lse, bal);
+    return launch_dependent(combine_kernel<Z, Out>, dim3((unsigned)((items + per_cta - 1) / per_cta)),
+                            dim3(CB_THREADS), 0, stream, part_out, part_lse, S, items, out, lse, bal);
 }
-
-}  // namespace
 
 // Z: warps per item, from the split count (up to 16 splits per warp, 8 warps at most;
 // balanced partials: a stream holds at most all slots, typically a few dozen; two warps
 // per item keep the grid near one wave (measured on c4: 4 warps 60.2 us per call, 2 warps
 // 58.3, 1 warp 58.1)).
-static cudaError_t launch_combine_any(const float* part_out, const float* part_lse, long long n_rows, int S,
-                                      float* out, float* lse, const CombineBalanced& bal, cudaStream_t stream) {
+template <typename Out>
+cudaError_t launch_combine_any(const float* part_out, const float* part_lse, long long n_rows, int S, Out* out,
+                               float* lse, const CombineBalanced& bal, cudaStream_t stream) {
     if (n_rows <= 0) return cudaSuccess;
     const int per = bal.on ? 2 * 16 : S;
     if (per <= 16) return launch_combine_z<1>(part_out, part_lse, n_rows, S, out, lse, bal, stream);
@@ -217,8 +216,17 @@ static cudaError_t launch_combine_any(const float* part_out, const float* part_l
     return launch_combine_z<8>(part_out, part_lse, n_rows, S, out, lse, bal, stream);
 }
 
+}  // namespace
+
 cudaError_t launch_combine(const float* part_out, const float* part_lse, long long n_rows, int S,
                            float* out, float* lse, cudaStream_t stream) {
+    CombineBalanced off;
+    memset(&off, 0, sizeof off);
+    return launch_combine_any(part_out, part_lse, n_rows, S, out, lse, off, stream);
+}
+
+cudaError_t launch_combine_bf16(const float* part_out, const float* part_lse, long long n_rows, int S,
+                                __nv_bfloat16* out, float* lse, cudaStream_t stream) {
     CombineBalanced off;
     memset(&off, 0, sizeof off);
     return launch_combine_any(part_out, part_lse, n_rows, S, out, lse, off, stream);

@@ -1,0 +1,156 @@
+// RMS norm of the latent dims and position rotation of the rope dims, for the queries'
+// heads and the new key rows of a step in one launch:
+//     y[d]         = x[d] * w[d] / sqrt(mean_{d<512} x[d]^2 + eps)            (d < 512; w NULL: x[d])
+//     (y_a, y_b)   = (x_a cos - x_b sin, x_b cos + x_a sin), angle = position * inv_freq[i]
+// with the pair (a, b) = 512 + (2i, 2i + 1) or 512 + (i, i + 32), i < 32.  Statistics and
+// products are fp32; each output value is rounded to bf16 once.
+//
+// Angle: a position times a frequency in fp32 is off by position * 2^-25, a sixteenth of a
+// radian at 2^20, and the GPU's few fp64 units would bound the kernel.  So the frequency is
+// held in turns as a 64-bit binary fraction F = inv_freq / (2 pi) * 2^64, made once per
+// block in fp64, and position * F modulo 2^64 is the angle's fraction of a turn: exact
+// integer arithmetic but for F's own rounding (2^-53 relative).
+//
+// Bound by HBM: a row is read once and written once (2 x 1152 B).  One block serves one
+// token: one warp computes the 32 sines and cosines that the token's rows share, then each
+// warp takes rows (heads, and the key row last) with one 16-byte piece of 8 dims a lane and
+// step.
+#include "../../include/mla_verify.h"
+#include "internal.cuh"
+
+#include <math.h>
+
+namespace mla {
+namespace {
+
+constexpr int NR_WARPS = 8;
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__global__ void __launch_bounds__(NR_WARPS * 32)
+    qk_norm_rope_kernel(const __nv_bfloat16* q, const __nv_bfloat16* kv, const __nv_bfloat16* __restrict__ q_weight,
+                        const __nv_bfloat16* __restrict__ kv_weight, const int32_t* __restrict__ positions,
+                        const float* __restrict__ inv_freq, float eps, int interleaved, int H, int rows_per_block,
+                        __nv_bfloat16* q_out, __nv_bfloat16* kv_out) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    __shared__ float s_cos[32], s_sin[32];
+    const int64_t t = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 0) {
+        const double turns = (double)inv_freq[lane] * 0.15915494309189533577;   // 1 / (2 pi)
+        // the fraction of a turn, as a 64-bit binary fraction (whole turns drop out)
+        const long long F = __double2ll_rn((turns - rint(turns)) * 18446744073709551616.0);
+        const long long frac = (long long)((unsigned long long)F * (unsigned long long)(long long)positions[t]);
+        float sn, cs;
+        sincospif((float)(int)(frac >> 32) * 4.656612873077393e-10f, &sn, &cs);  // half turns: 2^-31
+        s_cos[lane] = cs;
+        s_sin[lane] = sn;
+    }
+    __syncthreads();
+    const int n_q = q ? H : 0, rows = n_q + (kv ? 1 : 0);
+    const int r_end = min(rows, (int)(blockIdx.y + 1) * rows_per_block);
+    for (int r = blockIdx.y * rows_per_block + warp; r < r_end; r += NR_WARPS) {
+        const bool is_q = r < n_q;
+        const uint4* src = reinterpret_cast<const uint4*>(is_q ? q + (t * H + r) * D_QK : kv + t * D_QK);
+        uint4* dst = reinterpret_cast<uint4*>(is_q ? q_out + (t * H + r) * D_QK : kv_out + t * D_QK);
+        const uint4* w = reinterpret_cast<const uint4*>(is_q ? q_weight : kv_weight);
+        uint4 a = src[lane], b = src[32 + lane], c = make_uint4(0, 0, 0, 0);
+        if (lane < 8) c = src[64 + lane];
+        if (w) {
+            float fa[8], fb[8], wa[8], wb[8], ss = 0.f;
+            unpack8(a, fa);
+            unpack8(b, fb);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss += fa[i] * fa[i] + fb[i] * fb[i];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            const float inv = rsqrtf(ss * (1.f / D_V) + eps);
+            unpack8(__ldg(w + lane), wa);
+            unpack8(__ldg(w + 32 + lane), wb);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                fa[i] = fa[i] * inv * wa[i];
+                fb[i] = fb[i] * inv * wb[i];
+            }
+            a = pack8(fa);
+            b = pack8(fb);
+        }
+        dst[lane] = a;
+        dst[32 + lane] = b;
+        float x[8], y[8];
+        unpack8(c, x);
+        if (interleaved) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float cs = s_cos[(4 * lane + i) & 31], sn = s_sin[(4 * lane + i) & 31];
+                y[2 * i] = x[2 * i] * cs - x[2 * i + 1] * sn;
+                y[2 * i + 1] = x[2 * i + 1] * cs + x[2 * i] * sn;
+            }
+        } else {
+            // lanes 0-3 hold the pairs' first halves, lanes 4-7 the second
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float other = __shfl_xor_sync(0xffffffffu, x[i], 4);
+                const float cs = s_cos[(8 * lane + i) & 31], sn = s_sin[(8 * lane + i) & 31];
+                y[i] = lane < 4 ? x[i] * cs - other * sn : x[i] * cs + other * sn;
+            }
+        }
+        if (lane < 8) dst[64 + lane] = pack8(y);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_qk_norm_rope(const __nv_bfloat16* q, const __nv_bfloat16* kv, const __nv_bfloat16* q_weight,
+                                const __nv_bfloat16* kv_weight, const int32_t* positions, const float* inv_freq,
+                                float eps, int interleaved, int64_t T, int H, __nv_bfloat16* q_out,
+                                __nv_bfloat16* kv_out, cudaStream_t stream) {
+    const int rows = (q ? H : 0) + (kv ? 1 : 0);
+    const int rows_per_block = rows;
+    const dim3 grid((unsigned)T, (unsigned)((rows + rows_per_block - 1) / rows_per_block));
+    return launch_dependent(qk_norm_rope_kernel, grid, dim3(NR_WARPS * 32), 0, stream, q, kv, q_weight, kv_weight,
+                            positions, inv_freq, eps, interleaved, H, rows_per_block, q_out, kv_out);
+}
+
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" int mla_qk_norm_rope(const void* q, const void* kv, const void* q_weight, const void* kv_weight,
+                                const int32_t* positions, const float* inv_freq, float eps, int interleaved,
+                                int64_t n_tokens, int H, void* q_out, void* kv_out, mla_stream_t stream) {
+    if (n_tokens < 0 || n_tokens > 0x7fffffffLL || H < 1 || H > MLA_MAX_HEADS) return MLA_ERR_SHAPE;
+    if (n_tokens == 0) return MLA_OK;
+    if ((!q && !kv) || (q && !q_out) || (kv && !kv_out) || !positions || !inv_freq) return MLA_ERR_NULL;
+    if (!(eps >= 0.f) || !isfinite(eps)) return MLA_ERR_ARG;
+    if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(q_weight, 16) || !aligned(kv_weight, 16) ||
+        !aligned(q_out, 16) || !aligned(kv_out, 16) || !aligned(positions, 4) || !aligned(inv_freq, 4))
+        return MLA_ERR_ALIGN;
+    int rc = device_state(nullptr, nullptr, nullptr);
+    if (rc != MLA_OK) return rc;
+    using bf = __nv_bfloat16;
+    if (launch_qk_norm_rope(static_cast<const bf*>(q), static_cast<const bf*>(kv), static_cast<const bf*>(q_weight),
+                            static_cast<const bf*>(kv_weight), positions, inv_freq, eps, interleaved ? 1 : 0, n_tokens,
+                            H, static_cast<bf*>(q_out), static_cast<bf*>(kv_out),
+                            reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return MLA_ERR_LAUNCH;
+    return MLA_OK;
+}
