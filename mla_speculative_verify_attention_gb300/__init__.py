@@ -10,6 +10,7 @@ Build it with ``python -m mla_speculative_verify_attention_gb300.build`` (or
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -39,6 +40,7 @@ EXPORTS = ("mla_verify_workspace_bytes", "mla_verify_auto_nsplit", "mla_verify_a
 STATIC_SCRATCH_BYTES = 64 << 20
 
 _lib = None
+_calls = None
 
 
 class MlaError(RuntimeError):
@@ -341,60 +343,86 @@ def verify_combine(part_out: torch.Tensor, part_lse: torch.Tensor, B: int, q_len
     return out, lse
 
 
-class _Launch:
-    """Context of one call of the operators below: every tensor is a contiguous CUDA tensor of
-    one device, that device is the current one inside, and `stream` (default: the device's
-    current stream) is where the call is enqueued and what its own outputs and workspace are
-    allocated for, so that their memory is not handed out again before the call has run."""
-
-    def __init__(self, stream, *tensors):
-        self.device = None
-        for t in tensors:
-            if t is None:
-                continue
-            if not t.is_cuda or not t.is_contiguous():
-                raise ValueError("all tensors must be contiguous CUDA tensors")
-            if self.device is None:
-                self.device = t.device
-            elif t.device != self.device:
-                raise ValueError("all tensors must be on the same device")
-        if stream is not None and stream.device != self.device:
-            raise ValueError("the stream must belong to the tensors' device")
-        self.given = stream
-
-    def __enter__(self):
-        self.guard = None
-        if self.device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-        self.stream = self.given if self.given is not None else torch.cuda.current_stream()
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-    @property
-    def ptr(self):
-        return self.stream.cuda_stream
-
-    def empty(self, shape, dtype):
-        if self.given is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(self.given):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+# The operators below take the small calls of a decode loop, where the binding's own time counts: a
+# check compares a tensor's type and shape with the expected ones as whole objects.
+_SAME_DEVICE = contextlib.nullcontext()
 
 
 def _want(name, t, dtype, shape):
-    """`t` has this dtype and shape (None: any size)."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {str(dtype).replace('torch.', '')}, not {str(t.dtype).replace('torch.', '')}")
-    if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
+    """`t` has this dtype and exactly this shape."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}".replace("torch.", ""))
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, not {list(t.shape)}")
 
 
-def _addr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+def _want_dims(name, t, dtype, dims, last=None):
+    """`t` has this dtype, number of dims and (where given) last dim."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}".replace("torch.", ""))
+    if t.dim() != dims or (last is not None and t.shape[-1] != last):
+        raise ValueError(f"{name} must have {dims} dims" + (f", the last {last}" if last else "") +
+                         f", not shape {list(t.shape)}")
+
+
+def _device_of(*tensors) -> int:
+    """The one CUDA device of these tensors (None: left out), which all have to be contiguous."""
+    dev = -1
+    for t in tensors:
+        if t is None:
+            continue
+        d = t.get_device()
+        if d < 0 or not t.is_contiguous():
+            raise ValueError("all tensors must be contiguous CUDA tensors")
+        if d != dev:
+            if dev >= 0:
+                raise ValueError("all tensors must be on the same device")
+            dev = d
+    return dev
+
+
+def _on(dev: int):
+    """Makes `dev` the current device while a call is enqueued."""
+    return _SAME_DEVICE if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _stream_on(stream, dev: int) -> int:
+    """The stream a call is enqueued on: the given one, else the device's current one."""
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    if stream.device.index != dev:
+        raise ValueError("the stream must belong to the tensors' device")
+    return stream.cuda_stream
+
+
+def _empty(shape, dtype, dev: int, stream):
+    """Memory for a call on `stream`: allocated for that stream, so that it is not handed out
+    again before the call has run."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _addr(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _call(fn: str):
+    """The library's function with its pointers taken as 64-bit integers (0: NULL): a call with
+    twenty arguments then costs half of what ctypes takes to make pointers of them."""
+    global _calls
+    if _calls is None:
+        L, calls = load(), {}
+        for name in ("mla_qk_norm_rope", "mla_kv_append_quant", "mla_kv_read_fp8", "mla_verify_attn_fp8",
+                     "mla_draft_verify"):
+            f = L[name]                                # a function object of its own
+            f.argtypes = [ctypes.c_int64 if a in (ctypes.c_void_p, ctypes.c_size_t) else a
+                          for a in getattr(L, name).argtypes]
+            f.restype = ctypes.c_int
+            calls[name] = f
+        _calls = calls
+    return _calls[fn]
 
 
 def qk_norm_rope(q: Optional[torch.Tensor], kv: Optional[torch.Tensor], positions: torch.Tensor,
@@ -408,37 +436,47 @@ def qk_norm_rope(q: Optional[torch.Tensor], kv: Optional[torch.Tensor], position
     if q is None and kv is None:
         raise ValueError("qk_norm_rope needs q or kv")
     lead = tuple(positions.shape)
-    _want("positions", positions, torch.int32, lead)
+    if positions.dtype is not torch.int32:
+        raise TypeError("positions must be int32")
     _want("inv_freq", inv_freq, torch.float32, (32,))
     H = 1
     if q is not None:
-        _want("q", q, torch.bfloat16, lead + (None, D_QK))
+        _want_dims("q", q, torch.bfloat16, len(lead) + 2, D_QK)
         H = q.shape[-2]
+        _want("q", q, torch.bfloat16, lead + (H, D_QK))
+        if q_out is not None:
+            _want("q_out", q_out, torch.bfloat16, q.shape)
+        if q_weight is not None:
+            _want("q_weight", q_weight, torch.bfloat16, (D_V,))
+    elif q_out is not None or q_weight is not None:
+        raise ValueError("q_out and q_weight go with q")
     if kv is not None:
         _want("kv", kv, torch.bfloat16, lead + (D_QK,))
-    for name, w in (("q_weight", q_weight), ("kv_weight", kv_weight)):
-        if w is not None:
-            _want(name, w, torch.bfloat16, (D_V,))
-    for name, o, x in (("q_out", q_out, q), ("kv_out", kv_out, kv)):
-        if o is not None:
-            if x is None:
-                raise ValueError(f"{name} without its input")
-            _want(name, o, torch.bfloat16, tuple(x.shape))
-    with _Launch(stream, q, kv, positions, inv_freq, q_weight, kv_weight, q_out, kv_out) as at:
+        if kv_out is not None:
+            _want("kv_out", kv_out, torch.bfloat16, kv.shape)
+        if kv_weight is not None:
+            _want("kv_weight", kv_weight, torch.bfloat16, (D_V,))
+    elif kv_out is not None or kv_weight is not None:
+        raise ValueError("kv_out and kv_weight go with kv")
+    dev = _device_of(q, kv, positions, inv_freq, q_weight, kv_weight, q_out, kv_out)
+    with _on(dev):
+        at = _stream_on(stream, dev)
         if q is not None and q_out is None:
-            q_out = at.empty(q.shape, torch.bfloat16)
+            q_out = _empty(q.shape, torch.bfloat16, dev, stream)
         if kv is not None and kv_out is None:
-            kv_out = at.empty(kv.shape, torch.bfloat16)
-        _check("mla_qk_norm_rope", load().mla_qk_norm_rope(
+            kv_out = _empty(kv.shape, torch.bfloat16, dev, stream)
+        _check("mla_qk_norm_rope", _call("mla_qk_norm_rope")(
             _addr(q), _addr(kv), _addr(q_weight), _addr(kv_weight), positions.data_ptr(), inv_freq.data_ptr(),
-            float(eps), 1 if interleaved else 0, positions.numel(), H, _addr(q_out), _addr(kv_out), at.ptr))
+            eps, 1 if interleaved else 0, positions.numel(), H, _addr(q_out), _addr(kv_out), at))
     return q_out, kv_out
 
 
-def _want_fp8_cache(kv_lat, kv_scale, kv_rope):
-    _want("kv_lat", kv_lat, torch.uint8, (None, D_V))
-    _want("kv_scale", kv_scale, torch.float32, (kv_lat.shape[0],))
-    _want("kv_rope", kv_rope, torch.bfloat16, (kv_lat.shape[0], D_QK - D_V))
+def _want_fp8_cache(kv_lat, kv_scale, kv_rope) -> int:
+    n_pool = kv_lat.shape[0] if kv_lat.dim() else 0
+    _want("kv_lat", kv_lat, torch.uint8, (n_pool, D_V))
+    _want("kv_scale", kv_scale, torch.float32, (n_pool,))
+    _want("kv_rope", kv_rope, torch.bfloat16, (n_pool, D_QK - D_V))
+    return n_pool
 
 
 def kv_append_quant(kv_lat: torch.Tensor, kv_scale: torch.Tensor, kv_rope: torch.Tensor, slots: torch.Tensor,
@@ -446,28 +484,32 @@ def kv_append_quant(kv_lat: torch.Tensor, kv_scale: torch.Tensor, kv_rope: torch
     """mla_kv_append_quant: quantises rows [n, 576] (bf16) into the fp8 cache (kv_lat uint8
     [n_pool, 512], kv_scale fp32 [n_pool], kv_rope bf16 [n_pool, 64]) at pool rows slots [n]
     (int32, distinct)."""
-    _want_fp8_cache(kv_lat, kv_scale, kv_rope)
-    _want("slots", slots, torch.int32, (None,))
-    _want("rows", rows, torch.bfloat16, (slots.shape[0], D_QK))
-    with _Launch(stream, kv_lat, kv_scale, kv_rope, slots, rows) as at:
-        _check("mla_kv_append_quant", load().mla_kv_append_quant(
-            kv_lat.data_ptr(), kv_scale.data_ptr(), kv_rope.data_ptr(), kv_lat.shape[0], slots.data_ptr(),
-            rows.data_ptr(), slots.shape[0], at.ptr))
+    n_pool = _want_fp8_cache(kv_lat, kv_scale, kv_rope)
+    _want_dims("slots", slots, torch.int32, 1)
+    n = slots.shape[0]
+    _want("rows", rows, torch.bfloat16, (n, D_QK))
+    dev = _device_of(kv_lat, kv_scale, kv_rope, slots, rows)
+    with _on(dev):
+        _check("mla_kv_append_quant", _call("mla_kv_append_quant")(
+            kv_lat.data_ptr(), kv_scale.data_ptr(), kv_rope.data_ptr(), n_pool, slots.data_ptr(), rows.data_ptr(), n,
+            _stream_on(stream, dev)))
 
 
 def kv_read_fp8(kv_lat: torch.Tensor, kv_scale: torch.Tensor, kv_rope: torch.Tensor, slots: torch.Tensor, *,
                 out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """mla_kv_read_fp8: the cached rows slots [n] as bf16 [n, 576], bf16(scale * code) | rope."""
-    _want_fp8_cache(kv_lat, kv_scale, kv_rope)
-    _want("slots", slots, torch.int32, (None,))
+    n_pool = _want_fp8_cache(kv_lat, kv_scale, kv_rope)
+    _want_dims("slots", slots, torch.int32, 1)
+    n = slots.shape[0]
     if out is not None:
-        _want("out", out, torch.bfloat16, (slots.shape[0], D_QK))
-    with _Launch(stream, kv_lat, kv_scale, kv_rope, slots, out) as at:
+        _want("out", out, torch.bfloat16, (n, D_QK))
+    dev = _device_of(kv_lat, kv_scale, kv_rope, slots, out)
+    with _on(dev):
+        at = _stream_on(stream, dev)
         if out is None:
-            out = at.empty((slots.shape[0], D_QK), torch.bfloat16)
-        _check("mla_kv_read_fp8", load().mla_kv_read_fp8(
-            kv_lat.data_ptr(), kv_scale.data_ptr(), kv_rope.data_ptr(), kv_lat.shape[0], slots.data_ptr(),
-            out.data_ptr(), slots.shape[0], at.ptr))
+            out = _empty((n, D_QK), torch.bfloat16, dev, stream)
+        _check("mla_kv_read_fp8", _call("mla_kv_read_fp8")(
+            kv_lat.data_ptr(), kv_scale.data_ptr(), kv_rope.data_ptr(), n_pool, slots.data_ptr(), out.data_ptr(), n, at))
     return out
 
 
@@ -479,14 +521,16 @@ def verify_attn_fp8(q: torch.Tensor, kv_lat: torch.Tensor, kv_scale: torch.Tenso
     """mla_verify_attn_fp8: verify_attn over the fp8 cache of kv_append_quant; out bf16
     [B, q_len, H, 512] and lse fp32 [B, q_len, H].  ``draft_mask`` is uint8 [B, q_len, q_len],
     bit-packed int64 [B, q_len], or None (causal chain); ``workspace`` as for verify_attn."""
-    _want("q", q, torch.bfloat16, (None, None, None, D_QK))
+    _want_dims("q", q, torch.bfloat16, 4, D_QK)
     B, q_len, H, _ = q.shape
-    _want_fp8_cache(kv_lat, kv_scale, kv_rope)
-    _want("slot_table", slot_table, torch.int32, (B, None))
+    n_pool = _want_fp8_cache(kv_lat, kv_scale, kv_rope)
+    _want_dims("slot_table", slot_table, torch.int32, 2)
+    stride = slot_table.shape[1]
+    _want("slot_table", slot_table, torch.int32, (B, stride))
     _want("seq_lens", seq_lens, torch.int32, (B,))
-    mask = bits = None
+    mask = bits = 0
     if draft_mask is not None:
-        if draft_mask.dtype == torch.int64:
+        if draft_mask.dtype is torch.int64:
             _want("draft_mask", draft_mask, torch.int64, (B, q_len))
             bits = draft_mask.data_ptr()
         else:
@@ -497,19 +541,21 @@ def verify_attn_fp8(q: torch.Tensor, kv_lat: torch.Tensor, kv_scale: torch.Tenso
     if lse is not None:
         _want("lse", lse, torch.float32, (B, q_len, H))
     if workspace is not None:
-        _want("workspace", workspace, torch.uint8, (None,))
-    with _Launch(stream, q, kv_lat, kv_scale, kv_rope, slot_table, seq_lens, draft_mask, out, lse, workspace) as at:
+        _want_dims("workspace", workspace, torch.uint8, 1)
+    dev = _device_of(q, kv_lat, kv_scale, kv_rope, slot_table, seq_lens, draft_mask, out, lse, workspace)
+    with _on(dev):
+        at = _stream_on(stream, dev)
         if out is None:
-            out = at.empty((B, q_len, H, D_V), torch.bfloat16)
+            out = _empty((B, q_len, H, D_V), torch.bfloat16, dev, stream)
         if lse is None:
-            lse = at.empty((B, q_len, H), torch.float32)
+            lse = _empty((B, q_len, H), torch.float32, dev, stream)
         if workspace is None:
-            ns = nsplit if nsplit > 0 else auto_nsplit(B, q_len, H, slot_table.shape[1], num_sms(q.device), 1 << 62)
-            workspace = at.empty(max(workspace_bytes(B, q_len, H, ns), 256), torch.uint8)
-        _check("mla_verify_attn_fp8", load().mla_verify_attn_fp8(
-            q.data_ptr(), kv_lat.data_ptr(), kv_scale.data_ptr(), kv_rope.data_ptr(), kv_lat.shape[0],
-            slot_table.data_ptr(), slot_table.shape[1], seq_lens.data_ptr(), mask, bits, B, q_len, H, float(scale),
-            out.data_ptr(), lse.data_ptr(), nsplit, workspace.data_ptr(), workspace.numel(), at.ptr))
+            ns = nsplit if nsplit > 0 else auto_nsplit(B, q_len, H, stride, num_sms(dev), 1 << 62)
+            workspace = _empty((max(workspace_bytes(B, q_len, H, ns), 256),), torch.uint8, dev, stream)
+        _check("mla_verify_attn_fp8", _call("mla_verify_attn_fp8")(
+            q.data_ptr(), kv_lat.data_ptr(), kv_scale.data_ptr(), kv_rope.data_ptr(), n_pool, slot_table.data_ptr(),
+            stride, seq_lens.data_ptr(), mask, bits, B, q_len, H, scale, out.data_ptr(), lse.data_ptr(), nsplit,
+            workspace.data_ptr(), workspace.numel(), at))
     return out, lse
 
 
@@ -523,29 +569,35 @@ def draft_verify(target_probs: torch.Tensor, draft_probs: Optional[torch.Tensor]
     draft_tokens and parents int32 [B, q_len], u_accept fp32 [B, q_len], u_next fp32 [B].
     Returns (n_accepted [B], tokens [B, q_len], path [B, q_len]), int32: the accepted drafts'
     tokens followed by the next token, and the accepted drafts' nodes, padded with -1."""
-    _want("target_probs", target_probs, torch.float32, (None, None, None))
+    _want_dims("target_probs", target_probs, torch.float32, 3)
     B, q_len, vocab = target_probs.shape
+    nodes = (B, q_len)
     if draft_probs is not None:
         _want("draft_probs", draft_probs, torch.float32, (B, q_len, vocab))
-    _want("draft_tokens", draft_tokens, torch.int32, (B, q_len))
+    _want("draft_tokens", draft_tokens, torch.int32, nodes)
     if parents is not None:
-        _want("parents", parents, torch.int32, (B, q_len))
-    _want("u_accept", u_accept, torch.float32, (B, q_len))
+        _want("parents", parents, torch.int32, nodes)
+    _want("u_accept", u_accept, torch.float32, nodes)
     _want("u_next", u_next, torch.float32, (B,))
     if n_accepted is not None:
         _want("n_accepted", n_accepted, torch.int32, (B,))
-    for name, t in (("tokens", tokens), ("path", path)):
-        if t is not None:
-            _want(name, t, torch.int32, (B, q_len))
-    with _Launch(stream, target_probs, draft_probs, draft_tokens, parents, u_accept, u_next, n_accepted, tokens,
-                 path) as at:
-        n_accepted = at.empty((B,), torch.int32) if n_accepted is None else n_accepted
-        tokens = at.empty((B, q_len), torch.int32) if tokens is None else tokens
-        path = at.empty((B, q_len), torch.int32) if path is None else path
-        _check("mla_draft_verify", load().mla_draft_verify(
+    if tokens is not None:
+        _want("tokens", tokens, torch.int32, nodes)
+    if path is not None:
+        _want("path", path, torch.int32, nodes)
+    dev = _device_of(target_probs, draft_probs, draft_tokens, parents, u_accept, u_next, n_accepted, tokens, path)
+    with _on(dev):
+        at = _stream_on(stream, dev)
+        if n_accepted is None:
+            n_accepted = _empty((B,), torch.int32, dev, stream)
+        if tokens is None:
+            tokens = _empty(nodes, torch.int32, dev, stream)
+        if path is None:
+            path = _empty(nodes, torch.int32, dev, stream)
+        _check("mla_draft_verify", _call("mla_draft_verify")(
             target_probs.data_ptr(), _addr(draft_probs), draft_tokens.data_ptr(), _addr(parents),
             u_accept.data_ptr(), u_next.data_ptr(), B, q_len, vocab, n_accepted.data_ptr(), tokens.data_ptr(),
-            path.data_ptr(), at.ptr))
+            path.data_ptr(), at))
     return n_accepted, tokens, path
 
 

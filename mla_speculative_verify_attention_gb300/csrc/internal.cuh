@@ -68,7 +68,8 @@ __host__ __device__ inline void split_range(int n, int S, int s, int tile, int* 
 
 // Balanced key split of one launch over B <= 64 streams of unequal length, decided on
 // the device (the host does not know the lengths): with T the sum of the valid lengths,
-// the keys are cut into chunks of chunk = max(128, ceil(T / G) rounded up to 32) keys;
+// the keys are cut into chunks of chunk = max(128, ceil(T / G) rounded up to `unit`, the
+// keys of a tile) keys;
 // stream b gets ns_b = ceil(n_b / chunk) consecutive split slots (one for a stream whose
 // length is invalid, which then writes NaN), slots numbered stream after stream, at
 // most G + B of them.  Every warp evaluates it alike (lane i holds streams i and
@@ -80,7 +81,8 @@ struct BalancedPlan {
     int incl[2];    // inclusive prefix sums of the slot counts at those streams
 };
 
-__device__ inline BalancedPlan balanced_plan(const int32_t* seq_lens, int B, int q_len, int slot_stride, int G) {
+__device__ inline BalancedPlan balanced_plan(const int32_t* seq_lens, int B, int q_len, int slot_stride, int G,
+                                             int unit = 32) {
     const int lane = threadIdx.x & 31;
     BalancedPlan P;
     int* n = P.n;
@@ -97,7 +99,7 @@ __device__ inline BalancedPlan balanced_plan(const int32_t* seq_lens, int B, int
     for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     // 32-bit divisions whenever the total fits (warp-uniform branch)
     long long c = t < (1ll << 30) ? (long long)(((unsigned)t + (unsigned)G - 1u) / (unsigned)G) : (t + G - 1) / G;
-    c = (c + 31) / 32 * 32;
+    c = (c + unit - 1) / unit * unit;
     if (c < 128) c = 128;
     if (c > (1 << 30)) c = 1 << 30;
     P.chunk = (int)c;
@@ -149,7 +151,7 @@ constexpr int BALANCED_MAX_STREAMS = 64;
 
 // Status word's device address and SM count of the current device (MLA_OK or
 // MLA_ERR_DEVICE: no sm_103 device, or a CUDA runtime error); any output may be null.
-int device_state(int* dev_out, unsigned** status, int* num_sms);
+int device_state(int* dev_out, unsigned** status, int* num_sms, unsigned long long** rescales = nullptr);
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -194,5 +196,7 @@ cudaError_t launch_combine_bf16(const float* part_out, const float* part_lse, lo
                                 __nv_bfloat16* out, float* lse, cudaStream_t stream);
 // Combine of a balanced split (slot-major partials of VerifyArgs::balanced).
 cudaError_t launch_combine_balanced(const VerifyArgs& a, cudaStream_t stream);
+// The same with a bf16 output and chunks of whole tiles of `unit` keys.
+cudaError_t launch_combine_balanced_bf16(const VerifyArgs& a, __nv_bfloat16* out, int unit, cudaStream_t stream);
 
 }  // namespace mla

@@ -33,7 +33,7 @@ int g_arch_ok[MAX_DEVICES];      // 0 unknown, 1 sm_103, -1 other
 }  // namespace
 
 // Device properties and the status word's device address for the current device.
-int device_state(int* dev_out, unsigned** status, int* num_sms) {
+int device_state(int* dev_out, unsigned** status, int* num_sms, unsigned long long** rescales) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return MLA_ERR_DEVICE;
     if (g_arch_ok[dev] == 0) {
@@ -54,6 +54,7 @@ int device_state(int* dev_out, unsigned** status, int* num_sms) {
     if (dev_out) *dev_out = dev;
     if (status) *status = g_status_ptr[dev];
     if (num_sms) *num_sms = g_num_sms[dev];
+    if (rescales) *rescales = g_rescales_ptr[dev];
     return MLA_OK;
 }
 
@@ -83,7 +84,7 @@ constexpr int CB_BATCH = 8;
 struct CombineBalanced {
     int on;
     const int32_t* seq_lens;
-    int B, q_len, slot_stride, G, rows;
+    int B, q_len, slot_stride, G, rows, unit;
 };
 
 // The merged sums are fp32; a bf16 output rounds each of them once.
@@ -111,7 +112,8 @@ __global__ void __launch_bounds__(CB_THREADS) combine_kernel(const float* __rest
     const float* pl = part_lse + row * S_all;
     long long po = row * (long long)S_all * D_V;
     if (bal.on) {
-        const BalancedPlan P = balanced_plan(bal.seq_lens, bal.B, bal.q_len, bal.slot_stride, bal.G);
+        const BalancedPlan P = balanced_plan(bal.seq_lens, bal.B, bal.q_len, bal.slot_stride, bal.G,
+                                             bal.unit);
         const int b = (int)(row / bal.rows), r = (int)(row % bal.rows);
         int first, count;
         balanced_stream(P, b, &first, &count);
@@ -233,14 +235,25 @@ cudaError_t launch_combine_bf16(const float* part_out, const float* part_lse, lo
 }
 
 // S here bounds the slots of one stream (nsplit slots in all): the weights' shared memory.
-cudaError_t launch_combine_balanced(const VerifyArgs& a, cudaStream_t stream) {
+namespace {
+template <typename Out>
+cudaError_t combine_balanced(const VerifyArgs& a, Out* out, int unit, cudaStream_t stream) {
     CombineBalanced bal;
     bal.on = 1;
     bal.seq_lens = a.seq_lens;
     bal.B = a.B; bal.q_len = a.q_len; bal.slot_stride = a.slot_stride; bal.G = a.bal_G;
     bal.rows = a.q_len * a.H;
-    return launch_combine_any(a.part_out, a.part_lse, (long long)a.B * bal.rows, a.nsplit, a.out, a.lse, bal,
-                              stream);
+    bal.unit = unit;
+    return launch_combine_any(a.part_out, a.part_lse, (long long)a.B * bal.rows, a.nsplit, out, a.lse, bal, stream);
+}
+}  // namespace
+
+cudaError_t launch_combine_balanced(const VerifyArgs& a, cudaStream_t stream) {
+    return combine_balanced(a, a.out, 32, stream);
+}
+
+cudaError_t launch_combine_balanced_bf16(const VerifyArgs& a, __nv_bfloat16* out, int unit, cudaStream_t stream) {
+    return combine_balanced(a, out, unit, stream);
 }
 
 }  // namespace mla
