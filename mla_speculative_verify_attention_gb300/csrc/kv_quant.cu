@@ -29,28 +29,46 @@ __device__ __forceinline__ void row8(const uint4& v, float (&f)[8]) {
     }
 }
 
-__device__ __forceinline__ float finite_max8(const float (&f)[8], float m) {
+// max |f|, NaN left out; with `finite`, infinities too.
+__device__ __forceinline__ float max_abs8(const float (&f)[8], float m, bool finite) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float a = fabsf(f[i]);
-        if (a <= 3.4028234663852886e38f) m = fmaxf(m, a);       // neither infinite nor NaN
+        m = fmaxf(m, finite && a == INFINITY ? 0.f : a);
     }
     return m;
 }
 
-__device__ __forceinline__ uint2 encode8(const float (&f)[8], float scale) {
+__device__ __forceinline__ float warp_max(float m) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+}
+
+// x / scale, correctly rounded: with inv = 1 / scale correctly rounded, each step
+// q + (x - q scale) inv brings a quotient that is a few units off to within one, and one that is
+// within a unit to the correctly rounded one (Markstein 1990).  Needs a scale well inside
+// the normal range; five operations where the general division takes a dozen.
+__device__ __forceinline__ float divide(float x, float scale, float inv) {
+    float q = __fmul_rn(x, inv);
+    q = fmaf(fmaf(-q, scale, x), inv, q);
+    return fmaf(fmaf(-q, scale, x), inv, q);
+}
+
+__device__ __forceinline__ uint2 encode8(const float (&f)[8], float scale, float inv, bool finite) {
+    float r[8];
+    if (finite && scale > 8.6736174e-19f && scale < 1.1529215e18f) {       // 2^-60, 2^60
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = divide(f[i], scale, inv);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = scale > 0.f ? __fdiv_rn(f[i], scale) : f[i];
+    }
     uint32_t w[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint32_t o = 0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float x0 = f[4 * h + 2 * i], x1 = f[4 * h + 2 * i + 1];
-            const float2 r = scale > 0.f ? make_float2(__fdiv_rn(x0, scale), __fdiv_rn(x1, scale)) : make_float2(x0, x1);
-            o |= (uint32_t)__nv_cvt_float2_to_fp8x2(r, __NV_SATFINITE, __NV_E4M3) << (16 * i);
-        }
-        w[h] = o;
-    }
+    for (int h = 0; h < 2; ++h)
+        w[h] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(r[4 * h], r[4 * h + 1]), __NV_SATFINITE, __NV_E4M3) |
+               (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(r[4 * h + 2], r[4 * h + 3]), __NV_SATFINITE, __NV_E4M3) << 16;
     return make_uint2(w[0], w[1]);
 }
 
@@ -74,13 +92,14 @@ __global__ void __launch_bounds__(KQ_THREADS)
     row8(__ldg(src + 32 + lane), b);
     uint4 rope = make_uint4(0, 0, 0, 0);
     if (lane < 8) rope = __ldg(src + 64 + lane);
-    float m = finite_max8(b, finite_max8(a, 0.f));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float m = warp_max(max_abs8(b, max_abs8(a, 0.f, false), false));
+    const bool finite = m < INFINITY;                  // (of what is not NaN)
+    if (!finite) m = warp_max(max_abs8(b, max_abs8(a, 0.f, true), true));
     const float scale = __fdiv_rn(m, E4M3_MAX);
     uint2* lat = reinterpret_cast<uint2*>(kv_lat + (int64_t)s * D_V);
-    lat[lane] = encode8(a, scale);
-    lat[32 + lane] = encode8(b, scale);
+    const float inv = __frcp_rn(scale);
+    lat[lane] = encode8(a, scale, inv, finite);
+    lat[32 + lane] = encode8(b, scale, inv, finite);
     if (lane < 8) reinterpret_cast<uint4*>(kv_rope + (int64_t)s * 64)[lane] = rope;
     if (lane == 0) kv_scale[s] = scale;
 }

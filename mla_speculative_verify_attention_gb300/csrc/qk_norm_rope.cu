@@ -11,10 +11,10 @@
 // block in fp64, and position * F modulo 2^64 is the angle's fraction of a turn: exact
 // integer arithmetic but for F's own rounding (2^-53 relative).
 //
-// Bound by HBM: a row is read once and written once (2 x 1152 B).  One block serves one
-// token: one warp computes the 32 sines and cosines that the token's rows share, then each
-// warp takes rows (heads, and the key row last) with one 16-byte piece of 8 dims a lane and
-// step.
+// Bound by HBM: a row is read once and written once (2 x 1152 B).  A block serves up to 16 rows
+// of one token (heads, and the key row last): its warps issue the loads of up to four rows
+// each, one warp computes the 32 sines and cosines that the rows share while they are on their
+// way, and each lane then handles one 16-byte piece of 8 dims a step.
 #include "../../include/mla_verify.h"
 #include "internal.cuh"
 
@@ -23,7 +23,8 @@
 namespace mla {
 namespace {
 
-constexpr int NR_WARPS = 8;
+constexpr int NR_WARPS = 4;
+constexpr int NR_ROWS = 4;       // rows a warp has in flight
 
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -54,6 +55,19 @@ __global__ void __launch_bounds__(NR_WARPS * 32)
     __shared__ float s_cos[32], s_sin[32];
     const int64_t t = blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n_q = q ? H : 0, rows = n_q + (kv ? 1 : 0);
+    const int r0 = blockIdx.y * rows_per_block + warp, r_end = min(rows, (int)(blockIdx.y + 1) * rows_per_block);
+    // all of the warp's rows are under way before the angles are made
+    uint4 v[NR_ROWS][3];
+#pragma unroll
+    for (int u = 0; u < NR_ROWS; ++u) {
+        const int r = r0 + u * NR_WARPS;
+        if (r >= r_end) break;
+        const uint4* src = reinterpret_cast<const uint4*>(r < n_q ? q + (t * H + r) * D_QK : kv + t * D_QK);
+        v[u][0] = src[lane];
+        v[u][1] = src[32 + lane];
+        v[u][2] = lane < 8 ? src[64 + lane] : make_uint4(0, 0, 0, 0);
+    }
     if (warp == 0) {
         const double turns = (double)inv_freq[lane] * 0.15915494309189533577;   // 1 / (2 pi)
         // the fraction of a turn, as a 64-bit binary fraction (whole turns drop out)
@@ -65,38 +79,35 @@ __global__ void __launch_bounds__(NR_WARPS * 32)
         s_sin[lane] = sn;
     }
     __syncthreads();
-    const int n_q = q ? H : 0, rows = n_q + (kv ? 1 : 0);
-    const int r_end = min(rows, (int)(blockIdx.y + 1) * rows_per_block);
-    for (int r = blockIdx.y * rows_per_block + warp; r < r_end; r += NR_WARPS) {
+#pragma unroll
+    for (int u = 0; u < NR_ROWS; ++u) {
+        const int r = r0 + u * NR_WARPS;
+        if (r >= r_end) break;
         const bool is_q = r < n_q;
-        const uint4* src = reinterpret_cast<const uint4*>(is_q ? q + (t * H + r) * D_QK : kv + t * D_QK);
         uint4* dst = reinterpret_cast<uint4*>(is_q ? q_out + (t * H + r) * D_QK : kv_out + t * D_QK);
         const uint4* w = reinterpret_cast<const uint4*>(is_q ? q_weight : kv_weight);
-        uint4 a = src[lane], b = src[32 + lane], c = make_uint4(0, 0, 0, 0);
-        if (lane < 8) c = src[64 + lane];
         if (w) {
-            float fa[8], fb[8], wa[8], wb[8], ss = 0.f;
-            unpack8(a, fa);
-            unpack8(b, fb);
+            float fa[8], fb[8], wt[8], ss = 0.f;
+            unpack8(v[u][0], fa);
+            unpack8(v[u][1], fb);
 #pragma unroll
             for (int i = 0; i < 8; ++i) ss += fa[i] * fa[i] + fb[i] * fb[i];
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
             const float inv = rsqrtf(ss * (1.f / D_V) + eps);
-            unpack8(__ldg(w + lane), wa);
-            unpack8(__ldg(w + 32 + lane), wb);
+            unpack8(__ldg(w + lane), wt);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                fa[i] = fa[i] * inv * wa[i];
-                fb[i] = fb[i] * inv * wb[i];
-            }
-            a = pack8(fa);
-            b = pack8(fb);
+            for (int i = 0; i < 8; ++i) fa[i] = fa[i] * inv * wt[i];
+            unpack8(__ldg(w + 32 + lane), wt);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) fb[i] = fb[i] * inv * wt[i];
+            v[u][0] = pack8(fa);
+            v[u][1] = pack8(fb);
         }
-        dst[lane] = a;
-        dst[32 + lane] = b;
+        dst[lane] = v[u][0];
+        dst[32 + lane] = v[u][1];
         float x[8], y[8];
-        unpack8(c, x);
+        unpack8(v[u][2], x);
         if (interleaved) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -124,8 +135,9 @@ cudaError_t launch_qk_norm_rope(const __nv_bfloat16* q, const __nv_bfloat16* kv,
                                 float eps, int interleaved, int64_t T, int H, __nv_bfloat16* q_out,
                                 __nv_bfloat16* kv_out, cudaStream_t stream) {
     const int rows = (q ? H : 0) + (kv ? 1 : 0);
-    const int rows_per_block = rows;
-    const dim3 grid((unsigned)T, (unsigned)((rows + rows_per_block - 1) / rows_per_block));
+    const int blocks = (rows + NR_WARPS * NR_ROWS - 1) / (NR_WARPS * NR_ROWS);
+    const int rows_per_block = (rows + blocks - 1) / blocks;
+    const dim3 grid((unsigned)T, (unsigned)blocks);
     return launch_dependent(qk_norm_rope_kernel, grid, dim3(NR_WARPS * 32), 0, stream, q, kv, q_weight, kv_weight,
                             positions, inv_freq, eps, interleaved, H, rows_per_block, q_out, kv_out);
 }

@@ -103,6 +103,13 @@ __device__ __forceinline__ void cp_async_wait_pending(int n) {
         default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
     }
 }
+// 16 bytes that are read once: not kept in L1.
+__device__ __forceinline__ uint4 ld_stream(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
 // Arrive on `bar` once all cp.async issued so far by this thread have landed; the arrival
 // counts toward the barrier's expected count (no increment first).
 __device__ __forceinline__ void cp_async_arrive_noinc(uint64_t* bar) {

@@ -48,14 +48,15 @@ namespace {
 
 using namespace tc;
 
-constexpr int NK = 64;                               // keys per tile
-constexpr int MAX_R = 80;                            // query rows per CTA
+constexpr int NK = 48;                               // keys per tile
+constexpr int MAX_R = 72;                            // query rows per CTA
 constexpr int NT = 512;
 constexpr int WIDE_WARPS = 8;
-constexpr int STAGES = 2;
+constexpr int WK = NK / WIDE_WARPS;                  // keys of a tile per gather warp
+constexpr int STAGES = 3;
 constexpr int NCHUNK = D_QK / 64;                    // 8 latent chunks and the rope chunk
 constexpr int REGION = NK * 128;                     // one 64-dim chunk of a stage
-constexpr int STAGE_BYTES = NCHUNK * REGION;         // 73728 B
+constexpr int STAGE_BYTES = NCHUNK * REGION;         // 55296 B
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int A_COL = 0, C_COL = NK, O_COL = 2 * NK; // TMEM columns: A, C, O^T (4 R), Q chunks
 constexpr float TAU = 8.0f;                          // lazy rescale threshold (log2 units)
@@ -73,9 +74,11 @@ static_assert(B_COUNT * 8 <= BAR_BYTES, "barrier area");
 struct Layout {
     int kv, p, misc, total;                          // the Q chunks start at 0
 };
-__host__ __device__ inline Layout layout_for(int R, int nq_s) {
+// RQ: rows of a Q chunk (whole groups of eight).  The MMA reads 128 rows a chunk: what lies
+// behind the last, in the next chunk or the key stages, gives scores that nobody uses.
+__host__ __device__ inline Layout layout_for(int R, int RQ, int nq_s) {
     Layout L;
-    L.kv = (nq_s * R * 128 + 1023) / 1024 * 1024;
+    L.kv = (nq_s * RQ * 128 + 1023) / 1024 * 1024;
     L.p = L.kv + STAGES * STAGE_BYTES;
     L.misc = (L.p + R * NK * 2 + 127) / 128 * 128;
     L.total = L.misc + BAR_BYTES + 128 + STAGES * NK * 12 + 512 + 512;
@@ -101,7 +104,7 @@ struct Fp8Args {
     float* part_lse;
     int nsplit;
     int balanced, bal_G;
-    int R, R_step;
+    int R, RQ, R_step;            // MMA rows (of 16), Q rows in shared memory (of 8), rows per tile
     int debug_stall;
     unsigned* status;
     unsigned long long* rescales;
@@ -112,7 +115,7 @@ struct Misc {
     uint32_t* tmem_slot;
     volatile int* abort;
     float2* key_sl;               // [STAGES][NK]: scale (NaN: the key holds a NaN), log2 of the clamped scale
-    float* key_inv;               // [STAGES][NK]: 1 / clamped scale
+    float* key_inv;               // [STAGES][NK]: 1 / clamped scale (finite: a masked key's P of 0 stays 0)
     float* row_f;                 // [128]: alpha while the loop runs, 1 / l in the epilogue
     float* row_exp;               // [128]: the power of two that a query row was divided by
 };
@@ -169,8 +172,8 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
     constexpr int NQS = NCHUNK - NQT;
     extern __shared__ __align__(1024) uint8_t smem[];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int R = a.R;
-    const Layout L = layout_for(R, NQS);
+    const int R = a.R, RQ = a.RQ;
+    const Layout L = layout_for(R, RQ, NQS);
     const Misc M = misc_at(smem, L.misc);
     const uint32_t q_addr = smem_u32(smem), kv_addr = smem_u32(smem + L.kv), p_addr = smem_u32(smem + L.p);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -231,7 +234,7 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
         if (T > 0) {
             const uint32_t id_a = idesc_f16(128, NK, false, false), id_c = idesc_bf16(128, NK, false, false);
             const uint64_t dq = smem_desc_sw128(q_addr, 16, 1024), dk = smem_desc_sw128(kv_addr, 16, 1024);
-            const uint32_t q_region16 = (uint32_t)(R * 128) >> 4;
+            const uint32_t q_region16 = (uint32_t)(RQ * 128) >> 4;
             bool ok = __all_sync(0xffffffffu, mbar_wait(&M.bars[B_Q_FULL], 0, M.abort));
             fence_proxy_async_smem();
             for (int i = 0; i < T && ok; ++i) {
@@ -290,21 +293,21 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
         __syncwarp();
         }
     } else if (warp >= 8) {
-        // ================= gather and widening: keys 8w .. 8w+7 of every tile =================
+        // ================= gather and widening: keys WK w .. WK w + 5 of every tile =================
         asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
         const int w = warp - 8;
         bool bad_slot = false;
         const int32_t* slot_row = a.slot + (int64_t)b * a.slot_stride;
-        // lane l holds the slot of key 8 w + (l & 7) of tile t0 + (l >> 3), for the current group of
+        // lane l holds the slot of key WK w + (l & 7) of tile t0 + (l >> 3), for the current group of
         // four tiles and the next; indices are checked when their group becomes current
         auto load_slots = [&](int t0) -> int {
             const int t = t0 + (lane >> 3);
             if (t >= T) return 0;
-            return __ldg(slot_row + min(k_begin + t * NK + 8 * w + (lane & 7), k_end - 1));  // past the split: a valid key
+            return __ldg(slot_row + min(k_begin + t * NK + WK * w + min(lane & 7, WK - 1), k_end - 1));   // past the split: a valid key
         };
         int cur = load_slots(0), nxt = load_slots(4);
         struct Raw {
-            uint4 lat[8], rope[2];
+            uint4 lat[WK], rope[2];
             float scale;
         };
         auto load_tile = [&](Raw& r, int j) {
@@ -316,14 +319,14 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
                 }
                 if (cur < 0 || (int64_t)cur >= a.n_pool) { bad_slot = true; cur = 0; }
             }
-            const int sl = __shfl_sync(0xffffffffu, cur, ((j & 3) << 3) + (lane & 7));   // key 8 w + (lane & 7)
+            const int sl = __shfl_sync(0xffffffffu, cur, ((j & 3) << 3) + (lane & 7));   // key WK w + (lane & 7)
 #pragma unroll
-            for (int it = 0; it < 8; ++it)
-                r.lat[it] = __ldg(reinterpret_cast<const uint4*>(a.lat + (int64_t)__shfl_sync(0xffffffffu, sl, it) * D_V) + lane);
+            for (int it = 0; it < WK; ++it)
+                r.lat[it] = ld_stream(reinterpret_cast<const uint4*>(a.lat + (int64_t)__shfl_sync(0xffffffffu, sl, it) * D_V) + lane);
 #pragma unroll
             for (int it = 0; it < 2; ++it) {
-                const int f = it * 32 + lane;
-                r.rope[it] = __ldg(reinterpret_cast<const uint4*>(a.rope + (int64_t)__shfl_sync(0xffffffffu, sl, f >> 3) * 64) + (f & 7));
+                const int f = it * 32 + lane, rs = __shfl_sync(0xffffffffu, sl, f >> 3);
+                if (f < 8 * WK) r.rope[it] = ld_stream(reinterpret_cast<const uint4*>(a.rope + (int64_t)rs * 64) + (f & 7));
             }
             r.scale = __ldg(a.kscale + sl);
         };
@@ -332,15 +335,17 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
         const int region = lane >> 2, j0 = (lane & 3) * 2, odd = region & 1;
         auto widen_tile = [&](const Raw& r, int i) -> bool {
             const int st = i % STAGES;
-            if (i >= STAGES && !mbar_wait(&M.bars[B_KV_EMPTY + st], ((i - STAGES) / STAGES) & 1, M.abort)) {
+            // the last stage first holds the Q chunks on their way to TMEM
+            if ((i >= STAGES && !mbar_wait(&M.bars[B_KV_EMPTY + st], ((i - STAGES) / STAGES) & 1, M.abort)) ||
+                (i == STAGES - 1 && !mbar_wait(&M.bars[B_Q_FULL], 0, M.abort))) {
                 give_up(M, a.status);
                 return false;
             }
             uint8_t* base = smem + L.kv + st * STAGE_BYTES;
             __half2 top = __half2half2(__ushort_as_half(0));
 #pragma unroll
-            for (int it = 0; it < 8; ++it) {
-                const int key = 8 * w + it;
+            for (int it = 0; it < WK; ++it) {
+                const int key = WK * w + it;
                 const uint2 h0 = widen4(r.lat[it].x), h1 = widen4(r.lat[it].y), h2 = widen4(r.lat[it].z), h3 = widen4(r.lat[it].w);
                 const uint32_t hw[8] = {h0.x, h0.y, h1.x, h1.y, h2.x, h2.y, h3.x, h3.y};
 #pragma unroll
@@ -353,8 +358,8 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
 #pragma unroll
             for (int it = 0; it < 2; ++it) {
                 const int f = it * 32 + lane;
-                const int key = 8 * w + (f >> 3);
-                *reinterpret_cast<uint4*>(base + (NCHUNK - 1) * REGION + key * 128 + (((f & 7) ^ (key & 7)) << 4)) = r.rope[it];
+                const int key = WK * w + (f >> 3);
+                if (f < 8 * WK) *reinterpret_cast<uint4*>(base + (NCHUNK - 1) * REGION + key * 128 + (((f & 7) ^ (key & 7)) << 4)) = r.rope[it];
             }
             // A NaN code must reach the rows that see its key and no other, but as a value it would
             // meet the zero probabilities of the others: it is stored as 0 and the key's scale
@@ -362,8 +367,8 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
             float sc = r.scale >= 0.f ? r.scale : __int_as_float(0x7fc00000);
             if (__any_sync(0xffffffffu, __hisnan(__low2half(top)) || __hisnan(__high2half(top)))) {
 #pragma unroll 1
-                for (int it = 0; it < 8; ++it) {
-                    const int key = 8 * w + it;
+                for (int it = 0; it < WK; ++it) {
+                    const int key = WK * w + it;
                     uint32_t* row = reinterpret_cast<uint32_t*>(base + region * REGION + key * 128);
                     bool found = false;
                     for (int e = 0; e < 8; ++e) {
@@ -378,10 +383,10 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
                     if (__any_sync(0xffffffffu, found) && (lane & 7) == it) sc = __int_as_float(0x7fc00000);
                 }
             }
-            if (lane < 8) {
+            if (lane < WK) {
                 const float cl = fmaxf(sc, MIN_SCALE);
-                M.key_sl[st * NK + 8 * w + lane] = make_float2(sc, log2f(cl));
-                M.key_inv[st * NK + 8 * w + lane] = 1.f / cl;
+                M.key_sl[st * NK + WK * w + lane] = make_float2(sc, log2f(cl));
+                M.key_inv[st * NK + WK * w + lane] = 1.f / cl;
             }
             fence_proxy_async_smem();                    // generic stores -> tensor-core reads
             __syncwarp();
@@ -408,12 +413,14 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
         const bool row_ok = r < nrows;
         const __nv_bfloat16* q0 = a.q + ((int64_t)b * rows + row0) * D_QK;
         if (T > 0) {
-            // a warp a row: its largest element's exponent, and the shared-memory chunks
-            const int f = quad;
-            for (int rb = f; rb < R; rb += 16) {
-                uint4 v[4][3];
+            // a warp a row: its largest element's exponent, then the row in fp16 (bf16 for the rope
+            // chunk) to shared memory; chunks bound for TMEM by way of the last key stage
+            constexpr int QB = 9;                        // rows in flight
+            uint8_t* const q_tmp = smem + L.kv + (STAGES - 1) * STAGE_BYTES;
+            for (int rb = quad; rb < RQ; rb += 4 * QB) {
+                uint4 v[QB][3];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
+                for (int u = 0; u < QB; ++u) {
                     const int rr = rb + 4 * u;
                     const uint4* src = reinterpret_cast<const uint4*>(q0 + (int64_t)rr * D_QK);
 #pragma unroll
@@ -421,9 +428,9 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
                         v[u][c] = rr < nrows && c * 32 + lane < 72 ? __ldg(src + c * 32 + lane) : make_uint4(0, 0, 0, 0);
                 }
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
+                for (int u = 0; u < QB; ++u) {
                     const int rr = rb + 4 * u;
-                    if (rr >= R) break;
+                    if (rr >= RQ) break;
                     float top = fmaxf(max_abs8(v[u][0]), fmaxf(max_abs8(v[u][1]), max_abs8(v[u][2])));
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -434,7 +441,7 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
 #pragma unroll
                     for (int c = 0; c < 3; ++c) {
                         const int pc = c * 32 + lane, ch = pc >> 3;
-                        if (pc >= 72 || ch < NQT) continue;
+                        if (pc >= 72) continue;
                         uint4 o;
                         if (ch < NCHUNK - 1)
                             o = make_uint4(q_to_f16(v[u][c].x, mul), q_to_f16(v[u][c].y, mul), q_to_f16(v[u][c].z, mul),
@@ -442,26 +449,25 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
                         else
                             o = make_uint4(q_to_bf16(v[u][c].x, mul), q_to_bf16(v[u][c].y, mul),
                                            q_to_bf16(v[u][c].z, mul), q_to_bf16(v[u][c].w, mul));
-                        *reinterpret_cast<uint4*>(smem + (ch - NQT) * R * 128 + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4)) = o;
+                        uint8_t* chunk = ch < NQT ? q_tmp + ch * RQ * 128 : smem + (ch - NQT) * RQ * 128;
+                        *reinterpret_cast<uint4*>(chunk + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4)) = o;
                     }
                 }
             }
             bar_sync(1, 128);
             // a thread a row: the TMEM chunks
-            const float mul = row_ok ? __int_as_float((254 << 23) - __float_as_int(M.row_exp[r])) : 0.f;   // 1 / row_exp
+            if (quad * 32 < RQ) {
 #pragma unroll 1
-            for (int c = 0; c < NQT; ++c) {
-                uint4 v[8];
-                uint32_t h[32];
-                const uint4* src = reinterpret_cast<const uint4*>(q0 + (int64_t)r * D_QK) + c * 8;
+                for (int c = 0; c < NQT; ++c) {
+                    uint32_t h[32];
+                    const uint8_t* src = q_tmp + c * RQ * 128 + min(r, RQ - 1) * 128;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = row_ok ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    h[4 * j] = q_to_f16(v[j].x, mul); h[4 * j + 1] = q_to_f16(v[j].y, mul);
-                    h[4 * j + 2] = q_to_f16(v[j].z, mul); h[4 * j + 3] = q_to_f16(v[j].w, mul);
+                    for (int j = 0; j < 8; ++j) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(src + ((j ^ (r & 7)) << 4));
+                        h[4 * j] = v.x; h[4 * j + 1] = v.y; h[4 * j + 2] = v.z; h[4 * j + 3] = v.w;
+                    }
+                    tmem_st32(tmem + lane_base + q_col + c * 32, h);
                 }
-                tmem_st32(tmem + lane_base + q_col + c * 32, h);
             }
             tmem_st_wait();
             fence_proxy_async_smem();
@@ -484,6 +490,7 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
         }
         const float c2 = T > 0 && row_ok ? a.scale * LOG2E * M.row_exp[r] : 0.f;
         const int plain_end = min(p, k_end);             // keys below this need no mask
+        const bool rows_used = quad * 32 < R;
         float m = -INFINITY, l = 0.f;
         bool ok = true;
         for (int i = 0; i < T; ++i) {
@@ -495,39 +502,42 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
             float x[NK];
             float mt = -INFINITY;
             const int k0 = k_begin + i * NK;
-            const bool plain = row_ok && k0 + NK <= plain_end;
             const float2* sl = M.key_sl + st * NK;
             const float* inv = M.key_inv + st * NK;
-            if (ok) {
+            if (ok && !rows_used) {                      // no row of this warp is in the tile
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&M.bars[B_S_FREE]);
+            } else if (ok) {
+                uint32_t va[NK / 16][16], vc[NK / 16][16];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t va[32], vc[32];
-                    tmem_ld32(tmem + lane_base + A_COL + 32 * h, va);
-                    tmem_ld32(tmem + lane_base + C_COL + 32 * h, vc);
-                    tmem_ld_wait();
-                    if (h == 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&M.bars[B_S_FREE]);
-                    }
-#pragma unroll
-                    for (int k = 0; k < 32; k += 2) {
-                        const float4 c = *reinterpret_cast<const float4*>(sl + 32 * h + k);
-                        x[32 * h + k] = fmaf(fmaf(__uint_as_float(va[k]), c.x, __uint_as_float(vc[k])), c2, c.y);
-                        x[32 * h + k + 1] = fmaf(fmaf(__uint_as_float(va[k + 1]), c.z, __uint_as_float(vc[k + 1])), c2, c.w);
-                    }
+                for (int h = 0; h < NK / 16; ++h) {
+                    tmem_ld16(tmem + lane_base + A_COL + 16 * h, va[h]);
+                    tmem_ld16(tmem + lane_base + C_COL + 16 * h, vc[h]);
                 }
-                if (!plain) {
+                tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&M.bars[B_S_FREE]);
+#pragma unroll
+                for (int k = 0; k < NK; k += 2) {
+                    const float4 c = *reinterpret_cast<const float4*>(sl + k);
+                    x[k] = fmaf(fmaf(__uint_as_float(va[k / 16][k % 16]), c.x, __uint_as_float(vc[k / 16][k % 16])), c2, c.y);
+                    x[k + 1] = fmaf(fmaf(__uint_as_float(va[k / 16][k % 16 + 1]), c.z, __uint_as_float(vc[k / 16][k % 16 + 1])), c2, c.w);
+                }
+                // rows past the tile need no mask of their own: nothing reads their P
+                if (k0 + NK > plain_end) {
 #pragma unroll
                     for (int k = 0; k < NK; ++k) {
                         const int j = k0 + k;
-                        if (!(row_ok && j < k_end && (j < p || ((vis >> (j - p)) & 1ull)))) x[k] = -INFINITY;
+                        if (!(j < k_end && (j < p || ((vis >> (j - p)) & 1ull)))) x[k] = -INFINITY;
                     }
                 }
+                float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                for (int k = 0; k < NK; ++k) mt = fmaxf(mt, x[k]);
+                for (int k = 4; k < NK; ++k) mx[k & 3] = fmaxf(mx[k & 3], x[k]);
+                mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             }
-            const bool need = ok && mt > m + TAU;
+            const bool need = ok && row_ok && mt > m + TAU;
             float alpha = 1.f;
             if (need) {
                 alpha = ex2(m - mt);
@@ -535,26 +545,25 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
                 m = mt;
             }
             uint32_t pk[NK / 2];
-            if (ok) {
+            if (ok && rows_used) {
                 const float mu = m == -INFINITY ? 0.f : m - P_SHIFT;
                 float l0 = 0.f, l1 = 0.f;
 #pragma unroll
                 for (int k = 0; k < NK; k += 4) {
                     const float4 iv = *reinterpret_cast<const float4*>(inv + k);
                     const float p0 = ex2(x[k] - mu), p1 = ex2(x[k + 1] - mu), p2 = ex2(x[k + 2] - mu), p3 = ex2(x[k + 3] - mu);
-                    // the sum keeps fp32 probabilities; a masked key's 1 / s may be anything but meets p = 0
-                    l0 = fmaf(p0, p0 != 0.f ? iv.x : 0.f, l0);
-                    l1 = fmaf(p1, p1 != 0.f ? iv.y : 0.f, l1);
-                    l0 = fmaf(p2, p2 != 0.f ? iv.z : 0.f, l0);
-                    l1 = fmaf(p3, p3 != 0.f ? iv.w : 0.f, l1);
+                    l0 = fmaf(p0, iv.x, l0);             // the sum keeps fp32 probabilities
+                    l1 = fmaf(p1, iv.y, l1);
+                    l0 = fmaf(p2, iv.z, l0);
+                    l1 = fmaf(p3, iv.w, l1);
                     const __half2 h0 = __floats2half2_rn(p0, p1), h1 = __floats2half2_rn(p2, p3);
                     pk[k / 2] = *reinterpret_cast<const uint32_t*>(&h0);
                     pk[k / 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
                 }
                 l += l0 + l1;
-                // P's buffer and O^T are free once O^T of the tile before is done
-                if (i >= 1) ok = mbar_wait(&M.bars[B_KV_EMPTY + (i - 1) % STAGES], ((i - 1) / STAGES) & 1, M.abort);
             }
+            // P's buffer and O^T are free once O^T of the tile before is done
+            if (ok && i >= 1) ok = mbar_wait(&M.bars[B_KV_EMPTY + (i - 1) % STAGES], ((i - 1) / STAGES) & 1, M.abort);
             if (bar_red_or(1, 128, need || !ok)) {
                 if (bar_red_or(1, 128, !ok)) { ok = false; break; }
                 if (i >= 1) {
@@ -658,17 +667,17 @@ cudaError_t launch_one(const Fp8Args& a, dim3 grid, int dev, cudaStream_t stream
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
-    const int smem = layout_for(a.R, NCHUNK - NQT).total;
+    const int smem = layout_for(a.R, a.RQ, NCHUNK - NQT).total;
     if (smem > MAX_SMEM || O_COL + 4 * a.R + 32 * NQT > (int)TMEM_COLS) return cudaErrorInvalidConfiguration;
     return launch_dependent(verify_fp8_kernel<NQT>, grid, dim3(NT), (size_t)smem, stream, a);
 }
 
-// As many Q chunks in TMEM as fit beside the scores and O^T: 2 at 80 rows, 4 up to 64, 6 up to 48.
+// As many Q chunks in TMEM as fit beside the scores and O^T: 3 at 80 MMA rows, 5 up to 64, 7 up to 48.
 cudaError_t launch_verify_fp8(const Fp8Args& a, int n_tiles, int dev, cudaStream_t stream) {
     const dim3 grid(a.nsplit, n_tiles, a.balanced ? 1 : a.B);
-    if (a.R <= 48) return launch_one<6>(a, grid, dev, stream);
-    if (a.R <= 64) return launch_one<4>(a, grid, dev, stream);
-    return launch_one<2>(a, grid, dev, stream);
+    if (a.R <= 48) return launch_one<7>(a, grid, dev, stream);
+    if (a.R <= 64) return launch_one<5>(a, grid, dev, stream);
+    return launch_one<3>(a, grid, dev, stream);
 }
 
 }  // namespace
@@ -699,6 +708,7 @@ extern "C" int mla_verify_attn_fp8(const void* q, const uint8_t* kv_lat, const f
     if (rc != MLA_OK) return rc;
     int n_tiles;
     tc_tiling(q_len * H, MAX_R, &n_tiles, &a.R_step, &a.R);
+    a.RQ = (a.R_step + 7) / 8 * 8;
     const long long per_stream = (long long)q_len * H, rows = B * per_stream;
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.lat = kv_lat; a.kscale = kv_scale; a.rope = static_cast<const __nv_bfloat16*>(kv_rope);
