@@ -37,9 +37,10 @@ namespace cg = cooperative_groups;
 namespace mla {
 namespace {
 
-constexpr int DV_THREADS = 512;
+constexpr int DV_THREADS = 256;
 constexpr int DV_WARPS = DV_THREADS / 32;
 constexpr int DV_MAX_CLUSTER = 8;
+constexpr int DV_BATCH = 4;                          // vectors of a row that a thread has in flight
 constexpr double UNIT = 1.0 / 35184372088832.0;      // 2^-45, the unit of the integer sums
 
 struct DraftArgs {
@@ -58,16 +59,32 @@ struct DraftArgs {
 };
 
 // A probability as it counts: NaN and negative as 0, above 1 as 1.
-__device__ __forceinline__ float prob(float x) { return x > 0.f ? fminf(x, 1.f) : 0.f; }
+__device__ __forceinline__ float prob(float x) { return __saturatef(x); }
 
-// max(p - A q, 0) in units of 2^-45, A = ah + al.
-__device__ __forceinline__ long long residual(float p, float q, float ah, float al) {
+// The residual's coefficient A in two fp32 parts, and which of three forms it takes.
+enum { FROM_P, MINUS_Q, MINUS_AQ };                  // A = 0, A = 1, any A
+struct Coef {
+    float ah, al;
+};
+
+// max(p - A q, 0) in units of 2^-45.
+template <int FORM>
+__device__ __forceinline__ long long residual(float p, float q, const Coef& c) {
+    // p - A q = d + e, e the rounding errors of the product and of the difference (where d > 0)
     // (explicit roundings: a contracted multiply-add would lose the errors' meaning)
-    const float ph = __fmul_rn(ah, q);
-    const float pe = fmaf(al, q, fmaf(ah, q, -ph));   // A q = ph + pe
-    const float d = __fsub_rn(p, ph);
-    const float e = __fsub_rn(__fsub_rn(__fsub_rn(p, d), ph), pe);   // p - A q = d + e where d > 0
-    if (!(d + e > 0.f)) return 0;
+    float d = p, e = 0.f;
+    if (FORM == MINUS_Q) {
+        d = __fsub_rn(p, q);
+        e = __fsub_rn(__fsub_rn(p, d), q);
+    } else if (FORM == MINUS_AQ) {
+        const float ph = __fmul_rn(c.ah, q);
+        const float pe = fmaf(c.al, q, fmaf(c.ah, q, -ph));
+        d = __fsub_rn(p, ph);
+        e = __fsub_rn(__fsub_rn(__fsub_rn(p, d), ph), pe);
+    }
+    const bool some = FORM == FROM_P || d + e > 0.f;
+    d = some ? d : 0.f;
+    e = some ? e : 0.f;
     // adding 1.5 * 2^23 rounds to an integer and leaves it in the low mantissa bits
     constexpr float MAGIC = 12582912.f;
     const float th = fmaf(d, 4194304.f, MAGIC);                               // d * 2^22
@@ -77,12 +94,66 @@ __device__ __forceinline__ long long residual(float p, float q, float ah, float 
     return (long long)(__float_as_int(th) - 0x4B400000) * 8388608ll + (__float_as_int(tl) - 0x4B400000);
 }
 
+// A residual row: p and q of the current node.  Positions k run over whole vectors of four that
+// start on 16-byte boundaries, `shift` elements before the row; element x = k - shift.
+struct Row {
+    const float* p;
+    const float* q;
+    int V, shift;
+};
+
+__device__ __forceinline__ void load4(const float* row, int x, int V, float (&f)[4]) {
+    if (x >= 0 && x + 4 <= V) {
+        const float4 t = __ldg(reinterpret_cast<const float4*>(row + x));
+        f[0] = t.x; f[1] = t.y; f[2] = t.z; f[3] = t.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = x + j >= 0 && x + j < V ? __ldg(row + x + j) : 0.f;
+    }
+}
+
+// Sum of the residual over positions lo, lo + step, .. < hi (vectors of four).
+template <int FORM>
+__device__ __forceinline__ long long sum_row(const Row& r, const Coef& c, int lo, int hi, int step) {
+    long long sum = 0;
+    const int end = min(hi, r.V + r.shift);
+    for (int k = lo; k < end; k += DV_BATCH * step) {
+        float p[DV_BATCH][4], q[DV_BATCH][4];
+#pragma unroll
+        for (int u = 0; u < DV_BATCH; ++u) {
+            const int x = k + u * step < end ? k + u * step - r.shift : r.V;   // past the end: all zero
+            load4(r.p, x, r.V, p[u]);
+            if (FORM != FROM_P) load4(r.q, x, r.V, q[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < DV_BATCH; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum += residual<FORM>(prob(p[u][j]), FORM != FROM_P ? prob(q[u][j]) : 0.f, c);
+    }
+    return sum;
+}
+
+__device__ __forceinline__ long long one(const Row& r, const Coef& c, int form, int x) {
+    const float p = prob(r.p[x]);
+    if (form == FROM_P) return residual<FROM_P>(p, 0.f, c);
+    return residual<MINUS_AQ>(p, prob(r.q[x]), c);   // equal to MINUS_Q at A = 1
+}
+
+__device__ __forceinline__ long long sum_range(const Row& r, const Coef& c, int form, int lo, int hi, int step) {
+    if (form == FROM_P) return sum_row<FROM_P>(r, c, lo, hi, step);
+    if (form == MINUS_Q) return sum_row<MINUS_Q>(r, c, lo, hi, step);
+    return sum_row<MINUS_AQ>(r, c, lo, hi, step);
+}
+
 struct Shared {
-    int par[MLA_MAX_Q_LEN], tok[MLA_MAX_Q_LEN];
+    int tok[MLA_MAX_Q_LEN];
     float u[MLA_MAX_Q_LEN], pt[MLA_MAX_Q_LEN], qt[MLA_MAX_Q_LEN];   // p and q of the node's token at its parent
+    unsigned long long kids[MLA_MAX_Q_LEN];            // bit i: node i is a child
+    unsigned long long first;                          // bit i: node i passes as the first child tried
+    unsigned long long todo;                           // children of the current node that are still to try
     int removed[MLA_MAX_Q_LEN];                        // tokens taken out of p (no drafter)
     int acc[MLA_MAX_Q_LEN];                            // accepted nodes
-    int n_acc, n_removed, cur, node, done;
+    int n_acc, n_removed, cur, done;
     double A, S;
     int have_S;
     long long warp_sum[2][DV_WARPS];
@@ -97,7 +168,7 @@ __device__ __forceinline__ bool is_removed(const Shared& s, int x) {
     return false;
 }
 
-__global__ void __launch_bounds__(DV_THREADS) draft_verify_kernel(const DraftArgs a, int C, int per_cta, int per_warp) {
+__global__ void __launch_bounds__(DV_THREADS, 4) draft_verify_kernel(const DraftArgs a, int C, int per_cta, int per_warp) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ Shared s;
@@ -108,106 +179,84 @@ __global__ void __launch_bounds__(DV_THREADS) draft_verify_kernel(const DraftArg
     const int64_t base = (int64_t)b * a.q_len;
     const bool drafter = a.q != nullptr;
     // ---- the nodes: parent, token, random number and both probabilities of the token
-    if (tid < a.q_len) {
-        const int i = tid;
-        int par = a.parents ? a.parents[base + i] : i - 1;
-        const int tok = a.tokens[base + i];
-        bool bad = false;
-        if (i == 0) {
-            par = -2;                                  // the root is nobody's child
-        } else if (par < -1 || par >= i || (par >= 0 && (tok < 0 || tok >= a.V))) {
-            bad = true;
-        }
-        if (bad) {
-            par = -2;
-            if (rank == 0) atomicOr(a.status, DEV_BAD_DRAFT);
-        }
-        float pt = 0.f, qt = 1.f;
-        if (par >= 0) {
-            pt = prob(a.p[(base + par) * V + tok]);
-            if (drafter) qt = prob(a.q[(base + par) * V + tok]);
-        }
-        s.par[i] = par;
-        s.tok[i] = tok;
-        s.u[i] = a.u[base + i];
-        s.pt[i] = pt;
-        s.qt[i] = qt;
-    }
+    if (tid < MLA_MAX_Q_LEN) s.kids[tid] = 0;
     if (tid == 0) {
-        s.n_acc = 0; s.n_removed = 0; s.cur = 0; s.node = 1; s.done = 0;
+        s.first = 0;
+        s.n_acc = 0; s.n_removed = 0; s.cur = 0; s.done = 0;
         s.A = 0.0; s.S = 1.0; s.have_S = 1;
     }
     __syncthreads();
-    const int64_t my_lo = (int64_t)rank * per_cta + (int64_t)warp * per_warp;
-    int64_t my_hi = my_lo + per_warp;
-    if (my_hi > (int64_t)(rank + 1) * per_cta) my_hi = (int64_t)(rank + 1) * per_cta;
-    int phase = 0;
+    if (tid > 0 && tid < a.q_len) {
+        const int i = tid;
+        const int par = a.parents ? a.parents[base + i] : i - 1;
+        const int tok = a.tokens[base + i];
+        const float u = a.u[base + i];
+        if (par < -1 || par >= i || (par >= 0 && (tok < 0 || tok >= a.V))) {
+            if (rank == 0) atomicOr(a.status, DEV_BAD_DRAFT);
+        } else if (par >= 0) {
+            const float pt = prob(a.p[(base + par) * V + tok]);
+            const float qt = drafter ? prob(a.q[(base + par) * V + tok]) : 1.f;
+            s.tok[i] = tok;
+            s.u[i] = u;
+            s.pt[i] = pt;
+            s.qt[i] = qt;
+            atomicOr(&s.kids[par], 1ull << i);
+            if ((double)u * (double)qt < (double)pt) atomicOr(&s.first, 1ull << i);   // exact: 48 bits
+        }
+    }
+    __syncthreads();
+    if (tid == 0) s.todo = s.kids[0];
+    const int my_lo = rank * per_cta + warp * per_warp, my_hi = my_lo + per_warp;
+    int phase = 0, form = FROM_P;
     bool fallback = false;
     long long total = 0, before = 0;
+    Row row;
+    Coef c;
     for (;;) {
-        // ---- walk until a test needs the residual's sum, or the tree ends
+        // ---- walk until a test needs the residual's sum, or no child is left
         if (tid == 0 && !fallback) {
-            int i = s.node;
-            for (; i < a.q_len; ++i) {
-                if (s.par[i] != s.cur) continue;
-                if (!s.have_S) break;
-                const double qx = s.qt[i];
-                double r;
-                if (drafter) {
-                    r = (double)s.pt[i] - s.A * qx;
+            unsigned long long todo = s.todo;
+            while (todo && s.have_S) {
+                const int i = __ffsll((long long)todo) - 1;
+                todo &= todo - 1;
+                bool yes;
+                if (s.A == 0.0 && s.n_removed == 0) {
+                    yes = (s.first >> i) & 1;
                 } else {
-                    r = is_removed(s, s.tok[i]) ? 0.0 : (double)s.pt[i];
+                    const double qx = s.qt[i];
+                    const double r = drafter ? (double)s.pt[i] - s.A * qx : (is_removed(s, s.tok[i]) ? 0.0 : (double)s.pt[i]);
+                    yes = (double)s.u[i] * qx * s.S < r;
                 }
-                if ((double)s.u[i] * qx * s.S < r) {
+                if (yes) {
                     s.acc[s.n_acc++] = i;
                     s.cur = i;
-                    s.A = 0.0; s.S = 1.0; s.have_S = 1;
+                    s.A = 0.0; s.S = 1.0;
                     s.n_removed = 0;
+                    todo = s.kids[i];
                 } else {
                     s.A += s.S;
                     s.have_S = 0;
                     if (!drafter && !is_removed(s, s.tok[i])) s.removed[s.n_removed++] = s.tok[i];
                 }
             }
-            s.node = i;
-            s.done = i >= a.q_len;
+            s.todo = todo;
+            s.done = todo == 0;
         }
         __syncthreads();
         // ---- sum of the residual over this CTA's part of the vocabulary
-        const int64_t row = (base + s.cur) * V;
-        const bool use_q = drafter && s.A > 0.0;
-        const float ah = (float)s.A, al = (float)(s.A - (double)ah);
-        const float* p = a.p + row;
-        const float* q = use_q ? a.q + row : nullptr;
-        // vectors of four start on 16-byte boundaries, `shift` elements before the row
-        const int shift = (int)(row & 3);
-        long long sum = 0;
-        for (int64_t k = my_lo + lane * 4; k < my_hi; k += 128) {
-            const int64_t x = k - shift;
-            if (x >= V) break;
-            float pv[4], qv[4] = {0.f, 0.f, 0.f, 0.f};
-            if (x >= 0 && x + 4 <= V) {
-                const float4 t = __ldg(reinterpret_cast<const float4*>(p + x));
-                pv[0] = t.x; pv[1] = t.y; pv[2] = t.z; pv[3] = t.w;
-                if (use_q) {
-                    const float4 w = __ldg(reinterpret_cast<const float4*>(q + x));
-                    qv[0] = w.x; qv[1] = w.y; qv[2] = w.z; qv[3] = w.w;
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const bool in = x + j >= 0 && x + j < V;
-                    pv[j] = in ? p[x + j] : 0.f;
-                    if (use_q) qv[j] = in ? q[x + j] : 0.f;
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) sum += residual(prob(pv[j]), prob(qv[j]), ah, al);
-        }
+        const int64_t at = (base + s.cur) * V;
+        row.p = a.p + at;
+        row.q = drafter ? a.q + at : nullptr;
+        row.V = a.V;
+        row.shift = (int)(at & 3);
+        form = !drafter || s.A == 0.0 ? FROM_P : (s.A == 1.0 ? MINUS_Q : MINUS_AQ);
+        c.ah = (float)s.A;
+        c.al = (float)(s.A - (double)c.ah);
+        long long sum = sum_range(row, c, form, my_lo + lane * 4, my_hi, 128);
         if (!drafter && !fallback)
             for (int j = lane; j < s.n_removed; j += 32) {
-                const int64_t x = s.removed[j] + shift;
-                if (x >= my_lo && x < my_hi) sum -= residual(prob(p[s.removed[j]]), 0.f, 0.f, 0.f);
+                const int k = s.removed[j] + row.shift;
+                if (k >= my_lo && k < my_hi) sum -= one(row, c, FROM_P, s.removed[j]);
             }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -219,11 +268,14 @@ __global__ void __launch_bounds__(DV_THREADS) draft_verify_kernel(const DraftArg
             s.cta_sum[phase] = t;
         }
         cluster.sync();
-        total = before = 0;
-        for (int r = 0; r < C; ++r) {
-            const long long v = *cluster.map_shared_rank(&s.cta_sum[phase], r);
-            if (r < rank) before += v;
-            total += v;
+        long long v = 0;                               // lane r: the sum of rank r
+        if (lane < C) v = *cluster.map_shared_rank(&s.cta_sum[phase], lane);
+        total = v;
+        before = lane < rank ? v : 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            total += __shfl_xor_sync(0xffffffffu, total, o);
+            before += __shfl_xor_sync(0xffffffffu, before, o);
         }
         const bool done = s.done;
         if (done && (total > 0 || fallback)) break;    // a fallback without a sum: no probability anywhere
@@ -241,7 +293,6 @@ __global__ void __launch_bounds__(DV_THREADS) draft_verify_kernel(const DraftArg
         phase ^= 1;
     }
     // ---- the next token: the element at which the running sum passes u_next * total
-    int next = -1;
     if (total > 0) {
         const double want = (double)a.u_next[b] * (double)total;
         long long thr = want > 0.0 ? (long long)want : 0;          // floor; cum > u T  <=>  cum > floor(u T)
@@ -249,39 +300,41 @@ __global__ void __launch_bounds__(DV_THREADS) draft_verify_kernel(const DraftArg
         thr -= before;
         if (thr >= 0 && thr < s.cta_sum[phase]) {                  // in this CTA's part (uniform over the CTA)
             int w = 0;
-            while (thr >= s.warp_sum[phase][w]) thr -= s.warp_sum[phase][w++];
-            const int64_t row = (base + s.cur) * V;
-            const bool use_q = drafter && s.A > 0.0;
-            const float ah = (float)s.A, al = (float)(s.A - (double)ah);
-            const int shift = (int)(row & 3);
-            const int64_t lo = (int64_t)rank * per_cta + (int64_t)w * per_warp - shift;
-            if (tid == 0) s.found = 0;
-            for (int64_t k = lo; k < lo + per_warp; k += DV_THREADS) {
-                const int64_t x = k + tid;
-                long long v = 0;
-                if (x >= 0 && x < V && x < lo + per_warp && (drafter || !is_removed(s, (int)x)))
-                    v = residual(prob(a.p[row + x]), use_q ? prob(a.q[row + x]) : 0.f, ah, al);
-                long long c = v;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const long long t = __shfl_up_sync(0xffffffffu, c, o);
-                    if (lane >= o) c += t;
-                }
-                __syncthreads();                       // s.scan of the previous chunk has been read
-                if (lane == 31) s.scan[warp] = c;
-                __syncthreads();
-                long long all = 0, mine = 0;
-                for (int i = 0; i < DV_WARPS; ++i) {
-                    if (i < warp) mine += s.scan[i];
-                    all += s.scan[i];
-                }
-                if (mine + c > thr && mine + c - v <= thr) s.found = (int)x;   // exactly one thread, v > 0
-                if (all > thr) break;
-                thr -= all;
+            while (w < DV_WARPS - 1 && thr >= s.warp_sum[phase][w]) thr -= s.warp_sum[phase][w++];
+            // the block takes that warp's part, a contiguous piece a thread
+            const int piece = ((per_warp + DV_THREADS - 1) / DV_THREADS + 3) / 4 * 4;
+            const int lo = rank * per_cta + w * per_warp;
+            const int k0 = lo + tid * piece, k1 = min(k0 + piece, lo + per_warp);
+            long long mine = 0;
+            if (k0 < k1) {
+                mine = sum_range(row, c, form, k0, k1, 4);
+                if (!drafter)
+                    for (int j = 0; j < s.n_removed; ++j) {
+                        const int k = s.removed[j] + row.shift;
+                        if (k >= k0 && k < k1) mine -= one(row, c, FROM_P, s.removed[j]);
+                    }
             }
+            long long cum = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long t = __shfl_up_sync(0xffffffffu, cum, o);
+                if (lane >= o) cum += t;
+            }
+            if (lane == 31) s.scan[warp] = cum;
             __syncthreads();
-            next = s.found;
-            if (tid == 0) a.out_tokens[base + s.n_acc] = next;
+            for (int i = 0; i < warp; ++i) cum += s.scan[i];
+            if (cum > thr && cum - mine <= thr) {                  // exactly one thread
+                thr -= cum - mine;
+                int x = max(k0 - row.shift, 0);
+                const int last = min(k1 - row.shift, a.V) - 1;
+                for (; x < last; ++x) {
+                    if (!drafter && is_removed(s, x)) continue;
+                    const long long v = one(row, c, form, x);
+                    if (thr < v) break;
+                    thr -= v;
+                }
+                a.out_tokens[base + s.n_acc] = x;
+            }
         }
     } else if (rank == 0 && tid == 0) {
         a.out_tokens[base + s.n_acc] = -1;
@@ -298,9 +351,11 @@ __global__ void __launch_bounds__(DV_THREADS) draft_verify_kernel(const DraftArg
 
 }  // namespace
 
-cudaError_t launch_draft_verify(const DraftArgs& a, int B, cudaStream_t stream) {
+// CTAs a stream: up to eight while the launch stays within one wave of four CTAs an SM and a
+// thread has a vector of each row at least.
+cudaError_t launch_draft_verify(const DraftArgs& a, int B, int num_sms, cudaStream_t stream) {
     int C = 1;
-    while (C < DV_MAX_CLUSTER && (int64_t)C * DV_THREADS * 4 < a.V) C *= 2;
+    while (C < DV_MAX_CLUSTER && (int64_t)C * DV_THREADS * 4 < a.V && 2ll * C * B <= 4ll * num_sms) C *= 2;
     // whole vectors of 128 elements a warp step; three elements more for the largest shift
     const int64_t span = (int64_t)a.V + 3;
     const int64_t per_warp = ((span + (int64_t)C * DV_WARPS - 1) / ((int64_t)C * DV_WARPS) + 127) / 128 * 128;
@@ -340,8 +395,9 @@ extern "C" int mla_draft_verify(const float* target_probs, const float* draft_pr
     a.p = target_probs; a.q = draft_probs; a.tokens = draft_tokens; a.parents = parents;
     a.u = u_accept; a.u_next = u_next; a.q_len = q_len; a.V = vocab;
     a.n_accepted = n_accepted; a.out_tokens = tokens; a.path = path;
-    int rc = device_state(nullptr, &a.status, nullptr);
+    int num_sms = 0;
+    int rc = device_state(nullptr, &a.status, &num_sms);
     if (rc != MLA_OK) return rc;
-    if (launch_draft_verify(a, B, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_LAUNCH;
+    if (launch_draft_verify(a, B, num_sms, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_LAUNCH;
     return MLA_OK;
 }
