@@ -39,7 +39,7 @@ namespace {
 
 constexpr int DV_THREADS = 256;
 constexpr int DV_WARPS = DV_THREADS / 32;
-constexpr int DV_MAX_CLUSTER = 8;
+constexpr int DV_MAX_CLUSTER = 16;                   // (more than eight CTAs: opted into per device)
 constexpr int DV_BATCH = 4;                          // vectors of a row that a thread has in flight
 constexpr double UNIT = 1.0 / 35184372088832.0;      // 2^-45, the unit of the integer sums
 
@@ -151,15 +151,16 @@ struct Shared {
     unsigned long long kids[MLA_MAX_Q_LEN];            // bit i: node i is a child
     unsigned long long first;                          // bit i: node i passes as the first child tried
     unsigned long long todo;                           // children of the current node that are still to try
-    int removed[MLA_MAX_Q_LEN];                        // tokens taken out of p (no drafter)
+    int removed[MLA_MAX_Q_LEN];                        // tokens taken out of p (no drafter), and their p
+    long long removed_p[MLA_MAX_Q_LEN];
     int acc[MLA_MAX_Q_LEN];                            // accepted nodes
-    int n_acc, n_removed, cur, done;
+    int n_acc, n_removed, cur, done, sum_wanted;
     double A, S;
-    int have_S;
+    int have_S, have_sum;                              // S is known; the sums are those of p at `cur` (no drafter)
+    long long sum;
     long long warp_sum[2][DV_WARPS];
     long long cta_sum[2];
     long long scan[DV_WARPS];
-    int found;
 };
 
 __device__ __forceinline__ bool is_removed(const Shared& s, int x) {
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(DV_THREADS, 4) draft_verify_kernel(const Draft
     if (tid == 0) {
         s.first = 0;
         s.n_acc = 0; s.n_removed = 0; s.cur = 0; s.done = 0;
-        s.A = 0.0; s.S = 1.0; s.have_S = 1;
+        s.A = 0.0; s.S = 1.0; s.have_S = 1; s.have_sum = 0;
     }
     __syncthreads();
     if (tid > 0 && tid < a.q_len) {
@@ -206,21 +207,21 @@ __global__ void __launch_bounds__(DV_THREADS, 4) draft_verify_kernel(const Draft
     }
     __syncthreads();
     if (tid == 0) s.todo = s.kids[0];
-    const int my_lo = rank * per_cta + warp * per_warp, my_hi = my_lo + per_warp;
+    const int cta_lo = rank * per_cta, my_lo = cta_lo + warp * per_warp, my_hi = my_lo + per_warp;
     int phase = 0, form = FROM_P;
     bool fallback = false;
-    long long total = 0, before = 0;
+    long long total = 0, before = 0;                   // sums over the vocabulary, and before this CTA's part
     Row row;
     Coef c;
     for (;;) {
-        // ---- walk until a test needs the residual's sum, or no child is left
+        // ---- walk until a test needs a sum that is not there, or no child is left
         if (tid == 0 && !fallback) {
             unsigned long long todo = s.todo;
             while (todo && s.have_S) {
                 const int i = __ffsll((long long)todo) - 1;
                 todo &= todo - 1;
                 bool yes;
-                if (s.A == 0.0 && s.n_removed == 0) {
+                if (s.A == 0.0) {
                     yes = (s.first >> i) & 1;
                 } else {
                     const double qx = s.qt[i];
@@ -232,108 +233,146 @@ __global__ void __launch_bounds__(DV_THREADS, 4) draft_verify_kernel(const Draft
                     s.cur = i;
                     s.A = 0.0; s.S = 1.0;
                     s.n_removed = 0;
+                    s.have_sum = 0;
                     todo = s.kids[i];
-                } else {
+                } else if (drafter) {
                     s.A += s.S;
                     s.have_S = 0;
-                    if (!drafter && !is_removed(s, s.tok[i])) s.removed[s.n_removed++] = s.tok[i];
+                } else {
+                    s.A = 1.0;                         // some rejection
+                    if (!is_removed(s, s.tok[i])) {
+                        s.removed[s.n_removed] = s.tok[i];
+                        s.removed_p[s.n_removed++] = residual<FROM_P>(s.pt[i], 0.f, c);
+                    }
+                    s.have_S = s.have_sum;             // p's sum less the tokens taken out
+                    if (s.have_sum) {
+                        long long left = s.sum;
+                        for (int j = 0; j < s.n_removed; ++j) left -= s.removed_p[j];
+                        s.S = (double)left * UNIT;
+                    }
                 }
             }
             s.todo = todo;
             s.done = todo == 0;
+            s.sum_wanted = drafter || !s.have_sum;
         }
         __syncthreads();
-        // ---- sum of the residual over this CTA's part of the vocabulary
-        const int64_t at = (base + s.cur) * V;
-        row.p = a.p + at;
-        row.q = drafter ? a.q + at : nullptr;
-        row.V = a.V;
-        row.shift = (int)(at & 3);
-        form = !drafter || s.A == 0.0 ? FROM_P : (s.A == 1.0 ? MINUS_Q : MINUS_AQ);
-        c.ah = (float)s.A;
-        c.al = (float)(s.A - (double)c.ah);
-        long long sum = sum_range(row, c, form, my_lo + lane * 4, my_hi, 128);
-        if (!drafter && !fallback)
-            for (int j = lane; j < s.n_removed; j += 32) {
-                const int k = s.removed[j] + row.shift;
-                if (k >= my_lo && k < my_hi) sum -= one(row, c, FROM_P, s.removed[j]);
-            }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) s.warp_sum[phase][warp] = sum;
-        __syncthreads();
-        if (tid == 0) {
-            long long t = 0;
-            for (int w = 0; w < DV_WARPS; ++w) t += s.warp_sum[phase][w];
-            s.cta_sum[phase] = t;
-        }
-        cluster.sync();
-        long long v = 0;                               // lane r: the sum of rank r
-        if (lane < C) v = *cluster.map_shared_rank(&s.cta_sum[phase], lane);
-        total = v;
-        before = lane < rank ? v : 0;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            total += __shfl_xor_sync(0xffffffffu, total, o);
-            before += __shfl_xor_sync(0xffffffffu, before, o);
-        }
         const bool done = s.done;
-        if (done && (total > 0 || fallback)) break;    // a fallback without a sum: no probability anywhere
+        // ---- sum of the residual (without a drafter: of p) over this CTA's part of the vocabulary
+        if (s.sum_wanted) {
+            const int64_t at = (base + s.cur) * V;
+            row.p = a.p + at;
+            row.q = drafter ? a.q + at : nullptr;
+            row.V = a.V;
+            row.shift = (int)(at & 3);
+            form = !drafter || s.A == 0.0 ? FROM_P : (s.A == 1.0 ? MINUS_Q : MINUS_AQ);
+            c.ah = (float)s.A;
+            c.al = (float)(s.A - (double)c.ah);
+            phase ^= 1;
+            long long sum = sum_range(row, c, form, my_lo + lane * 4, my_hi, 128);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == 0) s.warp_sum[phase][warp] = sum;
+            __syncthreads();
+            if (tid == 0) {
+                long long t = 0;
+                for (int w = 0; w < DV_WARPS; ++w) t += s.warp_sum[phase][w];
+                s.cta_sum[phase] = t;
+            }
+            cluster.sync();
+            long long v = 0;                           // lane r: the sum of rank r
+            if (lane < C) v = *cluster.map_shared_rank(&s.cta_sum[phase], lane);
+            total = v;
+            before = lane < rank ? v : 0;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                total += __shfl_xor_sync(0xffffffffu, total, o);
+                before += __shfl_xor_sync(0xffffffffu, before, o);
+            }
+        }
+        long long left = total;
+        for (int j = 0; j < s.n_removed; ++j) left -= s.removed_p[j];
+        if (done && (left > 0 || fallback)) break;     // a fallback without a sum: no probability anywhere
         __syncthreads();                               // everyone has read the walk's state
         if (tid == 0) {
             if (done) {                                // nothing left of the residual: p itself
                 s.A = 0.0;
                 s.n_removed = 0;
+                s.sum_wanted = drafter;
             } else {
-                s.S = (double)total * UNIT;
+                s.sum = total;
+                s.have_sum = !drafter;
+                s.S = (double)left * UNIT;
                 s.have_S = 1;
             }
         }
         if (done) fallback = true;
-        phase ^= 1;
     }
-    // ---- the next token: the element at which the running sum passes u_next * total
+    // ---- the next token: the element at which the running sum passes u_next times the whole
+    long long mine_all = s.cta_sum[phase];
+    for (int j = 0; j < s.n_removed; ++j) {
+        const int k = s.removed[j] + row.shift;
+        total -= s.removed_p[j];
+        if (k < cta_lo) before -= s.removed_p[j];
+        else if (k < cta_lo + per_cta) mine_all -= s.removed_p[j];
+    }
     if (total > 0) {
         const double want = (double)a.u_next[b] * (double)total;
         long long thr = want > 0.0 ? (long long)want : 0;          // floor; cum > u T  <=>  cum > floor(u T)
         if (thr > total - 1) thr = total - 1;
         thr -= before;
-        if (thr >= 0 && thr < s.cta_sum[phase]) {                  // in this CTA's part (uniform over the CTA)
+        if (thr >= 0 && thr < mine_all) {                          // in this CTA's part (uniform over the CTA)
             int w = 0;
-            while (w < DV_WARPS - 1 && thr >= s.warp_sum[phase][w]) thr -= s.warp_sum[phase][w++];
-            // the block takes that warp's part, a contiguous piece a thread
+            for (; w < DV_WARPS - 1; ++w) {
+                long long ws = s.warp_sum[phase][w];
+                for (int j = 0; j < s.n_removed; ++j) {
+                    const int k = s.removed[j] + row.shift - cta_lo;
+                    if (k >= w * per_warp && k < (w + 1) * per_warp) ws -= s.removed_p[j];
+                }
+                if (thr < ws) break;
+                thr -= ws;
+            }
+            // the block takes that warp's part, a contiguous piece a thread; then the warp whose
+            // piece it is, an element a lane
             const int piece = ((per_warp + DV_THREADS - 1) / DV_THREADS + 3) / 4 * 4;
-            const int lo = rank * per_cta + w * per_warp;
-            const int k0 = lo + tid * piece, k1 = min(k0 + piece, lo + per_warp);
+            const int lo = cta_lo + w * per_warp, hi = lo + per_warp;
+            const int k0 = lo + tid * piece, k1 = min(k0 + piece, hi);
             long long mine = 0;
             if (k0 < k1) {
                 mine = sum_range(row, c, form, k0, k1, 4);
-                if (!drafter)
-                    for (int j = 0; j < s.n_removed; ++j) {
-                        const int k = s.removed[j] + row.shift;
-                        if (k >= k0 && k < k1) mine -= one(row, c, FROM_P, s.removed[j]);
-                    }
+                for (int j = 0; j < s.n_removed; ++j) {
+                    const int k = s.removed[j] + row.shift;
+                    if (k >= k0 && k < k1) mine -= s.removed_p[j];
+                }
             }
-            long long cum = mine;
+            auto scan = [&](long long v) {
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long t = __shfl_up_sync(0xffffffffu, cum, o);
-                if (lane >= o) cum += t;
-            }
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long t = __shfl_up_sync(0xffffffffu, v, o);
+                    if (lane >= o) v += t;
+                }
+                return v;
+            };
+            long long cum = scan(mine);
             if (lane == 31) s.scan[warp] = cum;
             __syncthreads();
             for (int i = 0; i < warp; ++i) cum += s.scan[i];
-            if (cum > thr && cum - mine <= thr) {                  // exactly one thread
-                thr -= cum - mine;
-                int x = max(k0 - row.shift, 0);
-                const int last = min(k1 - row.shift, a.V) - 1;
-                for (; x < last; ++x) {
-                    if (!drafter && is_removed(s, x)) continue;
-                    const long long v = one(row, c, form, x);
-                    if (thr < v) break;
-                    thr -= v;
+            const unsigned hit = __ballot_sync(0xffffffffu, cum > thr && cum - mine <= thr);   // one lane of the block
+            if (hit) {
+                const int L = __ffs(hit) - 1;
+                thr -= __shfl_sync(0xffffffffu, cum - mine, L);
+                const int x0 = __shfl_sync(0xffffffffu, k0, L) - row.shift, x1 = __shfl_sync(0xffffffffu, k1, L) - row.shift;
+                for (int x = x0 + lane;; x += 32) {
+                    long long v = 0;
+                    if (x >= 0 && x < min(x1, a.V) && !is_removed(s, x)) v = one(row, c, form, x);
+                    const long long upto = scan(v);
+                    const unsigned at = __ballot_sync(0xffffffffu, upto > thr);
+                    if (at || x - lane + 32 >= x1) {
+                        if (lane == (at ? __ffs(at) - 1 : 0)) a.out_tokens[base + s.n_acc] = x;
+                        break;
+                    }
+                    thr -= __shfl_sync(0xffffffffu, upto, 31);
                 }
-                a.out_tokens[base + s.n_acc] = x;
             }
         }
     } else if (rank == 0 && tid == 0) {
@@ -351,9 +390,15 @@ __global__ void __launch_bounds__(DV_THREADS, 4) draft_verify_kernel(const Draft
 
 }  // namespace
 
-// CTAs a stream: up to eight while the launch stays within one wave of four CTAs an SM and a
+// CTAs a stream: up to sixteen while the launch stays within one wave of four CTAs an SM and a
 // thread has a vector of each row at least.
-cudaError_t launch_draft_verify(const DraftArgs& a, int B, int num_sms, cudaStream_t stream) {
+cudaError_t launch_draft_verify(const DraftArgs& a, int B, int num_sms, int dev, cudaStream_t stream) {
+    static bool attr_set[64];
+    if (!attr_set[dev]) {
+        cudaError_t e = cudaFuncSetAttribute(draft_verify_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        attr_set[dev] = true;
+    }
     int C = 1;
     while (C < DV_MAX_CLUSTER && (int64_t)C * DV_THREADS * 4 < a.V && 2ll * C * B <= 4ll * num_sms) C *= 2;
     // whole vectors of 128 elements a warp step; three elements more for the largest shift
@@ -395,9 +440,9 @@ extern "C" int mla_draft_verify(const float* target_probs, const float* draft_pr
     a.p = target_probs; a.q = draft_probs; a.tokens = draft_tokens; a.parents = parents;
     a.u = u_accept; a.u_next = u_next; a.q_len = q_len; a.V = vocab;
     a.n_accepted = n_accepted; a.out_tokens = tokens; a.path = path;
-    int num_sms = 0;
-    int rc = device_state(nullptr, &a.status, &num_sms);
+    int num_sms = 0, dev = 0;
+    int rc = device_state(&dev, &a.status, &num_sms);
     if (rc != MLA_OK) return rc;
-    if (launch_draft_verify(a, B, num_sms, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_LAUNCH;
+    if (launch_draft_verify(a, B, num_sms, dev, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_LAUNCH;
     return MLA_OK;
 }
