@@ -68,8 +68,8 @@ __host__ __device__ inline void split_range(int n, int S, int s, int tile, int* 
 
 // Balanced key split of one launch over B <= 64 streams of unequal length, decided on
 // the device (the host does not know the lengths): with T the sum of the valid lengths,
-// the keys are cut into chunks of chunk = max(128, ceil(T / G) rounded up to `unit`, the
-// keys of a tile) keys;
+// the keys are cut into chunks of chunk = max(least, ceil(T / G)) keys, rounded up to `unit`, the
+// keys of a tile;
 // stream b gets ns_b = ceil(n_b / chunk) consecutive split slots (one for a stream whose
 // length is invalid, which then writes NaN), slots numbered stream after stream, at
 // most G + B of them.  Every warp evaluates it alike (lane i holds streams i and
@@ -82,7 +82,7 @@ struct BalancedPlan {
 };
 
 __device__ inline BalancedPlan balanced_plan(const int32_t* seq_lens, int B, int q_len, int slot_stride, int G,
-                                             int unit = 32) {
+                                             int unit = 32, int least = 128) {
     const int lane = threadIdx.x & 31;
     BalancedPlan P;
     int* n = P.n;
@@ -99,8 +99,8 @@ __device__ inline BalancedPlan balanced_plan(const int32_t* seq_lens, int B, int
     for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     // 32-bit divisions whenever the total fits (warp-uniform branch)
     long long c = t < (1ll << 30) ? (long long)(((unsigned)t + (unsigned)G - 1u) / (unsigned)G) : (t + G - 1) / G;
+    if (c < least) c = least;
     c = (c + unit - 1) / unit * unit;
-    if (c < 128) c = 128;
     if (c > (1 << 30)) c = 1 << 30;
     P.chunk = (int)c;
     int run = 0;

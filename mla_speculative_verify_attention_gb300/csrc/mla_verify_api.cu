@@ -84,7 +84,7 @@ constexpr int CB_BATCH = 8;
 struct CombineBalanced {
     int on;
     const int32_t* seq_lens;
-    int B, q_len, slot_stride, G, rows, unit;
+    int B, q_len, slot_stride, G, rows, unit, least;
 };
 
 // The merged sums are fp32; a bf16 output rounds each of them once.
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(CB_THREADS) combine_kernel(const float* __rest
     long long po = row * (long long)S_all * D_V;
     if (bal.on) {
         const BalancedPlan P = balanced_plan(bal.seq_lens, bal.B, bal.q_len, bal.slot_stride, bal.G,
-                                             bal.unit);
+                                             bal.unit, bal.least);
         const int b = (int)(row / bal.rows), r = (int)(row % bal.rows);
         int first, count;
         balanced_stream(P, b, &first, &count);
@@ -237,23 +237,24 @@ cudaError_t launch_combine_bf16(const float* part_out, const float* part_lse, lo
 // S here bounds the slots of one stream (nsplit slots in all): the weights' shared memory.
 namespace {
 template <typename Out>
-cudaError_t combine_balanced(const VerifyArgs& a, Out* out, int unit, cudaStream_t stream) {
+cudaError_t combine_balanced(const VerifyArgs& a, Out* out, int unit, int least, cudaStream_t stream) {
     CombineBalanced bal;
     bal.on = 1;
     bal.seq_lens = a.seq_lens;
     bal.B = a.B; bal.q_len = a.q_len; bal.slot_stride = a.slot_stride; bal.G = a.bal_G;
     bal.rows = a.q_len * a.H;
     bal.unit = unit;
+    bal.least = least;
     return launch_combine_any(a.part_out, a.part_lse, (long long)a.B * bal.rows, a.nsplit, out, a.lse, bal, stream);
 }
 }  // namespace
 
 cudaError_t launch_combine_balanced(const VerifyArgs& a, cudaStream_t stream) {
-    return combine_balanced(a, a.out, 32, stream);
+    return combine_balanced(a, a.out, 32, 128, stream);
 }
 
 cudaError_t launch_combine_balanced_bf16(const VerifyArgs& a, __nv_bfloat16* out, int unit, cudaStream_t stream) {
-    return combine_balanced(a, out, unit, stream);
+    return combine_balanced(a, out, unit, unit, stream);
 }
 
 }  // namespace mla
