@@ -17,7 +17,7 @@
 namespace mla {
 namespace {
 
-constexpr int KQ_THREADS = 256;
+constexpr int KQ_THREADS = 128;
 constexpr float E4M3_MAX = 448.f;
 
 __device__ __forceinline__ void row8(const uint4& v, float (&f)[8]) {
@@ -81,17 +81,18 @@ __global__ void __launch_bounds__(KQ_THREADS)
     const int64_t i = ((int64_t)blockIdx.x * KQ_THREADS + threadIdx.x) >> 5;
     const int lane = threadIdx.x & 31;
     if (i >= n_rows) return;
-    const int s = slots[i];
+    // the row is on its way before the slot is looked at
+    const int s = __ldg(slots + i);
+    const uint4* src = reinterpret_cast<const uint4*>(rows + i * D_QK);
+    const uint4 ra = __ldg(src + lane), rb = __ldg(src + 32 + lane);
+    const uint4 rope = lane < 8 ? __ldg(src + 64 + lane) : make_uint4(0, 0, 0, 0);
     if (s < 0 || (int64_t)s >= n_pool) {
         if (lane == 0) atomicOr(status, DEV_BAD_SLOT);
         return;
     }
-    const uint4* src = reinterpret_cast<const uint4*>(rows + i * D_QK);
     float a[8], b[8];
-    row8(__ldg(src + lane), a);
-    row8(__ldg(src + 32 + lane), b);
-    uint4 rope = make_uint4(0, 0, 0, 0);
-    if (lane < 8) rope = __ldg(src + 64 + lane);
+    row8(ra, a);
+    row8(rb, b);
     float m = warp_max(max_abs8(b, max_abs8(a, 0.f, false), false));
     const bool finite = m < INFINITY;                  // (of what is not NaN)
     if (!finite) m = warp_max(max_abs8(b, max_abs8(a, 0.f, true), true));
