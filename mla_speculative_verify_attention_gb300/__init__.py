@@ -369,15 +369,14 @@ def _device_of(*tensors) -> int:
     """The one CUDA device of these tensors (None: left out), which all have to be contiguous."""
     dev = -1
     for t in tensors:
-        if t is None:
-            continue
-        d = t.get_device()
-        if d < 0 or not t.is_contiguous():
-            raise ValueError("all tensors must be contiguous CUDA tensors")
-        if d != dev:
-            if dev >= 0:
-                raise ValueError("all tensors must be on the same device")
-            dev = d
+        if t is not None:
+            d = t.get_device()
+            if d < 0 or not t.is_contiguous():
+                raise ValueError("all tensors must be contiguous CUDA tensors")
+            if d != dev:
+                if dev >= 0:
+                    raise ValueError("all tensors must be on the same device")
+                dev = d
     return dev
 
 
@@ -389,19 +388,19 @@ def _on(dev: int):
 def _stream_on(stream, dev: int) -> int:
     """The stream a call is enqueued on: the given one, else the device's current one."""
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(dev)
     if stream.device.index != dev:
         raise ValueError("the stream must belong to the tensors' device")
     return stream.cuda_stream
 
 
-def _empty(shape, dtype, dev: int, stream):
-    """Memory for a call on `stream`: allocated for that stream, so that it is not handed out
-    again before the call has run."""
+def _empty(like: torch.Tensor, shape, dtype, stream):
+    """Memory for a call on `stream`, on the device of `like`: allocated for that stream, so that it
+    is not handed out again before the call has run."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _addr(t: Optional[torch.Tensor]) -> int:
@@ -462,9 +461,9 @@ def qk_norm_rope(q: Optional[torch.Tensor], kv: Optional[torch.Tensor], position
     with _on(dev):
         at = _stream_on(stream, dev)
         if q is not None and q_out is None:
-            q_out = _empty(q.shape, torch.bfloat16, dev, stream)
+            q_out = _empty(q, q.shape, torch.bfloat16, stream)
         if kv is not None and kv_out is None:
-            kv_out = _empty(kv.shape, torch.bfloat16, dev, stream)
+            kv_out = _empty(kv, kv.shape, torch.bfloat16, stream)
         _check("mla_qk_norm_rope", _call("mla_qk_norm_rope")(
             _addr(q), _addr(kv), _addr(q_weight), _addr(kv_weight), positions.data_ptr(), inv_freq.data_ptr(),
             eps, 1 if interleaved else 0, positions.numel(), H, _addr(q_out), _addr(kv_out), at))
@@ -507,7 +506,7 @@ def kv_read_fp8(kv_lat: torch.Tensor, kv_scale: torch.Tensor, kv_rope: torch.Ten
     with _on(dev):
         at = _stream_on(stream, dev)
         if out is None:
-            out = _empty((n, D_QK), torch.bfloat16, dev, stream)
+            out = _empty(kv_rope, (n, D_QK), torch.bfloat16, stream)
         _check("mla_kv_read_fp8", _call("mla_kv_read_fp8")(
             kv_lat.data_ptr(), kv_scale.data_ptr(), kv_rope.data_ptr(), n_pool, slots.data_ptr(), out.data_ptr(), n, at))
     return out
@@ -546,12 +545,12 @@ def verify_attn_fp8(q: torch.Tensor, kv_lat: torch.Tensor, kv_scale: torch.Tenso
     with _on(dev):
         at = _stream_on(stream, dev)
         if out is None:
-            out = _empty((B, q_len, H, D_V), torch.bfloat16, dev, stream)
+            out = _empty(q, (B, q_len, H, D_V), torch.bfloat16, stream)
         if lse is None:
-            lse = _empty((B, q_len, H), torch.float32, dev, stream)
+            lse = _empty(q, (B, q_len, H), torch.float32, stream)
         if workspace is None:
             ns = nsplit if nsplit > 0 else auto_nsplit(B, q_len, H, stride, num_sms(dev), 1 << 62)
-            workspace = _empty((max(workspace_bytes(B, q_len, H, ns), 256),), torch.uint8, dev, stream)
+            workspace = _empty(q, (max(workspace_bytes(B, q_len, H, ns), 256),), torch.uint8, stream)
         _check("mla_verify_attn_fp8", _call("mla_verify_attn_fp8")(
             q.data_ptr(), kv_lat.data_ptr(), kv_scale.data_ptr(), kv_rope.data_ptr(), n_pool, slot_table.data_ptr(),
             stride, seq_lens.data_ptr(), mask, bits, B, q_len, H, scale, out.data_ptr(), lse.data_ptr(), nsplit,
@@ -589,11 +588,11 @@ def draft_verify(target_probs: torch.Tensor, draft_probs: Optional[torch.Tensor]
     with _on(dev):
         at = _stream_on(stream, dev)
         if n_accepted is None:
-            n_accepted = _empty((B,), torch.int32, dev, stream)
+            n_accepted = _empty(draft_tokens, (B,), torch.int32, stream)
         if tokens is None:
-            tokens = _empty(nodes, torch.int32, dev, stream)
+            tokens = _empty(draft_tokens, nodes, torch.int32, stream)
         if path is None:
-            path = _empty(nodes, torch.int32, dev, stream)
+            path = _empty(draft_tokens, nodes, torch.int32, stream)
         _check("mla_draft_verify", _call("mla_draft_verify")(
             target_probs.data_ptr(), _addr(draft_probs), draft_tokens.data_ptr(), _addr(parents),
             u_accept.data_ptr(), u_next.data_ptr(), B, q_len, vocab, n_accepted.data_ptr(), tokens.data_ptr(),
