@@ -14,26 +14,37 @@
 // maximum may lag by 2^8 before O is rescaled); P's rounding is relative 2^-12.  Scales below
 // 2^-90 (rows of zeros) count as 2^-90 in the weight.
 //
-// One CTA handles up to 80 query rows (r = t * H + h of one stream) over one key split, in
-// tiles of 64 keys:
+// One CTA handles up to 72 query rows (r = t * H + h of one stream) over one key split, in
+// tiles of 48 keys:
 //   gather   eight warps read the tile's raw rows (512 code bytes, 128 rope bytes, scale) from
 //            the slot table straight into registers, two tiles ahead, and widen them
 //            (e4m3x2 -> f16x2, one instruction a pair) into a 128-byte-swizzled stage
-//   A, C     tcgen05.mma M=128 (query rows) x N=64 (keys): K=512 in fp16, K=64 (rope) in bf16;
+//   A, C     tcgen05.mma M=128 (query rows) x N=48 (keys): K=512 in fp16, K=64 (rope) in bf16;
 //            as many 64-dim chunks of Q as TMEM has columns for sit there
 //   P        one thread a query row: mask, running maximum and sum, P to shared memory
-//   O^T     += code^T P^T: M=128 (value dims) x N=rows x K=64 keys, four 128-dim chunks in TMEM
-// What bounds it: shared-memory bandwidth of the matrix operands (128 B a cycle): per tile of
-// 64 keys and 80 rows about 1600 cycles for A and C, 830 for O^T and 580 for the widened
-// stores, against 1930 for the keys' HBM bytes at 1/152 of the measured copy rate.  Tiles of 64 keys
-// read each Q chunk from shared memory half as often as tiles of 32.
+//   O^T     += code^T P^T: M=128 (value dims) x N=rows x K=48 keys, four 128-dim chunks in TMEM
+//
+// What bounds it, with long streams: shared memory (128 B a cycle).  A tile's matrix operands
+// take about 1900 cycles of it at 72 rows (a 128-row Q chunk is read whole, 4 KB an MMA), the
+// widened stores, the row loads' way through L1 and the softmax another 1200; its HBM bytes take
+// 1450 cycles at 1/152 of the measured copy rate.  Measured 1.9 us (3900 cycles) a tile: a mixed
+// batch of eight streams, 181 thousand keys, 74 us a call.  A tile is 48 keys because three such
+// stages fit beside Q (two of 64 keys wait for each other: 83 us; two of 48: 81 us).  Two forms that
+// were measured and not kept: codes as the matrix units' fp8 operands for scores and values, without
+// any widening (keys as rows of the scores, Q in two e4m3 pieces, P in three; half of the
+// shared-memory traffic, but only one tile of 128 keys fits, and scores, P and values follow each
+// other: 79 us, and 26 instead of 17 us at one tile a CTA, whose code is three times as long); rows
+// called into L2 four tiles ahead (80 us).
+// With few keys: the chain of cold reads (length, slots, rows; queries), the first pass through the
+// code and the epilogue's partial rows: 15.7 us a call at one tile a CTA and 72 rows.
 //
 // Warps (512 threads): 0 issues A and C, 1 issues O^T (whole warp, one elected lane), 4-7 Q,
-// softmax and epilogue (TMEM lane quadrant = warp % 4), 8-15 gather and widening (eight keys of
+// softmax and epilogue (TMEM lane quadrant = warp % 4), 8-15 gather and widening (six keys of
 // a tile each).  The launch's 512 x 128 registers are shared out again per warpgroup: 72 a
-// thread for warps 0-3, 168 for the softmax (a row's 64 scores), 136 for the gather (two
-// tiles in flight): 128 x (72 + 168 + 2 x 136) = 65536, the launch's total.  Every mbarrier wait is bounded; see verify_tc.cu's file for the scheme, which is
-// the same: the first to give up sets the abort flag and the status bit, every role leaves.
+// thread for warps 0-3, 168 for the softmax (a row's 48 scores in two parts), 136 for the gather
+// (two tiles in flight): 128 x (72 + 168 + 2 x 136) = 65536, the launch's total.  Every mbarrier
+// wait is bounded: the first to give up sets the abort flag and the status bit, and every role
+// leaves.
 #include "../../include/mla_verify.h"
 #include "internal.cuh"
 #include "tc_ptx.cuh"
@@ -666,6 +677,11 @@ cudaError_t launch_one(const Fp8Args& a, dim3 grid, int dev, cudaStream_t stream
     if (!attr_set[dev]) {
         cudaError_t e = cudaFuncSetAttribute(verify_fp8_kernel<NQT>, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
         if (e != cudaSuccess) return e;
+        // the warpgroups' shares have to be in the launch's registers, or their request would wait for ever
+        cudaFuncAttributes at;
+        e = cudaFuncGetAttributes(&at, verify_fp8_kernel<NQT>);
+        if (e != cudaSuccess) return e;
+        if (at.numRegs * NT < 128 * (72 + 168 + 2 * 136)) return cudaErrorInvalidConfiguration;
         attr_set[dev] = true;
     }
     const int smem = layout_for(a.R, a.RQ, NCHUNK - NQT).total;
