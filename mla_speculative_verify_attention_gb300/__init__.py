@@ -398,9 +398,17 @@ def _empty(like: torch.Tensor, shape, dtype, stream):
     """Memory for a call on `stream`, on the device of `like`: allocated for that stream, so that it
     is not handed out again before the call has run."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _empty_like(like: torch.Tensor, dtype, stream):
+    """_empty of the shape of `like` (a contiguous tensor); the quicker way for small outputs."""
+    if stream is None:
+        return torch.empty_like(like, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(like, dtype=dtype)
 
 
 def _addr(t: Optional[torch.Tensor]) -> int:
@@ -461,9 +469,9 @@ def qk_norm_rope(q: Optional[torch.Tensor], kv: Optional[torch.Tensor], position
     with _on(dev):
         at = _stream_on(stream, dev)
         if q is not None and q_out is None:
-            q_out = _empty(q, q.shape, torch.bfloat16, stream)
+            q_out = _empty_like(q, torch.bfloat16, stream)
         if kv is not None and kv_out is None:
-            kv_out = _empty(kv, kv.shape, torch.bfloat16, stream)
+            kv_out = _empty_like(kv, torch.bfloat16, stream)
         _check("mla_qk_norm_rope", _call("mla_qk_norm_rope")(
             _addr(q), _addr(kv), _addr(q_weight), _addr(kv_weight), positions.data_ptr(), inv_freq.data_ptr(),
             eps, 1 if interleaved else 0, positions.numel(), H, _addr(q_out), _addr(kv_out), at))
@@ -588,11 +596,11 @@ def draft_verify(target_probs: torch.Tensor, draft_probs: Optional[torch.Tensor]
     with _on(dev):
         at = _stream_on(stream, dev)
         if n_accepted is None:
-            n_accepted = _empty(draft_tokens, (B,), torch.int32, stream)
+            n_accepted = _empty_like(u_next, torch.int32, stream)
         if tokens is None:
-            tokens = _empty(draft_tokens, nodes, torch.int32, stream)
+            tokens = _empty_like(draft_tokens, torch.int32, stream)
         if path is None:
-            path = _empty(draft_tokens, nodes, torch.int32, stream)
+            path = _empty_like(draft_tokens, torch.int32, stream)
         _check("mla_draft_verify", _call("mla_draft_verify")(
             target_probs.data_ptr(), _addr(draft_probs), draft_tokens.data_ptr(), _addr(parents),
             u_accept.data_ptr(), u_next.data_ptr(), B, q_len, vocab, n_accepted.data_ptr(), tokens.data_ptr(),
