@@ -474,7 +474,7 @@ def qk_norm_rope(q: Optional[torch.Tensor], kv: Optional[torch.Tensor], position
             kv_out = _empty_like(kv, torch.bfloat16, stream)
         _check("mla_qk_norm_rope", _call("mla_qk_norm_rope")(
             _addr(q), _addr(kv), _addr(q_weight), _addr(kv_weight), positions.data_ptr(), inv_freq.data_ptr(),
-            eps, 1 if interleaved else 0, positions.numel(), H, _addr(q_out), _addr(kv_out), at))
+            float(eps), 1 if interleaved else 0, positions.numel(), H, _addr(q_out), _addr(kv_out), at))
     return q_out, kv_out
 
 
@@ -561,7 +561,7 @@ def verify_attn_fp8(q: torch.Tensor, kv_lat: torch.Tensor, kv_scale: torch.Tenso
             workspace = _empty(q, (max(workspace_bytes(B, q_len, H, ns), 256),), torch.uint8, stream)
         _check("mla_verify_attn_fp8", _call("mla_verify_attn_fp8")(
             q.data_ptr(), kv_lat.data_ptr(), kv_scale.data_ptr(), kv_rope.data_ptr(), n_pool, slot_table.data_ptr(),
-            stride, seq_lens.data_ptr(), mask, bits, B, q_len, H, scale, out.data_ptr(), lse.data_ptr(), nsplit,
+            stride, seq_lens.data_ptr(), mask, bits, B, q_len, H, float(scale), out.data_ptr(), lse.data_ptr(), nsplit,
             workspace.data_ptr(), workspace.numel(), at))
     return out, lse
 

@@ -40,7 +40,7 @@ namespace {
 constexpr int DV_THREADS = 256;
 constexpr int DV_WARPS = DV_THREADS / 32;
 constexpr int DV_MAX_CLUSTER = 16;                   // (more than eight CTAs: opted into per device)
-constexpr int DV_BATCH = 4;                          // vectors of a row that a thread has in flight
+constexpr int DV_BATCH = 2;                          // vectors of each row that a thread has in flight
 constexpr double UNIT = 1.0 / 35184372088832.0;      // 2^-45, the unit of the integer sums
 
 struct DraftArgs {

@@ -192,3 +192,21 @@ def test_graph_replay_and_given_outputs(cuda_lib):
         for k in range(3):
             en, et, ep = ref.accept(c[0][k], c[1][k], c[2][k], c[3][k], c[4][k], c[5][k])
             assert (int(outs[0][k]), outs[1][k].tolist(), outs[2][k].tolist()) == (en, et, ep)
+
+
+def test_many_streams_small_vocabulary(cuda_lib):
+    """More streams than CTAs fit the GPU at once, one CTA a stream."""
+    check(cuda_lib, make(700, 3, 70, seed=15, tree=True, size=1.5))
+
+
+def test_two_streams_at_once(cuda_lib):
+    mv = cuda_lib
+    c = make(4, 9, 30000, seed=16, tree=True)
+    dev = [torch.from_numpy(np.ascontiguousarray(x)).cuda() for x in c]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [mv.draft_verify(*dev, stream=s) for _ in range(5) for s in streams]
+    torch.cuda.synchronize()
+    want = check(mv, c)
+    for g in got:
+        assert all(np.array_equal(x.cpu().numpy(), y) for x, y in zip(g, want))

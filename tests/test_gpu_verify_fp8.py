@@ -64,7 +64,8 @@ def agree(out, lse, want, what=""):
     assert np.array_equal(np.isneginf(gl), empty), f"{what}: rows without a visible key differ"
     assert np.all(go[empty] == 0), f"{what}: rows without a visible key are zero"
     assert np.all(np.isfinite(go)) and np.all(np.isfinite(gl[~empty])), f"{what}: non-finite values"
-    assert np.all(np.abs(gl - l)[~empty] <= t_lse[~empty]), f"{what}: lse off by {np.max(np.abs(gl - l)[~empty]):.3e}"
+    dl = np.abs(gl[~empty] - l[~empty])
+    assert np.all(dl <= t_lse[~empty]), f"{what}: lse off by {np.max(dl):.3e}"
     d = np.abs(go - o) - t_out
     assert np.all(d <= 0), f"{what}: out off by {np.max(d):.3e} over its bound"
 
@@ -259,3 +260,66 @@ def test_side_stream_and_graph(cuda_lib):
         torch.cuda.synchronize()
         agree(out, lse, c.expected())
     assert mv.device_status() == 0
+
+
+def test_two_streams_at_once(cuda_lib):
+    """Calls on two streams at the same time, each with a workspace of its own, over one cache."""
+    mv = cuda_lib
+    c = Case(2, 9, 8, [3000, 700], seed=36, mask="tree")
+    dev, want = c.device(), c.expected()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(6):
+        for s in streams:
+            got.append(mv.verify_attn_fp8(*dev, stream=s))
+    torch.cuda.synchronize()
+    for out, lse in got:
+        agree(out, lse, want)
+        assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
+
+
+def test_same_cache_as_the_sparse_decode(cuda_lib):
+    """One token a stream over all of its keys: the sparse decode with every key listed, whose keys are
+    rounded to bf16 (a score moves by at most 2^-8 scale sum |q k|)."""
+    mv = cuda_lib
+    c = Case(3, 1, 16, [299, 299, 299], seed=37)
+    q, lat, sc, rope, table, seq, _, scale = c.device()
+    out, lse = mv.verify_attn_fp8(q, lat, sc, rope, table, seq, None, scale)
+    o2, l2 = mv.sparse_fp8_decode(q[:, 0].contiguous(), lat, sc, rope, table, scale)
+    torch.cuda.synchronize()
+    want = c.expected()
+    agree(out, lse, want)
+    for b in range(3):
+        k = c.keys_of(b)
+        ds = 2.0 ** -8 * scale * (np.abs(ref.f64(c.q[b, 0])) @ np.abs(k).T).max(1)
+        assert np.all(np.abs(ref.f64(l2[b]) - want[1][b, 0]) <= ds + want[3][b, 0])
+        p = np.exp(scale * ref.f64(c.q[b, 0]) @ k.T - want[1][b, 0][:, None])
+        size = p @ np.abs(k[:, :512])
+        assert np.all(np.abs(ref.f64(o2[b]) - want[0][b, 0]) <= want[2][b, 0] + size * (2.2 * ds[:, None] + 2.0 ** -8))
+
+
+def test_expired_wait_reports_timeout_and_context_survives(cuda_lib):
+    """The gather withholds its first arrival (test hook): the bounded waits run out, the status says
+    so, the outputs are finite, and the next call is exact again."""
+    mv = cuda_lib
+    c = Case(1, 9, 8, [200], seed=38, mask="tree")
+    dev = c.device()
+    mv.device_status(clear=True)
+    assert mv.load().mla_debug_stall_next_launch() == 0
+    out, _ = mv.verify_attn_fp8(*dev)
+    torch.cuda.synchronize()
+    assert mv.device_status(clear=True) & mv.DEV_TIMEOUT
+    assert bool(torch.isfinite(out).all())
+    check(mv, c)
+
+
+def test_rescale_branch_runs(cuda_lib):
+    """The rising scores of test_rising_scores_rescale really move the running maximum."""
+    mv = cuda_lib
+    c = Case(1, 9, 8, [1500], seed=39, spread=0.0, q_size=6.0)
+    s = c.table[0]
+    c.kscale[s] = (c.kscale[s] * np.linspace(0.01, 6.0, len(s))).astype(np.float32)
+    mv.debug_rescale_count()
+    check(mv, c, 1)
+    assert mv.debug_rescale_count() > 0
