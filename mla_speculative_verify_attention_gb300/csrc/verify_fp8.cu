@@ -168,13 +168,71 @@ __device__ __forceinline__ uint32_t q_to_bf16(uint32_t w, float f) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ float max_abs8(const uint4& v) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    float m = 0.f;
+// N query rows, a row a warp: rows first, first + step, ..; rows past nrows are zeros.
+template <int N>
+__device__ __forceinline__ void load_q_rows(uint4 (&v)[N][3], const __nv_bfloat16* q0, int first, int step, int nrows) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
-    return m;
+    for (int u = 0; u < N; ++u) {
+        const int rr = first + u * step;
+        const uint4* src = reinterpret_cast<const uint4*>(q0 + (int64_t)rr * D_QK);
+#pragma unroll
+        for (int c = 0; c < 3; ++c)
+            v[u][c] = rr < nrows && c * 32 + lane < 72 ? __ldg(src + c * 32 + lane) : make_uint4(0, 0, 0, 0);
+    }
+}
+
+// Those rows in fp16 (the rope chunk in bf16), each divided by row_exp, the power of two that brings
+// its largest element into [2^14, 2^15): chunks below NQT to q_tmp (bound for TMEM), the others to q_s;
+// rows of 128 B, 128-byte swizzle, RQ rows a chunk.
+template <int N, int NQT>
+__device__ __forceinline__ void store_q_rows(const uint4 (&v)[N][3], uint8_t* q_s, uint8_t* q_tmp, float* row_exp,
+                                             int first, int step, int end, int RQ) {
+    const int lane = threadIdx.x & 31;
+    __nv_bfloat162 top[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        __nv_bfloat162 m[3];
+#pragma unroll
+        for (int c = 0; c < 3; ++c) {
+            const uint32_t w[4] = {v[u][c].x & 0x7fff7fffu, v[u][c].y & 0x7fff7fffu, v[u][c].z & 0x7fff7fffu,
+                                   v[u][c].w & 0x7fff7fffu};
+            const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(w);
+            m[c] = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+        }
+        top[u] = __hmax2(__hmax2(m[0], m[1]), m[2]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const uint32_t w = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<const uint32_t*>(&top[u]), o);
+            top[u] = __hmax2(top[u], *reinterpret_cast<const __nv_bfloat162*>(&w));
+        }
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        const int rr = first + u * step;
+        // exponent of the row's largest element, within what keeps both factors finite
+        const float big = fmaxf(__low2float(top[u]), __high2float(top[u]));
+        const int e = min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 127);
+        const float mul = __int_as_float((14 - e + 127) << 23);
+        if (rr >= end) continue;
+        if (lane == 0) row_exp[rr] = __int_as_float((e - 14 + 127) << 23);
+#pragma unroll
+        for (int c = 0; c < 3; ++c) {
+            const int pc = c * 32 + lane, ch = pc >> 3;
+            const uint4 x = v[u][c];
+            if (pc < 64) {
+                const uint4 o = make_uint4(q_to_f16(x.x, mul), q_to_f16(x.y, mul), q_to_f16(x.z, mul), q_to_f16(x.w, mul));
+                uint8_t* chunk = ch < NQT ? q_tmp + ch * RQ * 128 : q_s + (ch - NQT) * RQ * 128;
+                *reinterpret_cast<uint4*>(chunk + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4)) = o;
+            } else if (pc < 72) {
+                const uint4 o = make_uint4(q_to_bf16(x.x, mul), q_to_bf16(x.y, mul), q_to_bf16(x.z, mul), q_to_bf16(x.w, mul));
+                *reinterpret_cast<uint4*>(q_s + (NCHUNK - 1 - NQT) * RQ * 128 + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4)) = o;
+            }
+        }
+    }
+    fence_proxy_async_smem();                            // generic stores -> tensor-core reads
 }
 
 // NQT: latent chunks of Q in TMEM (the others, and the rope chunk, in shared memory).
@@ -237,6 +295,12 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
     tc_fence_after();
     const uint32_t tmem = *M.tmem_slot;
     const int q_col = O_COL + 4 * R;                     // Q chunk c < NQT: columns q_col + 32 c ..
+    // The query rows' conversion: rows 0-59 by the softmax warps, 60-71 by warps 2 and 3; chunks bound
+    // for TMEM pass through the last key stage.
+    const __nv_bfloat16* q0 = a.q + ((int64_t)b * rows + row0) * D_QK;
+    uint8_t* const q_tmp = smem + L.kv + (STAGES - 1) * STAGE_BYTES;
+    constexpr int Q_SOFT = 60, Q_THREADS = 128 + 64;
+    static_assert(Q_SOFT + 12 == MAX_R, "every query row has its warp");
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -302,6 +366,13 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
         }
         if (!ok && lane == 0) give_up(M, a.status);
         __syncwarp();
+        } else if (T > 0) {
+            for (int first = Q_SOFT + warp - 2; first < MAX_R; first += 6) {
+                uint4 v[3][3];
+                load_q_rows(v, q0, first, 2, nrows);
+                store_q_rows<3, NQT>(v, smem, q_tmp, M.row_exp, first, 2, RQ, RQ);
+            }
+            bar_arrive(4, Q_THREADS);
         }
     } else if (warp >= 8) {
         // ================= gather and widening: keys WK w .. WK w + 5 of every tile =================
@@ -422,50 +493,14 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
         const int r = quad * 32 + lane;                  // query row of this thread (lane of A and C)
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
         const bool row_ok = r < nrows;
-        const __nv_bfloat16* q0 = a.q + ((int64_t)b * rows + row0) * D_QK;
         if (T > 0) {
-            // a warp a row: its largest element's exponent, then the row in fp16 (bf16 for the rope
-            // chunk) to shared memory; chunks bound for TMEM by way of the last key stage
-            constexpr int QB = 9;                        // rows in flight
-            uint8_t* const q_tmp = smem + L.kv + (STAGES - 1) * STAGE_BYTES;
-            for (int rb = quad; rb < RQ; rb += 4 * QB) {
+            constexpr int QB = 8;
+            for (int first = quad; first < min(RQ, Q_SOFT); first += 4 * QB) {
                 uint4 v[QB][3];
-#pragma unroll
-                for (int u = 0; u < QB; ++u) {
-                    const int rr = rb + 4 * u;
-                    const uint4* src = reinterpret_cast<const uint4*>(q0 + (int64_t)rr * D_QK);
-#pragma unroll
-                    for (int c = 0; c < 3; ++c)
-                        v[u][c] = rr < nrows && c * 32 + lane < 72 ? __ldg(src + c * 32 + lane) : make_uint4(0, 0, 0, 0);
-                }
-#pragma unroll
-                for (int u = 0; u < QB; ++u) {
-                    const int rr = rb + 4 * u;
-                    if (rr >= RQ) break;
-                    float top = fmaxf(max_abs8(v[u][0]), fmaxf(max_abs8(v[u][1]), max_abs8(v[u][2])));
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    // exponent of the row's largest element, within what keeps both factors finite
-                    const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127);
-                    const float mul = __int_as_float((14 - e + 127) << 23);
-                    if (lane == 0) M.row_exp[rr] = __int_as_float((e - 14 + 127) << 23);
-#pragma unroll
-                    for (int c = 0; c < 3; ++c) {
-                        const int pc = c * 32 + lane, ch = pc >> 3;
-                        if (pc >= 72) continue;
-                        uint4 o;
-                        if (ch < NCHUNK - 1)
-                            o = make_uint4(q_to_f16(v[u][c].x, mul), q_to_f16(v[u][c].y, mul), q_to_f16(v[u][c].z, mul),
-                                           q_to_f16(v[u][c].w, mul));
-                        else
-                            o = make_uint4(q_to_bf16(v[u][c].x, mul), q_to_bf16(v[u][c].y, mul),
-                                           q_to_bf16(v[u][c].z, mul), q_to_bf16(v[u][c].w, mul));
-                        uint8_t* chunk = ch < NQT ? q_tmp + ch * RQ * 128 : smem + (ch - NQT) * RQ * 128;
-                        *reinterpret_cast<uint4*>(chunk + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4)) = o;
-                    }
-                }
+                load_q_rows(v, q0, first, 4, min(nrows, Q_SOFT));
+                store_q_rows<QB, NQT>(v, smem, q_tmp, M.row_exp, first, 4, min(RQ, Q_SOFT), RQ);
             }
-            bar_sync(1, 128);
+            bar_sync(4, Q_THREADS);
             // a thread a row: the TMEM chunks
             if (quad * 32 < RQ) {
 #pragma unroll 1
@@ -481,7 +516,6 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
                 }
             }
             tmem_st_wait();
-            fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&M.bars[B_Q_FULL]);
