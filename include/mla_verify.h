@@ -300,14 +300,22 @@ int mla_kv_read_fp8(const uint8_t* kv_lat, const float* kv_scale, const void* kv
  *              mla_verify_attn_packed(); at most one of them, both NULL = causal chain
  *   out        bf16 [B, q_len, H, 512], 16-byte aligned, each value rounded once from fp32
  *   lse        fp32 [B, q_len, H]
- * Every other argument, limit, workspace size and device status is that of mla_verify_attn().
- * q_len = 1 is plain decode.
+ * Every other argument, limit and device status is that of mla_verify_attn().  An explicit nsplit needs
+ * the workspace that it needs there; nsplit = 0 uses what mla_verify_fp8_workspace_bytes() says, and
+ * works with less (fewer splits).  q_len = 1 is plain decode.
  */
 int mla_verify_attn_fp8(const void* q, const uint8_t* kv_lat, const float* kv_scale, const void* kv_rope,
                         int64_t n_pool, const int32_t* slot_table, int slot_stride, const int32_t* seq_lens,
                         const uint8_t* draft_mask, const uint64_t* draft_mask_bits, int B, int q_len, int H,
                         float scale, void* out, float* lse, int nsplit, void* workspace, size_t ws_bytes,
                         mla_stream_t stream);
+
+/*
+ * Bytes of workspace with which mla_verify_attn_fp8() with nsplit = 0 splits the keys as finely as it
+ * wants to (max_seq = slot_stride; num_sms of the device).  Pure host function; 0 where an argument
+ * is out of range, or where it does not split.
+ */
+size_t mla_verify_fp8_workspace_bytes(int B, int q_len, int H, int max_seq, int num_sms);
 
 /*
  * Acceptance of drafted tokens from given random numbers, the step after a verify pass:

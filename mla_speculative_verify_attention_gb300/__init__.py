@@ -36,7 +36,7 @@ EXPORTS = ("mla_verify_workspace_bytes", "mla_verify_auto_nsplit", "mla_verify_a
            "mla_status_string", "mla_verify_version", "mla_verify_attn_static_scratch",
            "mla_sparse_fp8_decode", "mla_sparse_fp8_partials", "mla_verify_attn_packed", "mla_kv_append", "mla_kv_append_fp8",
            "mla_debug_stall_next_launch", "mla_debug_rescale_count", "mla_qk_norm_rope", "mla_kv_append_quant",
-           "mla_kv_read_fp8", "mla_verify_attn_fp8", "mla_draft_verify")
+           "mla_kv_read_fp8", "mla_verify_attn_fp8", "mla_draft_verify", "mla_verify_fp8_workspace_bytes")
 STATIC_SCRATCH_BYTES = 64 << 20
 
 _lib = None
@@ -90,6 +90,8 @@ def load():
     L.mla_kv_read_fp8.restype = I
     L.mla_verify_attn_fp8.argtypes = [P, P, P, P, I64, P, I, P, P, P, I, I, I, F, P, P, I, P, SZ, P]
     L.mla_verify_attn_fp8.restype = I
+    L.mla_verify_fp8_workspace_bytes.argtypes = [I, I, I, I, I]
+    L.mla_verify_fp8_workspace_bytes.restype = SZ
     L.mla_draft_verify.argtypes = [P, P, P, P, P, P, I, I, I, P, P, P, P]
     L.mla_draft_verify.restype = I
     L.mla_verify_combine.argtypes = [P, P, I, I, I, I, P, P, P]
@@ -520,6 +522,12 @@ def kv_read_fp8(kv_lat: torch.Tensor, kv_scale: torch.Tensor, kv_rope: torch.Ten
     return out
 
 
+def verify_fp8_workspace_bytes(B: int, q_len: int, H: int, max_seq: int, num_sms: int) -> int:
+    """Bytes of workspace with which verify_attn_fp8 with nsplit = 0 splits as finely as it wants to
+    (max_seq: the slot table's row length)."""
+    return int(load().mla_verify_fp8_workspace_bytes(B, q_len, H, max_seq, num_sms))
+
+
 def verify_attn_fp8(q: torch.Tensor, kv_lat: torch.Tensor, kv_scale: torch.Tensor, kv_rope: torch.Tensor,
                     slot_table: torch.Tensor, seq_lens: torch.Tensor, draft_mask: Optional[torch.Tensor],
                     scale: float, *, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
@@ -527,7 +535,8 @@ def verify_attn_fp8(q: torch.Tensor, kv_lat: torch.Tensor, kv_scale: torch.Tenso
                     stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """mla_verify_attn_fp8: verify_attn over the fp8 cache of kv_append_quant; out bf16
     [B, q_len, H, 512] and lse fp32 [B, q_len, H].  ``draft_mask`` is uint8 [B, q_len, q_len],
-    bit-packed int64 [B, q_len], or None (causal chain); ``workspace`` as for verify_attn."""
+    bit-packed int64 [B, q_len], or None (causal chain); ``workspace`` is a byte (uint8) CUDA
+    tensor, allocated here when omitted (verify_fp8_workspace_bytes)."""
     _want_dims("q", q, torch.bfloat16, 4, D_QK)
     B, q_len, H, _ = q.shape
     n_pool = _want_fp8_cache(kv_lat, kv_scale, kv_rope)
@@ -557,8 +566,9 @@ def verify_attn_fp8(q: torch.Tensor, kv_lat: torch.Tensor, kv_scale: torch.Tenso
         if lse is None:
             lse = _empty(q, (B, q_len, H), torch.float32, stream)
         if workspace is None:
-            ns = nsplit if nsplit > 0 else auto_nsplit(B, q_len, H, stride, num_sms(dev), 1 << 62)
-            workspace = _empty(q, (max(workspace_bytes(B, q_len, H, ns), 256),), torch.uint8, stream)
+            need = workspace_bytes(B, q_len, H, nsplit) if nsplit > 0 else verify_fp8_workspace_bytes(
+                B, q_len, H, stride, num_sms(dev))
+            workspace = _empty(q, (max(need, 256),), torch.uint8, stream)
         _check("mla_verify_attn_fp8", _call("mla_verify_attn_fp8")(
             q.data_ptr(), kv_lat.data_ptr(), kv_scale.data_ptr(), kv_rope.data_ptr(), n_pool, slot_table.data_ptr(),
             stride, seq_lens.data_ptr(), mask, bits, B, q_len, H, float(scale), out.data_ptr(), lse.data_ptr(), nsplit,

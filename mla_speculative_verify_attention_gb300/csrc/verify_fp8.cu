@@ -14,8 +14,8 @@
 // maximum may lag by 2^8 before O is rescaled); P's rounding is relative 2^-12.  Scales below
 // 2^-90 (rows of zeros) count as 2^-90 in the weight.
 //
-// One CTA handles up to 72 query rows (r = t * H + h of one stream) over one key split, in
-// tiles of 48 keys:
+// One CTA handles up to 72 (in one form 96) query rows (r = t * H + h of one stream) over one key
+// split, in tiles of 48 keys:
 //   gather   eight warps read the tile's raw rows (512 code bytes, 128 rope bytes, scale) from
 //            the slot table straight into registers, two tiles ahead, and widen them
 //            (e4m3x2 -> f16x2, one instruction a pair) into a 128-byte-swizzled stage
@@ -34,9 +34,9 @@
 // any widening (keys as rows of the scores, Q in two e4m3 pieces, P in three; half of the
 // shared-memory traffic, but only one tile of 128 keys fits, and scores, P and values follow each
 // other: 79 us, and 26 instead of 17 us at one tile a CTA, whose code is three times as long); rows
-// called into L2 four tiles ahead (80 us).
-// With few keys: the chain of cold reads (length, slots, rows; queries), the first pass through the
-// code and the epilogue's partial rows: 15.7 us a call at one tile a CTA and 72 rows.
+// called into L2 four tiles ahead (80 us).  Partial rows in fp16: within 2 us either way.
+// With few keys: the chain of first reads (length, slots, rows), the queries' conversion, the first pass
+// through the code and the epilogue's partial rows: 15.0 us a call at one tile a CTA and 72 rows.
 //
 // Warps (512 threads): 0 issues A and C, 1 issues O^T (whole warp, one elected lane), 4-7 Q,
 // softmax and epilogue (TMEM lane quadrant = warp % 4), 8-15 gather and widening (six keys of
@@ -60,11 +60,12 @@ namespace {
 using namespace tc;
 
 constexpr int NK = 48;                               // keys per tile
-constexpr int MAX_R = 72;                            // query rows per CTA
+constexpr int MAX_R = 96;                            // query rows per CTA: 72 beside three key stages,
+constexpr int MAX_R3 = 72;                           // 96 beside two
 constexpr int NT = 512;
 constexpr int WIDE_WARPS = 8;
 constexpr int WK = NK / WIDE_WARPS;                  // keys of a tile per gather warp
-constexpr int STAGES = 3;
+constexpr int MAX_STAGES = 3;
 constexpr int NCHUNK = D_QK / 64;                    // 8 latent chunks and the rope chunk
 constexpr int REGION = NK * 128;                     // one 64-dim chunk of a stage
 constexpr int STAGE_BYTES = NCHUNK * REGION;         // 55296 B
@@ -77,7 +78,7 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr int MAX_SMEM = 232448;                     // opt-in shared memory per block on sm_103
 
-enum { B_KV_FULL = 0, B_KV_EMPTY = B_KV_FULL + STAGES, B_S_FULL = B_KV_EMPTY + STAGES, B_S_FREE, B_P_FULL, B_Q_FULL,
+enum { B_KV_FULL = 0, B_KV_EMPTY = B_KV_FULL + MAX_STAGES, B_S_FULL = B_KV_EMPTY + MAX_STAGES, B_S_FREE, B_P_FULL, B_Q_FULL,
        B_COUNT };
 constexpr int BAR_BYTES = 128;
 static_assert(B_COUNT * 8 <= BAR_BYTES, "barrier area");
@@ -87,12 +88,12 @@ struct Layout {
 };
 // RQ: rows of a Q chunk (whole groups of eight).  The MMA reads 128 rows a chunk: what lies
 // behind the last, in the next chunk or the key stages, gives scores that nobody uses.
-__host__ __device__ inline Layout layout_for(int R, int RQ, int nq_s) {
+__host__ __device__ inline Layout layout_for(int R, int RQ, int nq_s, int stages) {
     Layout L;
     L.kv = (nq_s * RQ * 128 + 1023) / 1024 * 1024;
-    L.p = L.kv + STAGES * STAGE_BYTES;
+    L.p = L.kv + stages * STAGE_BYTES;
     L.misc = (L.p + R * NK * 2 + 127) / 128 * 128;
-    L.total = L.misc + BAR_BYTES + 128 + STAGES * NK * 12 + 512 + 512;
+    L.total = L.misc + BAR_BYTES + 128 + MAX_STAGES * NK * 12 + 512 + 512;
     return L;
 }
 
@@ -125,8 +126,8 @@ struct Misc {
     uint64_t* bars;
     uint32_t* tmem_slot;
     volatile int* abort;
-    float2* key_sl;               // [STAGES][NK]: scale (NaN: the key holds a NaN), log2 of the clamped scale
-    float* key_inv;               // [STAGES][NK]: 1 / clamped scale (finite: a masked key's P of 0 stays 0)
+    float2* key_sl;               // [stage][NK]: scale (NaN: the key holds a NaN), log2 of the clamped scale
+    float* key_inv;               // [stage][NK]: 1 / clamped scale (finite: a masked key's P of 0 stays 0)
     float* row_f;                 // [128]: alpha while the loop runs, 1 / l in the epilogue
     float* row_exp;               // [128]: the power of two that a query row was divided by
 };
@@ -136,8 +137,8 @@ __device__ __forceinline__ Misc misc_at(uint8_t* smem, int off) {
     m.tmem_slot = reinterpret_cast<uint32_t*>(smem + off + BAR_BYTES);
     m.abort = reinterpret_cast<volatile int*>(smem + off + BAR_BYTES + 4);
     m.key_sl = reinterpret_cast<float2*>(smem + off + BAR_BYTES + 128);
-    m.key_inv = reinterpret_cast<float*>(smem + off + BAR_BYTES + 128 + STAGES * NK * 8);
-    m.row_f = reinterpret_cast<float*>(smem + off + BAR_BYTES + 128 + STAGES * NK * 12);
+    m.key_inv = reinterpret_cast<float*>(smem + off + BAR_BYTES + 128 + MAX_STAGES * NK * 8);
+    m.row_f = reinterpret_cast<float*>(smem + off + BAR_BYTES + 128 + MAX_STAGES * NK * 12);
     m.row_exp = m.row_f + 128;
     return m;
 }
@@ -235,14 +236,14 @@ __device__ __forceinline__ void store_q_rows(const uint4 (&v)[N][3], uint8_t* q_
     fence_proxy_async_smem();                            // generic stores -> tensor-core reads
 }
 
-// NQT: latent chunks of Q in TMEM (the others, and the rope chunk, in shared memory).
-template <int NQT>
+// NQT: latent chunks of Q in TMEM (the others, and the rope chunk, in shared memory); STAGES: key stages.
+template <int NQT, int STAGES>
 __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
     constexpr int NQS = NCHUNK - NQT;
     extern __shared__ __align__(1024) uint8_t smem[];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int R = a.R, RQ = a.RQ;
-    const Layout L = layout_for(R, RQ, NQS);
+    const Layout L = layout_for(R, RQ, NQS, STAGES);
     const Misc M = misc_at(smem, L.misc);
     const uint32_t q_addr = smem_u32(smem), kv_addr = smem_u32(smem + L.kv), p_addr = smem_u32(smem + L.p);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -295,12 +296,11 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
     tc_fence_after();
     const uint32_t tmem = *M.tmem_slot;
     const int q_col = O_COL + 4 * R;                     // Q chunk c < NQT: columns q_col + 32 c ..
-    // The query rows' conversion: rows 0-59 by the softmax warps, 60-71 by warps 2 and 3; chunks bound
-    // for TMEM pass through the last key stage.
+    // The query rows' conversion: by the softmax warps, the last sixth of the rows by warps 2 and 3;
+    // chunks bound for TMEM pass through the last key stage.
     const __nv_bfloat16* q0 = a.q + ((int64_t)b * rows + row0) * D_QK;
     uint8_t* const q_tmp = smem + L.kv + (STAGES - 1) * STAGE_BYTES;
-    constexpr int Q_SOFT = 60, Q_THREADS = 128 + 64;
-    static_assert(Q_SOFT + 12 == MAX_R, "every query row has its warp");
+    constexpr int Q_ROWS = STAGES == 3 ? MAX_R3 : MAX_R, Q_SOFT = Q_ROWS / 6 * 5, Q_THREADS = 128 + 64;
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
         if (!ok && lane == 0) give_up(M, a.status);
         __syncwarp();
         } else if (T > 0) {
-            for (int first = Q_SOFT + warp - 2; first < MAX_R; first += 6) {
+            for (int first = Q_SOFT + warp - 2; first < min(RQ, Q_ROWS); first += 6) {
                 uint4 v[3][3];
                 load_q_rows(v, q0, first, 2, nrows);
                 store_q_rows<3, NQT>(v, smem, q_tmp, M.row_exp, first, 2, RQ, RQ);
@@ -704,31 +704,63 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
     }
 }
 
-template <int NQT>
+template <int NQT, int STAGES>
 cudaError_t launch_one(const Fp8Args& a, dim3 grid, int dev, cudaStream_t stream) {
-    if (NQT * a.RQ * 128 > STAGE_BYTES) return cudaErrorInvalidConfiguration;   // the TMEM chunks' way station
+    auto* k = verify_fp8_kernel<NQT, STAGES>;
+    const int smem = layout_for(a.R, a.RQ, NCHUNK - NQT, STAGES).total;
+    if (a.RQ > (STAGES == 3 ? MAX_R3 : MAX_R) || smem > MAX_SMEM || O_COL + 4 * a.R + 32 * NQT > (int)TMEM_COLS ||
+        NQT * a.RQ * 128 > STAGE_BYTES)                  // (the TMEM chunks' way station)
+        return cudaErrorInvalidConfiguration;
     static bool attr_set[64];
     if (!attr_set[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(verify_fp8_kernel<NQT>, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
+        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
         if (e != cudaSuccess) return e;
         // the warpgroups' shares have to be in the launch's registers, or their request would wait for ever
         cudaFuncAttributes at;
-        e = cudaFuncGetAttributes(&at, verify_fp8_kernel<NQT>);
+        e = cudaFuncGetAttributes(&at, k);
         if (e != cudaSuccess) return e;
         if (at.numRegs * NT < 128 * (72 + 168 + 2 * 136)) return cudaErrorInvalidConfiguration;
         attr_set[dev] = true;
     }
-    const int smem = layout_for(a.R, a.RQ, NCHUNK - NQT).total;
-    if (smem > MAX_SMEM || O_COL + 4 * a.R + 32 * NQT > (int)TMEM_COLS) return cudaErrorInvalidConfiguration;
-    return launch_dependent(verify_fp8_kernel<NQT>, grid, dim3(NT), (size_t)smem, stream, a);
+    return launch_dependent(k, grid, dim3(NT), (size_t)smem, stream, a);
 }
 
-// As many Q chunks in TMEM as fit beside the scores and O^T: 3 at 80 MMA rows, 5 up to 64, 7 up to 48.
+// Row tiles of a stream: of up to 72 rows beside three key stages; 73 to 96 rows are one tile beside
+// two (measured, sixteen streams of 80 rows and 3000 keys: 41.1 us, as two tiles of 40 rows 49.4).  With
+// more rows the fewer and larger tiles cost as much as they save (one stream of 576 rows and 4105 keys: six
+// tiles of 96 rows 26.8 us, eight of 72 25.6).
+void fp8_tiling(int rows, int* n_tiles, int* R_step, int* R) {
+    tc_tiling(rows, MAX_R, n_tiles, R_step, R);
+    int n3, step3, r3;
+    tc_tiling(rows, MAX_R3, &n3, &step3, &r3);
+    if (n3 < 2 * *n_tiles) { *n_tiles = n3; *R_step = step3; *R = r3; }
+}
+
+// The automatic split count of a uniform call: one wave of CTAs (two for several streams, whose
+// lengths may differ), a tile a split at least: the longest stream's keys in whole tiles, without
+// splits that a full row would leave empty (measured, one stream of nine drafts and eight heads, 265
+// keys: 3 splits of two tiles 16.6 us, 6 of one 15.0; 1009 keys: 8 splits 18.8 us, 22 splits 16.2).
+int fp8_auto_nsplit(int B, int n_tiles, int max_seq, int num_sms) {
+    long long per = (long long)num_sms * (B > 1 ? 2 : 1) / ((long long)B * n_tiles);
+    per = max(per, 1ll);
+    const long long keys = ((max_seq + per - 1) / per + NK - 1) / NK * NK;
+    return (int)max(min((max_seq + keys - 1) / keys, (long long)MLA_MAX_NSPLIT), 1ll);
+}
+
+// Split slots of the balanced split of B streams (0: not taken).
+int fp8_balanced_slots(int B, int n_tiles, int num_sms) {
+    const int slots = num_sms / n_tiles;
+    return B >= 2 && B <= BALANCED_MAX_STREAMS && slots - B >= B ? slots : 0;
+}
+
+// As many Q chunks in TMEM as fit beside the scores and O^T: 1 at 96 MMA rows, 3 at 80, 5 up to 64, 7 up to 48.
 cudaError_t launch_verify_fp8(const Fp8Args& a, int n_tiles, int dev, cudaStream_t stream) {
     const dim3 grid(a.nsplit, n_tiles, a.balanced ? 1 : a.B);
-    if (a.R <= 48) return launch_one<7>(a, grid, dev, stream);
-    if (a.R <= 64) return launch_one<5>(a, grid, dev, stream);
-    return launch_one<3>(a, grid, dev, stream);
+    if (a.R <= 48) return launch_one<7, 3>(a, grid, dev, stream);
+    if (a.R <= 64) return launch_one<5, 3>(a, grid, dev, stream);
+    if (a.RQ <= MAX_R3) return launch_one<3, 3>(a, grid, dev, stream);
+    if (a.R <= 80) return launch_one<3, 2>(a, grid, dev, stream);
+    return launch_one<1, 2>(a, grid, dev, stream);
 }
 
 }  // namespace
@@ -758,7 +790,7 @@ extern "C" int mla_verify_attn_fp8(const void* q, const uint8_t* kv_lat, const f
     int rc = device_state(&dev, &a.status, &num_sms, &a.rescales);
     if (rc != MLA_OK) return rc;
     int n_tiles;
-    tc_tiling(q_len * H, MAX_R, &n_tiles, &a.R_step, &a.R);
+    fp8_tiling(q_len * H, &n_tiles, &a.R_step, &a.R);
     a.RQ = (a.R_step + 7) / 8 * 8;
     const long long per_stream = (long long)q_len * H, rows = B * per_stream;
     a.q = static_cast<const __nv_bfloat16*>(q);
@@ -769,14 +801,14 @@ extern "C" int mla_verify_attn_fp8(const void* q, const uint8_t* kv_lat, const f
     a.out = static_cast<__nv_bfloat16*>(out); a.lse = lse;
     a.debug_stall = take_debug_stall() ? 1 : 0;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (nsplit == 0 && B >= 2 && B <= BALANCED_MAX_STREAMS && workspace && aligned(workspace, 256)) {
+    const int slots = nsplit == 0 && workspace && aligned(workspace, 256) ? fp8_balanced_slots(B, n_tiles, num_sms) : 0;
+    if (slots) {
         // streams of unequal length: all their keys in equal chunks over one wave of CTAs
-        const long long slots = num_sms / n_tiles;
         const size_t out_b = align256((size_t)slots * per_stream * D_V * 4);
-        if (slots - B >= B && out_b + align256((size_t)slots * per_stream * 4) <= ws_bytes) {
+        if (out_b + align256((size_t)slots * per_stream * 4) <= ws_bytes) {
             a.balanced = 1;
-            a.bal_G = (int)(slots - B);
-            a.nsplit = (int)slots;
+            a.bal_G = slots - B;
+            a.nsplit = slots;
             a.part_out = static_cast<float*>(workspace);
             a.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + out_b);
             if (launch_verify_fp8(a, n_tiles, dev, st) != cudaSuccess) return MLA_ERR_LAUNCH;
@@ -790,17 +822,8 @@ extern "C" int mla_verify_attn_fp8(const void* q, const uint8_t* kv_lat, const f
     }
     int ns = nsplit;
     if (ns == 0) {
-        // one wave of CTAs (two for several streams, whose lengths may differ), a tile a split at least:
-        // the longest stream's keys in whole tiles, without splits that a full row would leave empty
-        // (measured, one stream of nine drafts and eight heads, 265 keys: 3 splits of two tiles 16.6 us,
-        // 6 of one 15.0; 1009 keys: 8 splits 18.8 us, 22 splits 16.2)
-        long long per = (long long)num_sms * (B > 1 ? 2 : 1) / ((long long)B * n_tiles);
-        per = max(per, 1ll);
-        const long long keys = ((slot_stride + per - 1) / per + NK - 1) / NK * NK;
-        per = (slot_stride + keys - 1) / keys;
-        per = max(min(per, (long long)MLA_MAX_NSPLIT), 1ll);
-        while (per > 1 && mla_verify_workspace_bytes(B, q_len, H, (int)per) > (workspace ? ws_bytes : 0)) --per;
-        ns = (int)per;
+        ns = fp8_auto_nsplit(B, n_tiles, slot_stride, num_sms);
+        while (ns > 1 && mla_verify_workspace_bytes(B, q_len, H, ns) > (workspace ? ws_bytes : 0)) --ns;
     }
     a.nsplit = ns;
     if (ns > 1) {
@@ -813,4 +836,14 @@ extern "C" int mla_verify_attn_fp8(const void* q, const uint8_t* kv_lat, const f
     if (ns > 1 && launch_combine_bf16(a.part_out, a.part_lse, rows, ns, a.out, lse, st) != cudaSuccess)
         return MLA_ERR_LAUNCH;
     return MLA_OK;
+}
+
+extern "C" size_t mla_verify_fp8_workspace_bytes(int B, int q_len, int H, int max_seq, int num_sms) {
+    if (B <= 0 || q_len < 1 || q_len > MLA_MAX_Q_LEN || H < 1 || H > MLA_MAX_HEADS || max_seq < 1 || num_sms < 1) return 0;
+    int n_tiles, R_step, R;
+    fp8_tiling(q_len * H, &n_tiles, &R_step, &R);
+    const size_t uniform = mla_verify_workspace_bytes(B, q_len, H, fp8_auto_nsplit(B, n_tiles, max_seq, num_sms));
+    const size_t slot_rows = (size_t)fp8_balanced_slots(B, n_tiles, num_sms) * q_len * H;
+    const size_t balanced = align256(slot_rows * D_V * 4) + align256(slot_rows * 4);
+    return balanced ? balanced : uniform;
 }

@@ -85,6 +85,9 @@ SHAPES = [  # B, q_len, H, prefixes, mask
     (1, 9, 64, [500], "tree"), (2, 1, 128, [129, 700], "none"), (4, 2, 20, [10, 300, 77, 0], "random"),
     (1, 64, 4, [200], "packed"), (2, 33, 5, [95, 33], "tree"), (5, 1, 64, [64, 1, 200, 33, 96], "chain"),
     (1, 17, 8, [1000], "random"), (1, 10, 8, [2100], "chain"), (1, 1, 80, [400], "chain"), (1, 1, 81, [90], "chain"),
+    # row tiles beside two key stages: 73 to 96 rows, and two or three tiles of them
+    (1, 1, 73, [300], "chain"), (2, 12, 8, [500, 96], "tree"), (1, 1, 89, [48], "chain"), (1, 10, 16, [700], "packed"),
+    (2, 19, 10, [200, 49], "tree"), (1, 9, 64, [47], "random"),
 ]
 
 

@@ -66,6 +66,21 @@ def test_verify_fp8_refusals(lib):
     assert f(B=0, q=None) == 0
 
 
+def test_verify_fp8_workspace(lib):
+    """What the automatic call wants: zero for bad arguments or one split, no more than a wave of splits
+    otherwise, and never more than the largest split count's."""
+    f = lib.mla_verify_fp8_workspace_bytes
+    f.argtypes, f.restype = [ctypes.c_int] * 5, ctypes.c_size_t
+    ws = lib.mla_verify_workspace_bytes
+    assert f(0, 9, 8, 100, 152) == f(1, 0, 8, 100, 152) == f(1, 65, 8, 100, 152) == f(1, 9, 129, 100, 152) == 0
+    assert f(1, 9, 8, 0, 152) == f(1, 9, 8, 100, 0) == 0
+    assert f(1, 9, 8, 48, 152) == 0 and f(1, 9, 8, 49, 152) == ws(1, 9, 8, 2)      # a tile of 48 keys a split
+    assert f(1, 9, 8, 265, 152) == ws(1, 9, 8, 6)
+    assert f(1, 9, 8, 1 << 20, 152) == ws(1, 9, 8, 152) and f(1, 9, 64, 1 << 20, 152) == ws(1, 9, 64, 19)
+    assert f(8, 9, 8, 46089, 152) == ws(1, 9, 8, 152)                              # one wave of slots, all streams
+    assert f(200, 1, 8, 4000, 152) == ws(200, 1, 8, 1) == 0
+
+
 def test_draft_verify_refusals(lib):
     f = caller(lib, "mla_draft_verify", p=16, q=16, tok=16, par=16, u=16, un=16, B=2, q_len=9, V=100, n=16, out=16, path=16,
                st=None)
