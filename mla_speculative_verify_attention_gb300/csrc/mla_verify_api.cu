@@ -206,12 +206,14 @@ cudaError_t launch_combine_z(const float* part_out, const float* part_lse, long 
 // Z: warps per item, from the split count (up to 16 splits per warp, 8 warps at most;
 // balanced partials: a stream holds at most all slots, typically a few dozen; two warps
 // per item keep the grid near one wave (measured on c4: 4 warps 60.2 us per call, 2 warps
-// 58.3, 1 warp 58.1)).
+// 58.3, 1 warp 58.1); one beside a bf16 output, whose streams are often short of splits
+// (32 streams of 64 rows, five splits each: 2 warps 44.5 us per call, 1 warp 38.9; eight
+// streams of 19 splits 75.7 and 75.9)).
 template <typename Out>
 cudaError_t launch_combine_any(const float* part_out, const float* part_lse, long long n_rows, int S, Out* out,
                                float* lse, const CombineBalanced& bal, cudaStream_t stream) {
     if (n_rows <= 0) return cudaSuccess;
-    const int per = bal.on ? 2 * 16 : S;
+    const int per = bal.on ? (sizeof(Out) == 4 ? 2 : 1) * 16 : S;
     if (per <= 16) return launch_combine_z<1>(part_out, part_lse, n_rows, S, out, lse, bal, stream);
     if (per <= 32) return launch_combine_z<2>(part_out, part_lse, n_rows, S, out, lse, bal, stream);
     if (per <= 64) return launch_combine_z<4>(part_out, part_lse, n_rows, S, out, lse, bal, stream);

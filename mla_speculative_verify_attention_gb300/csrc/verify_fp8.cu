@@ -736,15 +736,24 @@ void fp8_tiling(int rows, int* n_tiles, int* R_step, int* R) {
     if (n3 < 2 * *n_tiles) { *n_tiles = n3; *R_step = step3; *R = r3; }
 }
 
-// The automatic split count of a uniform call: one wave of CTAs (two for several streams, whose
-// lengths may differ), a tile a split at least: the longest stream's keys in whole tiles, without
-// splits that a full row would leave empty (measured, one stream of nine drafts and eight heads, 265
-// keys: 3 splits of two tiles 16.6 us, 6 of one 15.0; 1009 keys: 8 splits 18.8 us, 22 splits 16.2).
-int fp8_auto_nsplit(int B, int n_tiles, int max_seq, int num_sms) {
-    long long per = (long long)num_sms * (B > 1 ? 2 : 1) / ((long long)B * n_tiles);
-    per = max(per, 1ll);
-    const long long keys = ((max_seq + per - 1) / per + NK - 1) / NK * NK;
-    return (int)max(min((max_seq + keys - 1) / keys, (long long)MLA_MAX_NSPLIT), 1ll);
+// The automatic split count of a uniform call: the least of
+//     waves of CTAs x (start and epilogue of a CTA + its tiles) + the merge
+// over the counts from one to a tile a split, the longest stream's keys in whole tiles.  The times (ns)
+// are measured: a CTA of 16 rows starts and ends in 6 us and takes 1.6 us a tile, one of 72 rows 10 and
+// 1.8; the merge 3 us.  (One stream of 72 rows: 265 keys, six splits of a tile 15.0 us, three of two
+// 16.6, one of six 20.2; 64 streams of 128 rows and 2000 keys: one split 95 us, two 120.)
+int fp8_auto_nsplit(int B, int n_tiles, int R, int max_seq, int num_sms) {
+    const long long fixed = 5000 + 70 * R, tile = 1500 + 5 * R, merge = 3000;
+    const long long tiles = ((long long)max_seq + NK - 1) / NK;
+    const long long most = min(min(tiles, (long long)MLA_MAX_NSPLIT), 8ll * num_sms / ((long long)B * n_tiles) + 1);
+    long long best = 1, best_cost = 0;
+    for (long long want = 1; want <= most; ++want) {
+        const long long per_cta = (tiles + want - 1) / want, ns = (tiles + per_cta - 1) / per_cta;   // none empty
+        const long long waves = ((long long)B * n_tiles * ns + num_sms - 1) / num_sms;
+        const long long cost = waves * (fixed + per_cta * tile) + (ns > 1 ? merge : 0);
+        if (want == 1 || cost < best_cost) { best = ns; best_cost = cost; }
+    }
+    return (int)best;
 }
 
 // Split slots of the balanced split of B streams (0: not taken).
@@ -822,7 +831,7 @@ extern "C" int mla_verify_attn_fp8(const void* q, const uint8_t* kv_lat, const f
     }
     int ns = nsplit;
     if (ns == 0) {
-        ns = fp8_auto_nsplit(B, n_tiles, slot_stride, num_sms);
+        ns = fp8_auto_nsplit(B, n_tiles, a.R, slot_stride, num_sms);
         while (ns > 1 && mla_verify_workspace_bytes(B, q_len, H, ns) > (workspace ? ws_bytes : 0)) --ns;
     }
     a.nsplit = ns;
@@ -842,7 +851,7 @@ extern "C" size_t mla_verify_fp8_workspace_bytes(int B, int q_len, int H, int ma
     if (B <= 0 || q_len < 1 || q_len > MLA_MAX_Q_LEN || H < 1 || H > MLA_MAX_HEADS || max_seq < 1 || num_sms < 1) return 0;
     int n_tiles, R_step, R;
     fp8_tiling(q_len * H, &n_tiles, &R_step, &R);
-    const size_t uniform = mla_verify_workspace_bytes(B, q_len, H, fp8_auto_nsplit(B, n_tiles, max_seq, num_sms));
+    const size_t uniform = mla_verify_workspace_bytes(B, q_len, H, fp8_auto_nsplit(B, n_tiles, R, max_seq, num_sms));
     const size_t slot_rows = (size_t)fp8_balanced_slots(B, n_tiles, num_sms) * q_len * H;
     const size_t balanced = align256(slot_rows * D_V * 4) + align256(slot_rows * 4);
     return balanced ? balanced : uniform;

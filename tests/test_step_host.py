@@ -74,11 +74,13 @@ def test_verify_fp8_workspace(lib):
     ws = lib.mla_verify_workspace_bytes
     assert f(0, 9, 8, 100, 152) == f(1, 0, 8, 100, 152) == f(1, 65, 8, 100, 152) == f(1, 9, 129, 100, 152) == 0
     assert f(1, 9, 8, 0, 152) == f(1, 9, 8, 100, 0) == 0
-    assert f(1, 9, 8, 48, 152) == 0 and f(1, 9, 8, 49, 152) == ws(1, 9, 8, 2)      # a tile of 48 keys a split
-    assert f(1, 9, 8, 265, 152) == ws(1, 9, 8, 6)
+    assert f(1, 9, 8, 48, 152) == 0                                                # one tile, one split
+    assert f(1, 9, 8, 265, 152) == ws(1, 9, 8, 6)                                  # a tile of 48 keys a split
     assert f(1, 9, 8, 1 << 20, 152) == ws(1, 9, 8, 152) and f(1, 9, 64, 1 << 20, 152) == ws(1, 9, 64, 19)
     assert f(8, 9, 8, 46089, 152) == ws(1, 9, 8, 152)                              # one wave of slots, all streams
-    assert f(200, 1, 8, 4000, 152) == ws(200, 1, 8, 1) == 0
+    assert f(128, 1, 16, 1000, 152) == 0                                           # nearly a wave of whole streams
+    for args in [(200, 1, 8, 4000, 152), (65535, 64, 128, 1 << 30, 152), (1, 64, 128, 5000, 152), (1, 1, 1, (1 << 31) - 1, 1)]:
+        assert f(*args) <= ws(*args[:3], 1024)
 
 
 def test_draft_verify_refusals(lib):
