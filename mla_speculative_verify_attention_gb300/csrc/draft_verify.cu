@@ -67,9 +67,22 @@ struct Coef {
     float ah, al;
 };
 
-// max(p - A q, 0) in units of 2^-45.
+// Adding 1.5 * 2^23 rounds to an integer and leaves it in the low mantissa bits.
+constexpr float MAGIC = 12582912.f;
+constexpr unsigned MAGIC_BITS = 0x4B400000u;
+
+// A sum of up to 256 residuals in units of 2^-45: their leading parts, in units of 2^-22, and what
+// is left of them, each at most 2^22 and taken up as the float's bits (one 32-bit addition).
+struct Few {
+    unsigned hi, lo;
+    __device__ __forceinline__ long long sum(int n) const {
+        return (long long)(int)(hi - n * MAGIC_BITS) * 8388608ll + (int)(lo - n * MAGIC_BITS);
+    }
+};
+
+// Adds max(p - A q, 0).
 template <int FORM>
-__device__ __forceinline__ long long residual(float p, float q, const Coef& c) {
+__device__ __forceinline__ void add_residual(float p, float q, const Coef& c, Few& few) {
     // p - A q = d + e, e the rounding errors of the product and of the difference (where d > 0)
     // (explicit roundings: a contracted multiply-add would lose the errors' meaning)
     float d = p, e = 0.f;
@@ -85,13 +98,19 @@ __device__ __forceinline__ long long residual(float p, float q, const Coef& c) {
     const bool some = FORM == FROM_P || d + e > 0.f;
     d = some ? d : 0.f;
     e = some ? e : 0.f;
-    // adding 1.5 * 2^23 rounds to an integer and leaves it in the low mantissa bits
-    constexpr float MAGIC = 12582912.f;
     const float th = fmaf(d, 4194304.f, MAGIC);                               // d * 2^22
     const float hi = th - MAGIC;
     const float rem = fmaf(hi, -2.384185791015625e-07f, d) + e;               // |rem| <= 2^-23
     const float tl = fmaf(rem, 35184372088832.f, MAGIC);                      // rem * 2^45
-    return (long long)(__float_as_int(th) - 0x4B400000) * 8388608ll + (__float_as_int(tl) - 0x4B400000);
+    few.hi += __float_as_uint(th);
+    few.lo += __float_as_uint(tl);
+}
+
+template <int FORM>
+__device__ __forceinline__ long long residual(float p, float q, const Coef& c) {
+    Few few = {0, 0};
+    add_residual<FORM>(p, q, c, few);
+    return few.sum(1);
 }
 
 // A residual row: p and q of the current node.  Positions k run over whole vectors of four that
@@ -117,18 +136,28 @@ template <int FORM>
 __device__ __forceinline__ long long sum_row(const Row& r, const Coef& c, int lo, int hi, int step) {
     long long sum = 0;
     const int end = min(hi, r.V + r.shift);
-    for (int k = lo; k < end; k += DV_BATCH * step) {
-        float p[DV_BATCH][4], q[DV_BATCH][4];
+    float p[DV_BATCH][4], q[DV_BATCH][4], pn[DV_BATCH][4], qn[DV_BATCH][4];
+    auto load = [&](int k, float (&p)[DV_BATCH][4], float (&q)[DV_BATCH][4]) {
 #pragma unroll
         for (int u = 0; u < DV_BATCH; ++u) {
             const int x = k + u * step < end ? k + u * step - r.shift : r.V;   // past the end: all zero
             load4(r.p, x, r.V, p[u]);
             if (FORM != FROM_P) load4(r.q, x, r.V, q[u]);
         }
+    };
+    load(lo, p, q);
+    for (int k = lo; k < end; k += DV_BATCH * step) {
+        load(k + DV_BATCH * step, pn, qn);
+        Few few = {0, 0};
 #pragma unroll
         for (int u = 0; u < DV_BATCH; ++u)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sum += residual<FORM>(prob(p[u][j]), FORM != FROM_P ? prob(q[u][j]) : 0.f, c);
+            for (int j = 0; j < 4; ++j) add_residual<FORM>(prob(p[u][j]), FORM != FROM_P ? prob(q[u][j]) : 0.f, c, few);
+        sum += few.sum(4 * DV_BATCH);
+#pragma unroll
+        for (int u = 0; u < DV_BATCH; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) { p[u][j] = pn[u][j]; if (FORM != FROM_P) q[u][j] = qn[u][j]; }
     }
     return sum;
 }
@@ -159,7 +188,7 @@ struct Shared {
     int have_S, have_sum;                              // S is known; the sums are those of p at `cur` (no drafter)
     long long sum;
     long long warp_sum[2][DV_WARPS];
-    long long cta_sum[2];
+    long long cta_sum[2][DV_MAX_CLUSTER];              // of every CTA of the cluster
     long long scan[DV_WARPS];
 };
 
@@ -174,6 +203,7 @@ __global__ void __launch_bounds__(DV_THREADS, 4) draft_verify_kernel(const Draft
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ Shared s;
     cg::cluster_group cluster = cg::this_cluster();
+    cluster.barrier_arrive();
     const int b = blockIdx.x / C, rank = blockIdx.x % C;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t V = a.V;
@@ -209,7 +239,7 @@ __global__ void __launch_bounds__(DV_THREADS, 4) draft_verify_kernel(const Draft
     if (tid == 0) s.todo = s.kids[0];
     const int cta_lo = rank * per_cta, my_lo = cta_lo + warp * per_warp, my_hi = my_lo + per_warp;
     int phase = 0, form = FROM_P;
-    bool fallback = false;
+    bool fallback = false, started = false;
     long long total = 0, before = 0;                   // sums over the vocabulary, and before this CTA's part
     Row row;
     Coef c;
@@ -274,14 +304,15 @@ __global__ void __launch_bounds__(DV_THREADS, 4) draft_verify_kernel(const Draft
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             if (lane == 0) s.warp_sum[phase][warp] = sum;
             __syncthreads();
-            if (tid == 0) {
+            if (!started) cluster.barrier_wait();      // every CTA of the cluster runs
+            started = true;
+            if (tid < C) {
                 long long t = 0;
                 for (int w = 0; w < DV_WARPS; ++w) t += s.warp_sum[phase][w];
-                s.cta_sum[phase] = t;
+                *cluster.map_shared_rank(&s.cta_sum[phase][rank], tid) = t;
             }
             cluster.sync();
-            long long v = 0;                           // lane r: the sum of rank r
-            if (lane < C) v = *cluster.map_shared_rank(&s.cta_sum[phase], lane);
+            const long long v = lane < C ? s.cta_sum[phase][lane] : 0;
             total = v;
             before = lane < rank ? v : 0;
 #pragma unroll
@@ -309,7 +340,7 @@ __global__ void __launch_bounds__(DV_THREADS, 4) draft_verify_kernel(const Draft
         if (done) fallback = true;
     }
     // ---- the next token: the element at which the running sum passes u_next times the whole
-    long long mine_all = s.cta_sum[phase];
+    long long mine_all = s.cta_sum[phase][rank];
     for (int j = 0; j < s.n_removed; ++j) {
         const int k = s.removed[j] + row.shift;
         total -= s.removed_p[j];
@@ -385,7 +416,6 @@ __global__ void __launch_bounds__(DV_THREADS, 4) draft_verify_kernel(const Draft
         a.path[base + tid] = in ? s.acc[tid] : -1;
         if (tid != s.n_acc) a.out_tokens[base + tid] = in ? s.tok[s.acc[tid]] : -1;
     }
-    cluster.sync();                                    // no CTA leaves while another may read its sums
 }
 
 }  // namespace
