@@ -10,6 +10,10 @@
 //
 // Both are bound by HBM (1152 B of bf16 row and 644 B of quantised row each way): one warp
 // a row, 8 dims a lane and step, so that every load and store is a full line.
+//
+// Measured on GB300: append of 46080 rows 15.6 us (5.3 TB/s), read of 169817 scattered rows 48.2 us
+// (6.3 TB/s); 72 and 4105 rows 1.7 and 2.3 us, a launch.  Append with the slot read and checked
+// before the row is loaded takes 17.9 us, so the row's loads come first.
 #include "../../include/mla_verify.h"
 #include "fp8_decode.cuh"
 #include "internal.cuh"
