@@ -293,7 +293,8 @@ int mla_kv_read_fp8(const uint8_t* kv_lat, const float* kv_scale, const void* kv
  * Verify attention over the fp8 latent cache: mla_verify_attn() with the keys
  *     k_j = [ kv_scale[s_j] * decode_e4m3(kv_lat[s_j]) | kv_rope[s_j] ],  s_j = slot_table[b, j]
  * and their first 512 dims as values.  The keys enter the scores without a rounding of their
- * own; the probabilities are rounded once for the product with the values.
+ * own; the probabilities are rounded once for the product with the values.  As a weight of the
+ * values, a scale below 2^-90 counts as 2^-90.
  *   kv_lat uint8 [n_pool, 512], kv_scale fp32 [n_pool] (>= 0), kv_rope bf16 [n_pool, 64], as
  *              mla_kv_append_quant() leaves them (lat / rope 16-byte aligned)
  *   draft_mask / draft_mask_bits  the mask of mla_verify_attn() or of
@@ -338,8 +339,9 @@ size_t mla_verify_fp8_workspace_bytes(int B, int q_len, int H, int max_seq, int 
  *   tokens       int32 [B, q_len]: the accepted drafts' tokens, the next token, then -1
  *   path         int32 [B, q_len]: the accepted drafts' nodes, then -1
  * Probabilities count as 0 where they are negative or NaN and as 1 above 1; rows need not
- * sum to exactly 1.  Sums are integers of 2^-45, so results do not depend on the order of
- * summation.  A node whose token is outside [0, vocab) or whose parent is outside [-1, i)
+ * sum to exactly 1 (of one that sums to more than 32, as raw scores may, the next token is
+ * unspecified: a token or -1).  Sums are integers of 2^-45, so results do not depend on the
+ * order of summation.  A node whose token is outside [0, vocab) or whose parent is outside [-1, i)
  * is passed over and sets MLA_DEV_BAD_DRAFT; a current node without any probability gives the
  * next token -1 and sets it too.  target_probs and draft_probs are 16-byte aligned.
  * Limits: 1 <= q_len <= 64, 0 <= B <= 65535, 1 <= vocab <= MLA_MAX_VOCAB.

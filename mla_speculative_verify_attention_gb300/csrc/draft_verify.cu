@@ -49,6 +49,7 @@ constexpr int DV_THREADS = 256;
 constexpr int DV_WARPS = DV_THREADS / 32;
 constexpr int DV_MAX_CLUSTER = 16;                   // (more than eight CTAs: opted into per device)
 constexpr int DV_BATCH = 2;                          // vectors of each row that a thread has in flight
+constexpr long long MOST = 1ll << 50;                // a thread's sum at most (32): 4096 of them do not overflow
 constexpr double UNIT = 1.0 / 35184372088832.0;      // 2^-45, the unit of the integer sums
 
 struct DraftArgs {
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(DV_THREADS, 4) draft_verify_kernel(const Draft
             c.ah = (float)s.A;
             c.al = (float)(s.A - (double)c.ah);
             phase ^= 1;
-            long long sum = sum_range(row, c, form, my_lo + lane * 4, my_hi, 128);
+            long long sum = min(sum_range(row, c, form, my_lo + lane * 4, my_hi, 128), MOST);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             if (lane == 0) s.warp_sum[phase][warp] = sum;
@@ -410,7 +411,7 @@ __global__ void __launch_bounds__(DV_THREADS, 4) draft_verify_kernel(const Draft
             const int k0 = lo + tid * piece, k1 = min(k0 + piece, hi);
             long long mine = 0;
             if (k0 < k1) {
-                mine = sum_range(row, c, form, k0, k1, 4);
+                mine = min(sum_range(row, c, form, k0, k1, 4), MOST);
                 for (int j = 0; j < s.n_removed; ++j) {
                     const int k = s.removed[j] + row.shift;
                     if (k >= k0 && k < k1) mine -= s.removed_p[j];
@@ -428,7 +429,10 @@ __global__ void __launch_bounds__(DV_THREADS, 4) draft_verify_kernel(const Draft
             if (lane == 31) s.scan[warp] = cum;
             __syncthreads();
             for (int i = 0; i < warp; ++i) cum += s.scan[i];
-            const unsigned hit = __ballot_sync(0xffffffffu, cum > thr && cum - mine <= thr);   // one lane of the block
+            const bool here = cum > thr && cum - mine <= thr;
+            const unsigned hit = __ballot_sync(0xffffffffu, here);               // one lane of the block
+            // (none where a sum was cut off at MOST: the row is no distribution)
+            if (!__syncthreads_or(here) && tid == 0) a.out_tokens[base + s.n_acc] = -1;
             if (hit) {
                 const int L = __ffs(hit) - 1;
                 thr -= __shfl_sync(0xffffffffu, cum - mine, L);
@@ -439,7 +443,7 @@ __global__ void __launch_bounds__(DV_THREADS, 4) draft_verify_kernel(const Draft
                     const long long upto = scan(v);
                     const unsigned at = __ballot_sync(0xffffffffu, upto > thr);
                     if (at || x - lane + 32 >= x1) {
-                        if (lane == (at ? __ffs(at) - 1 : 0)) a.out_tokens[base + s.n_acc] = x;
+                        if (lane == (at ? __ffs(at) - 1 : 0)) a.out_tokens[base + s.n_acc] = x >= 0 && x < a.V ? x : -1;
                         break;
                     }
                     thr -= __shfl_sync(0xffffffffu, upto, 31);

@@ -210,3 +210,22 @@ def test_two_streams_at_once(cuda_lib):
     want = check(mv, c)
     for g in got:
         assert all(np.array_equal(x.cpu().numpy(), y) for x, y in zip(g, want))
+
+
+@pytest.mark.parametrize("drafter", [True, False])
+@pytest.mark.parametrize("V", [300001, 1 << 20])
+def test_rows_that_are_no_distribution(cuda_lib, V, drafter):
+    """Raw scores in place of probabilities: sums that 64 bits would not hold."""
+    B, q_len = 2, 3
+    p = torch.ones(B, q_len, V, device="cuda")
+    q = torch.full_like(p, 2.0 ** -20) if drafter else None
+    tok = torch.tensor([[0, 5, 7]] * B, dtype=torch.int32, device="cuda")
+    u = torch.full((B, q_len), 0.5, device="cuda")
+    for u_next in (0.0, 0.3, 0.999999):
+        got = [torch.full(s, 123456789, dtype=torch.int32, device="cuda") for s in ((B,), (B, q_len), (B, q_len))]
+        n, toks, path = cuda_lib.draft_verify(p, q, tok, None, u, torch.full((B,), u_next, device="cuda"),
+                                              n_accepted=got[0], tokens=got[1], path=got[2])
+        assert n.tolist() == [2] * B and path.tolist() == [[1, 2, -1]] * B
+        assert toks[:, :2].tolist() == [[5, 7]] * B
+        assert bool(((toks[:, 2] >= -1) & (toks[:, 2] < V)).all())
+    cuda_lib.device_status(clear=True)
