@@ -204,9 +204,26 @@ __device__ __forceinline__ long long sum_row(const Row& r, const Coef& c, int lo
 }
 
 __device__ __forceinline__ long long one(const Row& r, const Coef& c, int form, int x) {
-    const float p = prob(r.p[x]);
-    if (form == FROM_P) return residual<FROM_P>(p, 0.f, c);
-    return residual<MINUS_AQ>(p, prob(r.q[x]), c);   // equal to MINUS_Q at A = 1
+    return residual<MINUS_AQ>(prob(r.p[x]), form == FROM_P ? 0.f : prob(r.q[x]), c);
+}
+
+// The same sum over lo .. < hi by one thread, for short pieces (one form for all: equal to MINUS_Q at
+// A = 1, and to FROM_P at q = 0).
+__device__ __forceinline__ long long sum_piece(const Row& r, const Coef& c, int form, int lo, int hi) {
+    long long sum = 0;
+    const int end = min(hi, r.V + r.shift);
+#pragma unroll 1
+    for (int k = lo; k < end; k += 4) {
+        float p[4], q[4] = {0.f, 0.f, 0.f, 0.f};
+        load4(r.p, k - r.shift, r.V, p);
+        if (form != FROM_P) load4(r.q, k - r.shift, r.V, q);
+        Few few = {0, 0};
+#pragma unroll
+        for (int j = 0; j < 4; j += 2)
+            add_residuals<MINUS_AQ>(prob(p[j]), prob(p[j + 1]), prob(q[j]), prob(q[j + 1]), c, few);
+        sum += few.sum(4);
+    }
+    return sum;
 }
 
 __device__ __forceinline__ long long sum_range(const Row& r, const Coef& c, int form, int lo, int hi, int step) {
@@ -411,7 +428,7 @@ __global__ void __launch_bounds__(DV_THREADS, 4) draft_verify_kernel(const Draft
             const int k0 = lo + tid * piece, k1 = min(k0 + piece, hi);
             long long mine = 0;
             if (k0 < k1) {
-                mine = min(sum_range(row, c, form, k0, k1, 4), MOST);
+                mine = min(sum_piece(row, c, form, k0, k1), MOST);
                 for (int j = 0; j < s.n_removed; ++j) {
                     const int k = s.removed[j] + row.shift;
                     if (k >= k0 && k < k1) mine -= s.removed_p[j];
