@@ -42,7 +42,7 @@ def listed():
         # one stream with every head on the GPU: bound by the matrix products
         {"name": "attn-4k-h64", "op": "attn", "B": 1, "q_len": 9, "H": 64, "lo": 4096, "hi": 4096, "mask": "tree", "pool": 8192},
         # eight streams of mixed prefixes up to 46080 keys, draft trees: bound by the cache's bytes
-        {"name": "attn-mixed", "op": "attn", "B": 8, "q_len": 9, "H": 8, "lo": 1024, "hi": 46080, "mask": "packed", "pool": 368712},
+        {"name": "attn-mixed", "op": "attn", "B": 8, "q_len": 9, "H": 8, "lo": 1024, "hi": 46080, "mask": "packed", "pool": 262144},
         # plain decode (one token a stream), 32 streams with 64 heads
         {"name": "attn-decode", "op": "attn", "B": 32, "q_len": 1, "H": 64, "lo": 1500, "hi": 2047, "mask": "chain", "pool": 65536},
         # one stream's chain of eight drafts, a small vocabulary: latency
