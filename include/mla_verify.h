@@ -340,8 +340,8 @@ size_t mla_verify_fp8_workspace_bytes(int B, int q_len, int H, int max_seq, int 
  *   path         int32 [B, q_len]: the accepted drafts' nodes, then -1
  * Probabilities count as 0 where they are negative or NaN and as 1 above 1; rows need not
  * sum to exactly 1 (of one that sums to more than 32, as raw scores may, the next token is
- * unspecified: a token or -1).  Sums are integers of 2^-45, so results do not depend on the
- * order of summation.  A node whose token is outside [0, vocab) or whose parent is outside [-1, i)
+ * unspecified: a token or -1).  Sums are integers of 2^-44, to which each element of R is rounded (to within one),
+ * so results do not depend on the order of summation.  A node whose token is outside [0, vocab) or whose parent is outside [-1, i)
  * is passed over and sets MLA_DEV_BAD_DRAFT; a current node without any probability gives the
  * next token -1 and sets it too.  target_probs and draft_probs are 16-byte aligned.
  * Limits: 1 <= q_len <= 64, 0 <= B <= 65535, 1 <= vocab <= MLA_MAX_VOCAB.

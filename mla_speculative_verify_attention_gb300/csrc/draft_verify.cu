@@ -16,8 +16,8 @@
 //
 // Exactness: the tokens are whole numbers, so a sum that is off near a border gives another
 // token.  p - A q is formed with its fp32 rounding error kept beside it (Dekker 1971, Knuth:
-// two-sum and the product's error by a fused multiply-add), rounded to a multiple of 2^-45
-// and summed as a 64-bit integer: sums do not depend on their order or on how the
+// two-sum and the product's error by a fused multiply-add), rounded to a multiple of 2^-44
+// (residual.cuh) and summed as a 64-bit integer: sums do not depend on their order or on how the
 // vocabulary is split, and the GPU's few fp64 units see a handful of operations a node.
 //
 // Bound by HBM, one pass over the row pair of the node the walk stops at (8 V bytes a
@@ -36,6 +36,7 @@
 // vectors ahead: the same for trees, 0.4 us more for chains.
 #include "../../include/mla_verify.h"
 #include "internal.cuh"
+#include "residual.cuh"
 
 #include <cooperative_groups.h>
 #include <math.h>
@@ -49,8 +50,7 @@ constexpr int DV_THREADS = 256;
 constexpr int DV_WARPS = DV_THREADS / 32;
 constexpr int DV_MAX_CLUSTER = 16;                   // (more than eight CTAs: opted into per device)
 constexpr int DV_BATCH = 2;                          // vectors of each row that a thread has in flight
-constexpr long long MOST = 1ll << 50;                // a thread's sum at most (32): 4096 of them do not overflow
-constexpr double UNIT = 1.0 / 35184372088832.0;      // 2^-45, the unit of the integer sums
+constexpr long long MOST = 1ll << 49;                // a thread's sum at most (32): 4096 of them do not overflow
 
 struct DraftArgs {
     const float* p;               // [B, q_len, V]
@@ -69,88 +69,6 @@ struct DraftArgs {
 
 // A probability as it counts: NaN and negative as 0, above 1 as 1.
 __device__ __forceinline__ float prob(float x) { return __saturatef(x); }
-
-// The residual's coefficient A in two fp32 parts, and which of three forms it takes.
-enum { FROM_P, MINUS_Q, MINUS_AQ };                  // A = 0, A = 1, any A
-struct Coef {
-    float ah, al;
-};
-
-// Adding 1.5 * 2^23 rounds to an integer and leaves it in the low mantissa bits.
-constexpr float MAGIC = 12582912.f;
-constexpr unsigned MAGIC_BITS = 0x4B400000u;
-
-// Two elements a step: the fp32 operations on pairs (64 trees 43.2 -> 42.2 us).
-struct Pair {
-    unsigned long long v;
-    __device__ __forceinline__ Pair() {}
-    __device__ __forceinline__ Pair(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
-    __device__ __forceinline__ explicit Pair(float a) : Pair(a, a) {}
-    __device__ __forceinline__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-};
-__device__ __forceinline__ Pair mul(Pair a, Pair b) {
-    Pair r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ Pair add(Pair a, Pair b) {
-    Pair r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ Pair mul_add(Pair a, Pair b, Pair c) {
-    Pair r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-__device__ __forceinline__ Pair minus(Pair a, Pair b) { return mul_add(b, Pair(-1.f), a); }
-
-// A sum of up to 256 residuals in units of 2^-45: their leading parts, in units of 2^-22, and what
-// is left of them, each at most 2^22 and taken up as the float's bits (one 32-bit addition).
-struct Few {
-    unsigned hi, lo;
-    __device__ __forceinline__ long long sum(int n) const {
-        return (long long)(int)(hi - n * MAGIC_BITS) * 8388608ll + (int)(lo - n * MAGIC_BITS);
-    }
-};
-
-// Adds max(p - A q, 0) of two elements.
-template <int FORM>
-__device__ __forceinline__ void add_residuals(float p0, float p1, float q0, float q1, const Coef& c, Few& few) {
-    // p - A q = d + e, e the rounding errors of the product and of the difference (where d > 0)
-    Pair d(p0, p1), e(0.f);
-    if (FORM != FROM_P) {
-        const Pair p = d, q(q0, q1);
-        const Pair aq = mul(Pair(FORM == MINUS_Q ? -1.f : -c.ah), q);             // - A q, rounded
-        d = add(p, aq);
-        e = add(minus(p, d), aq);
-        if (FORM == MINUS_AQ) e = minus(e, mul_add(Pair(c.al), q, mul_add(Pair(c.ah), q, aq)));
-        float s0, s1, d0, d1, e0, e1;
-        add(d, e).get(s0, s1);
-        d.get(d0, d1);
-        e.get(e0, e1);
-        d = Pair(s0 > 0.f ? d0 : 0.f, s1 > 0.f ? d1 : 0.f);
-        e = Pair(s0 > 0.f ? e0 : 0.f, s1 > 0.f ? e1 : 0.f);
-    }
-    const Pair th = mul_add(d, Pair(4194304.f), Pair(MAGIC));                     // d * 2^22
-    const Pair hi = add(th, Pair(-MAGIC));
-    Pair rem = mul_add(hi, Pair(-2.384185791015625e-07f), d);                     // |rem| <= 2^-23
-    if (FORM != FROM_P) rem = add(rem, e);
-    const Pair tl = mul_add(rem, Pair(35184372088832.f), Pair(MAGIC));            // rem * 2^45
-    float a0, a1, b0, b1;
-    th.get(a0, a1);
-    tl.get(b0, b1);
-    few.hi += __float_as_uint(a0) + __float_as_uint(a1);
-    few.lo += __float_as_uint(b0) + __float_as_uint(b1);
-}
-
-// Of one element.
-template <int FORM>
-__device__ __forceinline__ long long residual(float p, float q, const Coef& c) {
-    Few few = {0, 0};
-    add_residuals<FORM>(p, 0.f, q, 0.f, c, few);
-    return few.sum(2);
-}
 
 // A residual row: p and q of the current node.  Positions k run over whole vectors of four that
 // start on 16-byte boundaries, `shift` elements before the row; element x = k - shift.
