@@ -51,12 +51,13 @@ __device__ __forceinline__ float warp_max(float m) {
 
 // x / scale, correctly rounded: with inv = 1 / scale correctly rounded, each step
 // q + (x - q scale) inv brings a quotient that is a few units off to within one, and one that is
-// within a unit to the correctly rounded one (Markstein 1990).  Needs a scale well inside
-// the normal range; five operations where the general division takes a dozen.
+// within a unit to the correctly rounded one (Markstein 1990).  Taken as q - (q scale - x) inv: a zero
+// of either sign then leaves q = +-0 as it is, where a correction that is added makes +0 of it.  Needs
+// a scale well inside the normal range; five operations where the general division takes a dozen.
 __device__ __forceinline__ float divide(float x, float scale, float inv) {
     float q = __fmul_rn(x, inv);
-    q = fmaf(fmaf(-q, scale, x), inv, q);
-    return fmaf(fmaf(-q, scale, x), inv, q);
+    q = fmaf(-fmaf(q, scale, -x), inv, q);
+    return fmaf(-fmaf(q, scale, -x), inv, q);
 }
 
 __device__ __forceinline__ uint2 encode8(const float (&f)[8], float scale, float inv, bool finite) {
