@@ -417,10 +417,10 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
         const int region = lane >> 2, j0 = (lane & 3) * 2, odd = region & 1;
         auto widen_tile = [&](const Raw& r, int i) -> bool {
             const int st = i % STAGES;
-            // the last stage first holds the Q chunks on their way to TMEM
-            if ((i >= STAGES && !mbar_wait(&M.bars[B_KV_EMPTY + st], ((i - STAGES) / STAGES) & 1, M.abort)) ||
-                (i == STAGES - 1 && !mbar_wait(&M.bars[B_Q_FULL], 0, M.abort))) {
-                give_up(M, a.status);
+            // the last stage first holds the Q chunks on their way to TMEM; the warp goes on or leaves as a whole
+            if ((i >= STAGES && !mbar_wait_warp(&M.bars[B_KV_EMPTY + st], ((i - STAGES) / STAGES) & 1, M.abort)) ||
+                (i == STAGES - 1 && !mbar_wait_warp(&M.bars[B_Q_FULL], 0, M.abort))) {
+                if (lane == 0) give_up(M, a.status);
                 return false;
             }
             uint8_t* base = smem + L.kv + st * STAGE_BYTES;
@@ -476,6 +476,8 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
             return true;
         };
         Raw r0, r1;
+        // (The votes on what every lane knows keep the warp together behind lane 0's arrival: without them
+        // 70.2 instead of 68.8 us on the mixed batch.)
         load_tile(r0, 0);
         load_tile(r1, 1);
         for (int i = 0; i < T; i += 2) {
