@@ -312,7 +312,8 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
             const uint32_t q_region16 = (uint32_t)(RQ * 128) >> 4;
             bool ok = __all_sync(0xffffffffu, mbar_wait(&M.bars[B_Q_FULL], 0, M.abort));
             fence_proxy_async_smem();
-            for (int i = 0; i < T && ok; ++i) {
+            int i = 0;                                   // tiles issued
+            for (; i < T && ok; ++i) {
                 const int st = i % STAGES;
                 ok = mbar_wait(&M.bars[B_KV_FULL + st], (i / STAGES) & 1, M.abort);
                 if (ok && i >= 1) ok = mbar_wait(&M.bars[B_S_FREE], (i - 1) & 1, M.abort);
@@ -337,7 +338,10 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
                 }
                 __syncwarp();
             }
-            if (!ok && lane == 0) give_up(M, a.status);
+            if (!ok) {
+                if (lane == 0) give_up(M, a.status);
+                if (i > 0) mbar_drain(&M.bars[B_S_FULL], (i - 1) & 1);
+            }
         }
         __syncwarp();
         } else if (warp == 1) {
@@ -348,7 +352,8 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
         // P: K-major, no swizzle, 8-key blocks R * 16 B apart, 8-row blocks 128 B apart
         const uint64_t dp = smem_desc(p_addr, R * 16, 128);
         bool ok = true;
-        for (int j = 0; j < T && ok; ++j) {
+        int j = 0;                                       // tiles issued
+        for (; j < T && ok; ++j) {
             ok = __all_sync(0xffffffffu, mbar_wait(&M.bars[B_P_FULL], j & 1, M.abort));
             if (!ok) break;
             tc_fence_after();
@@ -364,7 +369,10 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
             }
             __syncwarp();
         }
-        if (!ok && lane == 0) give_up(M, a.status);
+        if (!ok) {
+            if (lane == 0) give_up(M, a.status);
+            if (j > 0) mbar_drain(&M.bars[B_KV_EMPTY + (j - 1) % STAGES], ((j - 1) / STAGES) & 1);
+        }
         __syncwarp();
         } else if (T > 0) {
             for (int first = Q_SOFT + warp - 2; first < min(RQ, Q_ROWS); first += 6) {
