@@ -81,6 +81,7 @@ typedef enum {
 #define MLA_MAX_HEADS 128
 #define MLA_MAX_NSPLIT 1024
 #define MLA_MAX_VOCAB (1 << 24)
+#define MLA_MAX_FP8_KEYS (1 << 30) /* slot_stride of mla_verify_attn_fp8() */
 
 /*
  * Bytes of workspace that mla_verify_attn() needs for `nsplit` key splits
@@ -303,7 +304,8 @@ int mla_kv_read_fp8(const uint8_t* kv_lat, const float* kv_scale, const void* kv
  *   lse        fp32 [B, q_len, H]
  * Every other argument, limit and device status is that of mla_verify_attn().  An explicit nsplit needs
  * the workspace that it needs there; nsplit = 0 uses what mla_verify_fp8_workspace_bytes() says, and
- * works with less (fewer splits).  q_len = 1 is plain decode.
+ * works with less (fewer splits).  q_len = 1 is plain decode.  slot_stride is at most MLA_MAX_FP8_KEYS
+ * (key positions past it would overflow 32 bits at the end of the last tile).
  */
 int mla_verify_attn_fp8(const void* q, const uint8_t* kv_lat, const float* kv_scale, const void* kv_rope,
                         int64_t n_pool, const int32_t* slot_table, int slot_stride, const int32_t* seq_lens,

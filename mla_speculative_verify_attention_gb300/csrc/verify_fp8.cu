@@ -796,7 +796,8 @@ extern "C" int mla_verify_attn_fp8(const void* q, const uint8_t* kv_lat, const f
     if (nsplit < 0 || nsplit > MLA_MAX_NSPLIT) return MLA_ERR_NSPLIT;
     if (B == 0) return MLA_OK;
     if (!q || !kv_lat || !kv_scale || !kv_rope || !slot_table || !seq_lens || !out || !lse) return MLA_ERR_NULL;
-    if (n_pool < 1 || n_pool > 0x7fffffffLL || slot_stride < q_len) return MLA_ERR_SHAPE;
+    // (key positions are 32-bit, up to a tile and a split count past the last)
+    if (n_pool < 1 || n_pool > 0x7fffffffLL || slot_stride < q_len || slot_stride > MLA_MAX_FP8_KEYS) return MLA_ERR_SHAPE;
     if ((long long)B * q_len * H > 0x7fffffffLL) return MLA_ERR_SHAPE;
     if (!isfinite(scale) || (draft_mask && draft_mask_bits)) return MLA_ERR_ARG;
     if (!aligned(q, 16) || !aligned(kv_lat, 16) || !aligned(kv_rope, 16) || !aligned(kv_scale, 4) ||
