@@ -41,6 +41,8 @@
 #include <cooperative_groups.h>
 #include <math.h>
 
+#include <atomic>
+
 namespace cg = cooperative_groups;
 
 namespace mla {
@@ -402,11 +404,11 @@ __global__ void __launch_bounds__(DV_THREADS, 4) draft_verify_kernel(const Draft
 // CTAs a stream: up to sixteen while the launch stays within one wave of four CTAs an SM and a
 // thread has a vector of each row at least.
 cudaError_t launch_draft_verify(const DraftArgs& a, int B, int num_sms, int dev, cudaStream_t stream) {
-    static bool attr_set[64];
-    if (!attr_set[dev]) {
+    static std::atomic<bool> attr_set[64];
+    if (!attr_set[dev].load(std::memory_order_acquire)) {
         cudaError_t e = cudaFuncSetAttribute(draft_verify_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
-        attr_set[dev] = true;
+        attr_set[dev].store(true, std::memory_order_release);
     }
     int C = 1;
     while (C < DV_MAX_CLUSTER && (int64_t)C * DV_THREADS * 4 < a.V && 2ll * C * B <= 4ll * num_sms) C *= 2;

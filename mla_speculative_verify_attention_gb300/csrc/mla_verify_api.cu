@@ -6,6 +6,7 @@
 #include <string.h>
 
 #include <atomic>
+#include <mutex>
 
 #include "../../include/mla_verify.h"
 #include "internal.cuh"
@@ -28,7 +29,10 @@ constexpr int MAX_DEVICES = 64;
 unsigned* g_status_ptr[MAX_DEVICES];
 unsigned long long* g_rescales_ptr[MAX_DEVICES];
 int g_num_sms[MAX_DEVICES];
-int g_arch_ok[MAX_DEVICES];      // 0 unknown, 1 sm_103, -1 other
+// 0 unknown, 1 sm_103, -1 other.  Set last and read first, so that a host thread sees either none of a
+// device's values or all of them; threads that meet in its first calls set them one after the other.
+std::atomic<int> g_arch_ok[MAX_DEVICES];
+std::mutex g_set_up;
 
 }  // namespace
 
@@ -36,7 +40,9 @@ int g_arch_ok[MAX_DEVICES];      // 0 unknown, 1 sm_103, -1 other
 int device_state(int* dev_out, unsigned** status, int* num_sms, unsigned long long** rescales) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return MLA_ERR_DEVICE;
-    if (g_arch_ok[dev] == 0) {
+    int arch_ok = g_arch_ok[dev].load(std::memory_order_acquire);
+    if (arch_ok == 0) {
+        std::lock_guard<std::mutex> lock(g_set_up);
         int major = 0, minor = 0, sms = 0;
         if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
@@ -48,9 +54,10 @@ int device_state(int* dev_out, unsigned** status, int* num_sms, unsigned long lo
         if (cudaGetSymbolAddress(&p, g_rescales) != cudaSuccess) return MLA_ERR_DEVICE;
         g_rescales_ptr[dev] = static_cast<unsigned long long*>(p);
         g_num_sms[dev] = sms;
-        g_arch_ok[dev] = (major == 10 && minor == 3) ? 1 : -1;
+        arch_ok = (major == 10 && minor == 3) ? 1 : -1;
+        g_arch_ok[dev].store(arch_ok, std::memory_order_release);
     }
-    if (g_arch_ok[dev] != 1) return MLA_ERR_DEVICE;
+    if (arch_ok != 1) return MLA_ERR_DEVICE;
     if (dev_out) *dev_out = dev;
     if (status) *status = g_status_ptr[dev];
     if (num_sms) *num_sms = g_num_sms[dev];

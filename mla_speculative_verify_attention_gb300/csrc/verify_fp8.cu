@@ -54,6 +54,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <atomic>
+
 namespace mla {
 namespace {
 
@@ -721,8 +723,8 @@ cudaError_t launch_one(const Fp8Args& a, dim3 grid, int dev, cudaStream_t stream
     if (a.RQ > (STAGES == 3 ? MAX_R3 : MAX_R) || smem > MAX_SMEM || O_COL + 4 * a.R + 32 * NQT > (int)TMEM_COLS ||
         NQT * a.RQ * 128 > STAGE_BYTES)                  // (the TMEM chunks' way station)
         return cudaErrorInvalidConfiguration;
-    static bool attr_set[64];
-    if (!attr_set[dev]) {
+    static std::atomic<bool> attr_set[64];
+    if (!attr_set[dev].load(std::memory_order_acquire)) {
         cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
         if (e != cudaSuccess) return e;
         // the warpgroups' shares have to be in the launch's registers, or their request would wait for ever
@@ -730,7 +732,7 @@ cudaError_t launch_one(const Fp8Args& a, dim3 grid, int dev, cudaStream_t stream
         e = cudaFuncGetAttributes(&at, k);
         if (e != cudaSuccess) return e;
         if (at.numRegs * NT < 128 * (72 + 168 + 2 * 136)) return cudaErrorInvalidConfiguration;
-        attr_set[dev] = true;
+        attr_set[dev].store(true, std::memory_order_release);
     }
     return launch_dependent(k, grid, dim3(NT), (size_t)smem, stream, a);
 }

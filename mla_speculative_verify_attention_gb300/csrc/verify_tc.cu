@@ -55,6 +55,8 @@
 // gather sized to the SM's load path, and the split-count policy of the host code.
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 #include "fp8_decode.cuh"
 #include "internal.cuh"
 #include "tc_ptx.cuh"
@@ -791,7 +793,7 @@ cudaError_t launch_one(bool set_attr, dim3 grid, cudaStream_t stream, const Veri
 cudaError_t launch_verify_tc(const VerifyArgs& a_in, cudaStream_t stream) {
     VerifyArgs a = a_in;
     a.debug_stall = take_debug_stall() ? 1 : 0;
-    static bool attr_set[64][5];
+    static std::atomic<bool> attr_set[64][5];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -809,7 +811,7 @@ cudaError_t launch_verify_tc(const VerifyArgs& a_in, cudaStream_t stream) {
     int which;
     if (!a.kv_fp8) which = R <= 80 ? 0 : 1;
     else which = q_tmem_chunks(R, 1) >= 7 ? 2 : 3;
-    const bool set = !attr_set[dev][which];
+    const bool set = !attr_set[dev][which].load(std::memory_order_acquire);
     switch (which) {
         case 0: e = launch_one<false, 5, 5, 1, 1>(set, grid, stream, a, q_map, R, R_step); break;
         case 1: e = launch_one<false, 3, 2, 2, 2>(set, grid, stream, a, q_map, R, R_step); break;
@@ -817,7 +819,7 @@ cudaError_t launch_verify_tc(const VerifyArgs& a_in, cudaStream_t stream) {
         case 3: e = launch_one<true, 3, 5, 1, 2>(set, grid, stream, a, q_map, R, R_step); break;
         default: e = cudaErrorInvalidConfiguration; break;
     }
-    if (e == cudaSuccess) attr_set[dev][which] = true;
+    if (e == cudaSuccess) attr_set[dev][which].store(true, std::memory_order_release);
     return e;
 }
 
