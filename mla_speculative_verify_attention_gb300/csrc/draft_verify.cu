@@ -72,6 +72,17 @@ struct DraftArgs {
 // A probability as it counts: NaN and negative as 0, above 1 as 1.
 __device__ __forceinline__ float prob(float x) { return __saturatef(x); }
 
+// floor(u T) for u in [0, 1), T >= 0; at most T (u of 1 and more), and 0 for a negative u or a NaN.
+__device__ __forceinline__ long long floor_product(float u, long long T) {
+    if (!(u > 0.f)) return 0;
+    if (u >= 1.f) return T;
+    const unsigned bits = __float_as_uint(u), e = bits >> 23;
+    const unsigned long long m = (bits & 0x7fffffu) | (e ? 0x800000u : 0u);     // u = m 2^-shift, shift >= 24
+    const int shift = 150 - (int)max(e, 1u);
+    const unsigned long long lo = m * (unsigned long long)T, hi = __umul64hi(m, (unsigned long long)T);
+    return (long long)(shift < 64 ? hi << (64 - shift) | lo >> shift : (shift < 128 ? hi >> (shift - 64) : 0ull));
+}
+
 // A residual row: p and q of the current node.  Positions k run over whole vectors of four that
 // start on 16-byte boundaries, `shift` elements before the row; element x = k - shift.
 struct Row {
@@ -326,8 +337,8 @@ __global__ void __launch_bounds__(DV_THREADS, 4) draft_verify_kernel(const Draft
         else if (k < cta_lo + per_cta) mine_all -= s.removed_p[j];
     }
     if (total > 0) {
-        const double want = (double)a.u_next[b] * (double)total;
-        long long thr = want > 0.0 ? (long long)want : 0;          // floor; cum > u T  <=>  cum > floor(u T)
+        // cum > u T  <=>  cum > floor(u T), in whole numbers
+        long long thr = floor_product(a.u_next[b], total);
         if (thr > total - 1) thr = total - 1;
         thr -= before;
         if (thr >= 0 && thr < mine_all) {                          // in this CTA's part (uniform over the CTA)

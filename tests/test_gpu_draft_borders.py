@@ -95,3 +95,46 @@ def test_random_borders(cuda_lib, kind, rejected):
     assert len(live) > 0.9 * B
     bad = [b for b in live if toks[b, 0] != want[b]]
     assert not bad, f"{len(bad)} of {len(live)}: stream {bad[0]}, token {toks[bad[0], 0]} for {want[bad[0]]}"
+
+
+def test_product_with_u_next(cuda_lib):
+    """Rows whose first two elements sum to the integer (in units of 2^-44) next above u_next times the
+    whole, less than 2^-10 away, so that the product rounds to that integer: the second element is the
+    token, since the sum up to it is greater than the product.  And rows where the two are equal: it is not."""
+    rng = np.random.default_rng(7)
+    unit, B = 1 << 44, 200
+    p, un, want = np.zeros((B, 1, 4), np.float32), np.zeros(B, np.float32), []
+    two = lambda c: (c >> 21 << 21, c & (1 << 21) - 1)          # each a float's 24 bits
+    for b in range(B):
+        while True:
+            total = int(rng.integers(unit * 6 // 10, unit * 9 // 10))
+            m = rng.integers(1 << 23, 1 << 24, 4096, dtype=np.uint64)
+            if b % 2:                                           # the product is an integer
+                total, m = total >> 24 << 24, m[:1]
+                break
+            low = (m * np.uint64(total & 0xffffff)) % np.uint64(1 << 24)     # of the product, in units of 2^-24
+            m = m[low >= np.uint64((1 << 24) - (1 << 14) + 1)]
+            if len(m):
+                break
+        m = int(m[0])
+        border = -(-m * total >> 24)                            # ceil(u T)
+        p[b, 0] = [Fraction(x, unit) for x in (*two(border), *two(total - border))]
+        assert sum(Fraction(float(x)) for x in p[b, 0]) == Fraction(total, unit)
+        un[b] = m / (1 << 24)
+        want.append(next_token([Fraction(float(x)) for x in p[b, 0]], un[b])[0])
+    assert want[::2] == [1] * (B // 2) and all(w >= 2 for w in want[1::2])
+    zero = np.zeros((B, 1), np.int32)
+    _, toks, _ = run(cuda_lib, p, None, zero, None, np.zeros((B, 1), np.float32), un)
+    assert toks[:, 0].tolist() == want
+
+
+def test_small_u_next(cuda_lib):
+    """u_next down to the smallest float, in front of elements of zero and of one unit."""
+    un = np.float32([0.0, 1e-45, 1e-40, 1.2e-38, 2.0 ** -64, 2.0 ** -63, 2.0 ** -44, 2.0 ** -43, 2.0 ** -41, 2.0 ** -24, 0.5])
+    row = np.zeros(70, np.float32)
+    row[[3, 5, 6, 40]] = 2.0 ** -44, 2.0 ** -43, 0.5, 0.5
+    p = np.broadcast_to(row, (len(un), 1, 70)).copy()
+    want = [next_token([Fraction(float(x)) for x in row], u)[0] for u in un]
+    zero = np.zeros((len(un), 1), np.int32)
+    _, toks, _ = run(cuda_lib, p, None, zero, None, np.zeros((len(un), 1), np.float32), un)
+    assert toks[:, 0].tolist() == want and set(want) >= {3, 5, 6}
