@@ -271,7 +271,8 @@ int mla_qk_norm_rope(const void* q, const void* kv, const void* q_weight, const 
  *     kv_lat[d] = e4m3(x[d] / kv_scale)              (fp32 quotient, round to nearest even)
  *     kv_rope   = x[512:576]                         (bf16, as it is)
  * 448 is the largest e4m3 value.  An infinity saturates to +-448, a NaN becomes the NaN
- * code, a row of zeros gets scale 0.
+ * code, -0 keeps its sign.  A row whose finite values are all zeros gets scale 0: it reads back as
+ * zeros, its infinities too (and NaN where it holds one).
  *   kv_lat uint8 [n_pool, 512], kv_scale fp32 [n_pool], kv_rope bf16 [n_pool, 64]: written
  *   slots int32 [n_rows], distinct in one call (which of two rows lands in a shared slot is
  *   unspecified, and its parts may come from both); rows bf16 [n_rows, 576]
@@ -283,7 +284,7 @@ int mla_kv_append_quant(uint8_t* kv_lat, float* kv_scale, void* kv_rope, int64_t
 
 /*
  * Reads cached rows back: out[i] = [ bf16(kv_scale[s] * decode_e4m3(kv_lat[s])) | kv_rope[s] ]
- * with s = slots[i] (duplicates allowed), one rounding.  out bf16 [n_rows, 576]; alignment
+ * with s = slots[i] (duplicates allowed), the product in fp32.  out bf16 [n_rows, 576]; alignment
  * as for mla_kv_append_quant().  A slot outside [0, n_pool) gives a row of zeros and sets
  * MLA_DEV_BAD_SLOT.
  */
@@ -294,8 +295,10 @@ int mla_kv_read_fp8(const uint8_t* kv_lat, const float* kv_scale, const void* kv
  * Verify attention over the fp8 latent cache: mla_verify_attn() with the keys
  *     k_j = [ kv_scale[s_j] * decode_e4m3(kv_lat[s_j]) | kv_rope[s_j] ],  s_j = slot_table[b, j]
  * and their first 512 dims as values.  The keys enter the scores without a rounding of their
- * own; the probabilities are rounded once for the product with the values.  As a weight of the
- * values, a scale below 2^-90 counts as 2^-90.
+ * own, the queries too down to 2^-31 of a row's largest element; the probabilities are rounded once,
+ * to fp16, for the product with the values (relative 2^-11; less than 2^-32 of the row's largest
+ * weight, probability times key scale, may count as nothing there).  As a weight of the values, a scale
+ * below 2^-90 counts as 2^-90.
  *   kv_lat uint8 [n_pool, 512], kv_scale fp32 [n_pool] (>= 0), kv_rope bf16 [n_pool, 64], as
  *              mla_kv_append_quant() leaves them (lat / rope 16-byte aligned)
  *   draft_mask / draft_mask_bits  the mask of mla_verify_attn() or of

@@ -27,9 +27,9 @@
 // meet in distributed shared memory.  Every CTA repeats the walk (a few dozen operations),
 // so only sums cross CTAs.
 //
-// Measured on GB300 (GPU time a call): one chain of 8 drafts over 32000 tokens 6.7 us, a chain of
-// dependent reads and one cluster barrier; 64 chains of 15 over 131072 tokens 20.1 us, of which
-// the pass over 67 MB takes 12 us (5.6 TB/s); 64 trees of 16 nodes 42.2 us: the mean stream
+// Measured on GB300 (GPU time a call): one chain of 8 drafts over 32000 tokens 6.5 us, a chain of
+// dependent reads and one cluster barrier; 64 chains of 15 over 131072 tokens 20.0 us, of which
+// the pass over 67 MB takes 12 us (5.6 TB/s); 64 trees of 16 nodes 41.9 us: the mean stream
 // makes 1.9 passes, the slowest six, and each pass after the first takes 4.5 us for its 128 KB a CTA,
 // plus 2 us for barrier and walk.  For the 64 trees (at 47.4 us, before loads ran a batch ahead): clusters
 // of 4 61 us, of 16 (two waves) 54 us, blocks of 512 threads 59 us.  Copies to shared memory five

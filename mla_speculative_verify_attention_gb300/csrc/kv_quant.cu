@@ -5,8 +5,9 @@
 // 448 being the largest e4m3 value, e4m3() rounding to nearest even and saturating; the
 // rope dims stay bf16.  One scale a token, so a row can be written without touching any
 // other.  The maximum is over the finite values: an infinity saturates to +-448 and a NaN
-// keeps the NaN code, so neither costs the other 511 values their precision.  A row of zeros
-// has scale 0.  Read: the reverse, bf16(scale * decode(code)), one rounding.
+// keeps the NaN code, so neither costs the other 511 values their precision.  A row without a
+// finite value other than zero has scale 0, and reads back as zeros (and NaN).  Read: the reverse,
+// scale * decode(code) in fp32 (28 bits rounded to 24) and that product in bf16.
 //
 // Both are bound by HBM (1152 B of bf16 row and 644 B of quantised row each way): one warp
 // a row, 8 dims a lane and step, so that every load and store is a full line.

@@ -3,16 +3,19 @@
 // key), output in bf16, on the 5th-generation tensor cores (tcgen05, TMEM).
 //
 // Mathematics.  The codes go to the tensor cores as they are: every e4m3 value is an fp16
-// value, and a bf16 query is one too after its row is brought to [2^14, 2^15) by a power of
-// two, so the products code * q are exact and a score has no error but its fp32 sum's.  With
+// value, and so is a bf16 query after its row is brought to [2^14, 2^15) by a power of two, as
+// long as it is within 2^-31 of the row's largest (smaller ones lose bits below 2^-24, 2^-38 of the
+// largest).  So the products code * q are exact, and a score has no error but its fp32 sum's.  With
 // A = sum_d q_d code_jd and C = sum_d q_d rope_jd in two fp32 accumulators,
 //     x_j  = c (s_j A + C)                              score in log2 units, c = scale log2(e) 2^e_row
 //     y_j  = x_j + log2 s_j,   P_j = 2^(y_j - m)        fp16, m the running maximum of y
 //     out  = sum_j P_j code_j / l,   l = sum_j P_j / s_j,   lse = (m + log2 l) ln 2
 // so a key's scale enters its probability's weight, in fp32, and the value product again
 // runs on the bare codes.  m is shifted by 7 so that P fills the fp16 range up to 2^15 (the
-// maximum may lag by 2^8 before O is rescaled); P's rounding is relative 2^-12.  Scales below
-// 2^-90 (rows of zeros) count as 2^-90 in the weight.
+// maximum may lag by 2^8 before O is rescaled).  P's rounding is relative 2^-11, and absolute 2^-25
+// below 2^-14: a key whose weight is less than 2^-32 of the row's largest may add nothing to out, while l,
+// which takes P before the rounding, still counts it.  Scales below 2^-90 (rows of zeros) count as
+// 2^-90 in the weight.
 //
 // One CTA handles up to 72 (in one form 96) query rows (r = t * H + h of one stream) over one key
 // split, in tiles of 48 keys:
@@ -24,11 +27,12 @@
 //   P        one thread a query row: mask, running maximum and sum, P to shared memory
 //   O^T     += code^T P^T: M=128 (value dims) x N=rows x K=48 keys, four 128-dim chunks in TMEM
 //
-// What bounds it, with long streams: shared memory (128 B a cycle).  A tile's matrix operands
-// take about 1900 cycles of it at 72 rows (a 128-row Q chunk is read whole, 4 KB an MMA), the
-// widened stores, the row loads' way through L1 and the softmax another 1200; its HBM bytes take
-// 1450 cycles at 1/152 of the measured copy rate.  Measured 1.9 us (3900 cycles) a tile: a mixed
-// batch of eight streams, 181 thousand keys, 74 us a call.  A tile is 48 keys because three such
+// What bounds it, with long streams: the gather's warps, 1.9 us a tile at 72 rows (time stamps a role,
+// mixed batch of eight streams): 0.95 us until the loads of a tile are issued, behind those in flight,
+// 0.7 for the widening and its stores, 0.25 waiting for a free stage, one after the other in each warp.
+// The scores wait 0.6 us a tile for keys, the softmax works 1.05 and waits 0.8.  Neither the matrix
+// operands' 1900 cycles of shared memory (128 B a cycle; 0.95 us) nor the HBM bytes, 0.7 us, are the
+// period.  The mixed batch with 200 thousand keys takes 76 us a call.  A tile is 48 keys because three such
 // stages fit beside Q (two of 64 keys wait for each other: 83 us; two of 48: 81 us).  Two forms that
 // were measured and not kept: codes as the matrix units' fp8 operands for scores and values, without
 // any widening (keys as rows of the scores, Q in two e4m3 pieces, P in three; half of the
@@ -36,7 +40,7 @@
 // other: 79 us, and 26 instead of 17 us at one tile a CTA, whose code is three times as long); rows
 // called into L2 four tiles ahead (80 us).  Partial rows in fp16: within 2 us either way.
 // With few keys: the chain of first reads (length, slots, rows), the queries' conversion, the first pass
-// through the code and the epilogue's partial rows: 15.0 us a call at one tile a CTA and 72 rows.
+// through the code and the epilogue's partial rows: 15.1 us a call at one tile a CTA and 72 rows.
 //
 // Warps (512 threads): 0 issues A and C, 1 issues O^T (whole warp, one elected lane), 4-7 Q,
 // softmax and epilogue (TMEM lane quadrant = warp % 4), 8-15 gather and widening (six keys of
