@@ -81,7 +81,7 @@ typedef enum {
 #define MLA_MAX_HEADS 128
 #define MLA_MAX_NSPLIT 1024
 #define MLA_MAX_VOCAB (1 << 24)
-#define MLA_MAX_FP8_KEYS (1 << 30) /* slot_stride of mla_verify_attn_fp8() */
+#define MLA_MAX_FP8_KEYS (1 << 30) /* slot_stride of mla_verify_attn_fp8(), its rules' form, key weights and eviction */
 
 /*
  * Bytes of workspace that mla_verify_attn() needs for `nsplit` key splits
@@ -322,6 +322,83 @@ int mla_verify_attn_fp8(const void* q, const uint8_t* kv_lat, const float* kv_sc
  * is out of range, or where it does not split.
  */
 size_t mla_verify_fp8_workspace_bytes(int B, int q_len, int H, int max_seq, int num_sms);
+
+/*
+ * mla_verify_attn_fp8() under score rules.  With pos(j) = key_pos[b, j] (key_pos NULL: j), doc(j) =
+ * key_doc[b, j], and draft t's position and document those of its own key j_t = seq_lens[b] - q_len + t:
+ *     z = scale q.k_j,   z = softcap tanh(z / softcap)  (softcap > 0),   z += slopes[h] (pos(j) - pos(j_t))
+ *     key j is visible to draft t  iff  ( (draft mask and window) or pos(j) < prefix_lens[b] )
+ *                                       and ( doc(j) == doc(j_t) or doc(j) < 0 )
+ *     draft mask  j < seq_lens[b] - q_len, or the mask's bit of draft j;   window  pos(j_t) - pos(j) < window
+ *   softcap     finite, >= 0 (0: no cap)
+ *   slopes      fp32 [H], or NULL: no bias.  A positive slope favours near keys.
+ *   key_pos     int32 [B, slot_stride], any order (mla_kv_evict() leaves a table whose positions have gaps),
+ *               or NULL.  Positions that a bias compares are less than 2^31 apart.
+ *   window      >= 0 (0: no window).  Without key_pos, keys that no draft sees are not read.
+ *   prefix_lens int32 [B], or NULL: no prefix.  Prefix keys are visible both ways: a draft whose own
+ *               position is in the prefix is seen by every draft of its stream.
+ *   key_doc     int32 [B, slot_stride], or NULL: one document.  A negative number is shared by all.
+ * tanh is off by at most 2^-19 of itself.  A row that sees nothing gets out = 0, lse = -inf.  Every other
+ * argument, limit and error is that of mla_verify_attn_fp8(); with nsplit = 0 the workspace that it uses is
+ * mla_verify_fp8_workspace_bytes() of max_seq = slot_stride, or of min(slot_stride, window - 1 + q_len)
+ * with a window and no key_pos.
+ */
+int mla_verify_attn_fp8_rules(const void* q, const uint8_t* kv_lat, const float* kv_scale, const void* kv_rope,
+                              int64_t n_pool, const int32_t* slot_table, int slot_stride, const int32_t* seq_lens,
+                              const uint8_t* draft_mask, const uint64_t* draft_mask_bits, int B, int q_len, int H,
+                              float scale, float softcap, const float* slopes, const int32_t* key_pos, int window,
+                              const int32_t* prefix_lens, const int32_t* key_doc, void* out, float* lse, int nsplit,
+                              void* workspace, size_t ws_bytes, mla_stream_t stream);
+
+/*
+ * The weight that each key of a stream got from the rows of a step, added up:
+ *     new[b, j] = sum over the counted drafts t that see key j, and all heads h, of exp(z[b,t,h,j] - lse[b,t,h])
+ *     out[b, j] = decay * weights[b, j] + new[b, j]     j < seq_lens[b] - q_len
+ *     out[b, j] = new[b, j]                             the drafts' own keys (new in the table)
+ * with the scores z and the visibility of mla_verify_attn_fp8_rules(), and lse as the attention left it.
+ * What mla_kv_evict() chooses by.  The keys enter the scores without a rounding of their own, the queries
+ * as in mla_verify_attn_fp8().  Sums are fp32 in a fixed order: equal calls give equal bits.
+ *   lse      fp32 [B, q_len, H]; a row with lse -inf saw nothing and adds nothing, one with NaN gives NaN
+ *   counted  uint8 [B, q_len], or NULL: every draft counts (else e.g. only the accepted ones)
+ *   weights  fp32 [B, slot_stride], or NULL: zeros;  decay finite
+ *   out      fp32 [B, slot_stride], may be `weights`; entries from seq_lens[b] on stay as they were
+ *   q, the cache, table, lengths, masks, rules, limits and errors as for mla_verify_attn_fp8_rules();
+ *   of a stream with a bad length nothing is written.  slot_stride is at most MLA_MAX_FP8_KEYS.
+ * mla_key_weights() is the same over the bf16 cache [n_pool, 576] of mla_verify_attn().
+ */
+int mla_key_weights_fp8(const void* q, const uint8_t* kv_lat, const float* kv_scale, const void* kv_rope,
+                        int64_t n_pool, const int32_t* slot_table, int slot_stride, const int32_t* seq_lens,
+                        const uint8_t* draft_mask, const uint64_t* draft_mask_bits, int B, int q_len, int H,
+                        float scale, float softcap, const float* slopes, const int32_t* key_pos, int window,
+                        const int32_t* prefix_lens, const int32_t* key_doc, const float* lse, const uint8_t* counted,
+                        const float* weights, float decay, float* out, mla_stream_t stream);
+int mla_key_weights(const void* q, const void* kv_cache, int64_t n_pool, const int32_t* slot_table, int slot_stride,
+                    const int32_t* seq_lens, const uint8_t* draft_mask, const uint64_t* draft_mask_bits, int B,
+                    int q_len, int H, float scale, float softcap, const float* slopes, const int32_t* key_pos,
+                    int window, const int32_t* prefix_lens, const int32_t* key_doc, const float* lse,
+                    const uint8_t* counted, const float* weights, float decay, float* out, mla_stream_t stream);
+
+/*
+ * Eviction: of each stream's n = seq_lens[b] keys, K = min(n, max(budget, sink + recent)) stay: the first
+ * `sink`, the last `recent`, and of those between them the ones with the largest weights (of equal ones
+ * the lower index; NaN counts as the largest, -0 as 0).  The table's entries that stay move together in
+ * their order, and the others are listed for the allocator:
+ *     table_out / weights_out / pos_out / doc_out [b, 0:K]   the kept keys' slots, weights, positions, documents
+ *     lens_out[b] = K,   freed[b, 0:n-K] the other slots in order,   n_freed[b] = n - K
+ *   slot_table int32 [B, slot_stride], seq_lens int32 [B] (0 <= n <= slot_stride), weights fp32 [B, slot_stride]
+ *   key_pos    int32 [B, slot_stride], or NULL: a key's position is its index (which pos_out then gets)
+ *   key_doc    int32 [B, slot_stride], or NULL
+ *   budgets    int32 [B] on the device, or NULL: `budget` for every stream (< 0 counts as 0)
+ *   pos_out, doc_out (NULL where key_doc is), freed and n_freed (both or neither) may be NULL: not written
+ * An output may be its own input (in place); other overlaps are not allowed.  Entries past those named stay
+ * as they were.  A length outside [0, slot_stride] sets MLA_DEV_BAD_LEN: the stream is left alone, with
+ * lens_out[b] = n and n_freed[b] = 0.  No cache row moves: slots are only handed back.
+ * Limits: 0 <= B <= 65535, 1 <= slot_stride <= MLA_MAX_FP8_KEYS, sink >= 0, recent >= 0.
+ */
+int mla_kv_evict(const int32_t* slot_table, const int32_t* seq_lens, const float* weights, const int32_t* key_pos,
+                 const int32_t* key_doc, int B, int slot_stride, const int32_t* budgets, int budget, int sink,
+                 int recent, int32_t* table_out, int32_t* lens_out, float* weights_out, int32_t* pos_out,
+                 int32_t* doc_out, int32_t* freed, int32_t* n_freed, mla_stream_t stream);
 
 /*
  * Acceptance of drafted tokens from given random numbers, the step after a verify pass:

@@ -13,7 +13,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple, Union
 
 import torch
 
@@ -36,7 +36,8 @@ EXPORTS = ("mla_verify_workspace_bytes", "mla_verify_auto_nsplit", "mla_verify_a
            "mla_status_string", "mla_verify_version", "mla_verify_attn_static_scratch",
            "mla_sparse_fp8_decode", "mla_sparse_fp8_partials", "mla_verify_attn_packed", "mla_kv_append", "mla_kv_append_fp8",
            "mla_debug_stall_next_launch", "mla_debug_rescale_count", "mla_qk_norm_rope", "mla_kv_append_quant",
-           "mla_kv_read_fp8", "mla_verify_attn_fp8", "mla_draft_verify", "mla_verify_fp8_workspace_bytes")
+           "mla_kv_read_fp8", "mla_verify_attn_fp8", "mla_draft_verify", "mla_verify_fp8_workspace_bytes",
+           "mla_verify_attn_fp8_rules", "mla_key_weights_fp8", "mla_key_weights", "mla_kv_evict")
 STATIC_SCRATCH_BYTES = 64 << 20
 
 _lib = None
@@ -90,6 +91,15 @@ def load():
     L.mla_kv_read_fp8.restype = I
     L.mla_verify_attn_fp8.argtypes = [P, P, P, P, I64, P, I, P, P, P, I, I, I, F, P, P, I, P, SZ, P]
     L.mla_verify_attn_fp8.restype = I
+    rules = [F, P, P, I, P, P]
+    L.mla_verify_attn_fp8_rules.argtypes = [P, P, P, P, I64, P, I, P, P, P, I, I, I, F] + rules + [P, P, I, P, SZ, P]
+    L.mla_verify_attn_fp8_rules.restype = I
+    L.mla_key_weights_fp8.argtypes = [P, P, P, P, I64, P, I, P, P, P, I, I, I, F] + rules + [P, P, P, F, P, P]
+    L.mla_key_weights_fp8.restype = I
+    L.mla_key_weights.argtypes = [P, P, I64, P, I, P, P, P, I, I, I, F] + rules + [P, P, P, F, P, P]
+    L.mla_key_weights.restype = I
+    L.mla_kv_evict.argtypes = [P, P, P, P, P, I, I, P, I, I, I, P, P, P, P, P, P, P, P]
+    L.mla_kv_evict.restype = I
     L.mla_verify_fp8_workspace_bytes.argtypes = [I, I, I, I, I]
     L.mla_verify_fp8_workspace_bytes.restype = SZ
     L.mla_draft_verify.argtypes = [P, P, P, P, P, P, I, I, I, P, P, P, P]
@@ -424,7 +434,8 @@ def _call(fn: str):
     if _calls is None:
         L, calls = load(), {}
         for name in ("mla_qk_norm_rope", "mla_kv_append_quant", "mla_kv_read_fp8", "mla_verify_attn_fp8",
-                     "mla_draft_verify"):
+                     "mla_draft_verify", "mla_verify_attn_fp8_rules", "mla_key_weights_fp8", "mla_key_weights",
+                     "mla_kv_evict"):
             f = L[name]                                # a function object of its own
             f.argtypes = [ctypes.c_int64 if a in (ctypes.c_void_p, ctypes.c_size_t) else a
                           for a in getattr(L, name).argtypes]
@@ -574,6 +585,223 @@ def verify_attn_fp8(q: torch.Tensor, kv_lat: torch.Tensor, kv_scale: torch.Tenso
             stride, seq_lens.data_ptr(), mask, bits, B, q_len, H, float(scale), out.data_ptr(), lse.data_ptr(), nsplit,
             workspace.data_ptr(), workspace.numel(), at))
     return out, lse
+
+
+def _want_mask(draft_mask, B: int, q_len: int):
+    """(byte mask, packed mask) addresses."""
+    if draft_mask is None:
+        return 0, 0
+    if draft_mask.dtype is torch.int64:
+        _want("draft_mask", draft_mask, torch.int64, (B, q_len))
+        return 0, draft_mask.data_ptr()
+    _want("draft_mask", draft_mask, torch.uint8, (B, q_len, q_len))
+    return draft_mask.data_ptr(), 0
+
+
+def _want_int(name, v, least: int = 0):
+    """`v` is an int that the library's 32-bit argument holds."""
+    if not least <= v <= 0x7fffffff:
+        raise ValueError(f"{name} must be in [{least}, 2^31), not {v}")
+
+
+def _want_rules(B: int, H: int, stride: int, slopes, key_pos, window: int, prefix_lens, key_doc):
+    _want_int("window", window)
+    if slopes is not None:
+        _want("slopes", slopes, torch.float32, (H,))
+    if key_pos is not None:
+        _want("key_pos", key_pos, torch.int32, (B, stride))
+    if prefix_lens is not None:
+        _want("prefix_lens", prefix_lens, torch.int32, (B,))
+    if key_doc is not None:
+        _want("key_doc", key_doc, torch.int32, (B, stride))
+
+
+def verify_attn_fp8_rules(q: torch.Tensor, kv_lat: torch.Tensor, kv_scale: torch.Tensor, kv_rope: torch.Tensor,
+                          slot_table: torch.Tensor, seq_lens: torch.Tensor, draft_mask: Optional[torch.Tensor],
+                          scale: float, *, softcap: float = 0.0, slopes: Optional[torch.Tensor] = None,
+                          key_pos: Optional[torch.Tensor] = None, window: int = 0,
+                          prefix_lens: Optional[torch.Tensor] = None, key_doc: Optional[torch.Tensor] = None,
+                          out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, nsplit: int = 0,
+                          workspace: Optional[torch.Tensor] = None,
+                          stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """mla_verify_attn_fp8_rules: verify_attn_fp8 with scores capped by softcap * tanh(z / softcap), a bias
+    slopes [H] (fp32) times the distance of positions, a sliding window, a prefix of prefix_lens [B] (int32)
+    positions that every draft sees, and documents key_doc [B, stride] (int32; negative: shared).  key_pos
+    int32 [B, stride] are the keys' positions (None: their index); a draft's position and document are
+    those of its own key."""
+    _want_dims("q", q, torch.bfloat16, 4, D_QK)
+    B, q_len, H, _ = q.shape
+    n_pool = _want_fp8_cache(kv_lat, kv_scale, kv_rope)
+    _want_dims("slot_table", slot_table, torch.int32, 2)
+    stride = slot_table.shape[1]
+    _want("slot_table", slot_table, torch.int32, (B, stride))
+    _want("seq_lens", seq_lens, torch.int32, (B,))
+    mask, bits = _want_mask(draft_mask, B, q_len)
+    _want_rules(B, H, stride, slopes, key_pos, window, prefix_lens, key_doc)
+    if out is not None:
+        _want("out", out, torch.bfloat16, (B, q_len, H, D_V))
+    if lse is not None:
+        _want("lse", lse, torch.float32, (B, q_len, H))
+    if workspace is not None:
+        _want_dims("workspace", workspace, torch.uint8, 1)
+    dev = _device_of(q, kv_lat, kv_scale, kv_rope, slot_table, seq_lens, draft_mask, slopes, key_pos, prefix_lens,
+                     key_doc, out, lse, workspace)
+    with _on(dev):
+        at = _stream_on(stream, dev)
+        if out is None:
+            out = _empty(q, (B, q_len, H, D_V), torch.bfloat16, stream)
+        if lse is None:
+            lse = _empty(q, (B, q_len, H), torch.float32, stream)
+        if workspace is None:
+            longest = min(stride, window - 1 + q_len) if window > 0 and key_pos is None else stride
+            need = workspace_bytes(B, q_len, H, nsplit) if nsplit > 0 else verify_fp8_workspace_bytes(
+                B, q_len, H, longest, num_sms(dev))
+            workspace = _empty(q, (max(need, 256),), torch.uint8, stream)
+        _check("mla_verify_attn_fp8_rules", _call("mla_verify_attn_fp8_rules")(
+            q.data_ptr(), kv_lat.data_ptr(), kv_scale.data_ptr(), kv_rope.data_ptr(), n_pool, slot_table.data_ptr(),
+            stride, seq_lens.data_ptr(), mask, bits, B, q_len, H, float(scale), float(softcap), _addr(slopes),
+            _addr(key_pos), window, _addr(prefix_lens), _addr(key_doc), out.data_ptr(), lse.data_ptr(), nsplit,
+            workspace.data_ptr(), workspace.numel(), at))
+    return out, lse
+
+
+def _key_weights(fn, cache, n_pool, q, slot_table, seq_lens, draft_mask, scale, lse, softcap, slopes, key_pos, window,
+                 prefix_lens, key_doc, weights, decay, counted, out, stream):
+    _want_dims("q", q, torch.bfloat16, 4, D_QK)
+    B, q_len, H, _ = q.shape
+    _want_dims("slot_table", slot_table, torch.int32, 2)
+    stride = slot_table.shape[1]
+    _want("slot_table", slot_table, torch.int32, (B, stride))
+    _want("seq_lens", seq_lens, torch.int32, (B,))
+    _want("lse", lse, torch.float32, (B, q_len, H))
+    mask, bits = _want_mask(draft_mask, B, q_len)
+    _want_rules(B, H, stride, slopes, key_pos, window, prefix_lens, key_doc)
+    if counted is not None:
+        _want("counted", counted, torch.uint8, (B, q_len))
+    if weights is not None:
+        _want("weights", weights, torch.float32, (B, stride))
+    if out is not None:
+        _want("out", out, torch.float32, (B, stride))
+    dev = _device_of(*cache, q, slot_table, seq_lens, lse, draft_mask, slopes, key_pos, prefix_lens, key_doc, weights,
+                     counted, out)
+    with _on(dev):
+        at = _stream_on(stream, dev)
+        if out is None:
+            if weights is None:                            # what lies behind a stream's last key is 0
+                out = _empty(lse, (B, stride), torch.float32, stream)
+                with torch.cuda.stream(stream):            # (None: the current one)
+                    out.zero_()
+            else:
+                out = weights
+        _check(fn, _call(fn)(
+            *(t.data_ptr() for t in cache), n_pool, slot_table.data_ptr(), stride, seq_lens.data_ptr(), mask, bits, B,
+            q_len, H, float(scale), float(softcap), _addr(slopes), _addr(key_pos), window, _addr(prefix_lens),
+            _addr(key_doc), lse.data_ptr(), _addr(counted), _addr(weights), float(decay), out.data_ptr(), at))
+    return out
+
+
+def key_weights_fp8(q: torch.Tensor, kv_lat: torch.Tensor, kv_scale: torch.Tensor, kv_rope: torch.Tensor,
+                    slot_table: torch.Tensor, seq_lens: torch.Tensor, draft_mask: Optional[torch.Tensor], scale: float,
+                    lse: torch.Tensor, *, softcap: float = 0.0, slopes: Optional[torch.Tensor] = None,
+                    key_pos: Optional[torch.Tensor] = None, window: int = 0,
+                    prefix_lens: Optional[torch.Tensor] = None, key_doc: Optional[torch.Tensor] = None,
+                    weights: Optional[torch.Tensor] = None, decay: float = 1.0,
+                    counted: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """mla_key_weights_fp8: adds to decay * weights [B, stride] (fp32) what weight every key got from the
+    step's rows, given the attention's lse and under the same rules.  ``counted`` uint8 [B, q_len]: the
+    drafts that count (None: all).  Writes ``out``, by default ``weights`` itself (a new tensor where
+    that is None), and returns it."""
+    n_pool = _want_fp8_cache(kv_lat, kv_scale, kv_rope)
+    return _key_weights("mla_key_weights_fp8", (q, kv_lat, kv_scale, kv_rope), n_pool, q, slot_table, seq_lens,
+                        draft_mask, scale, lse, softcap, slopes, key_pos, window, prefix_lens, key_doc, weights, decay,
+                        counted, out, stream)
+
+
+def key_weights(q: torch.Tensor, kv_cache: torch.Tensor, slot_table: torch.Tensor, seq_lens: torch.Tensor,
+                draft_mask: Optional[torch.Tensor], scale: float, lse: torch.Tensor, *, softcap: float = 0.0,
+                slopes: Optional[torch.Tensor] = None, key_pos: Optional[torch.Tensor] = None, window: int = 0,
+                prefix_lens: Optional[torch.Tensor] = None, key_doc: Optional[torch.Tensor] = None,
+                weights: Optional[torch.Tensor] = None, decay: float = 1.0, counted: Optional[torch.Tensor] = None,
+                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """mla_key_weights: key_weights_fp8 over the bf16 cache [n_pool, 576] of verify_attn."""
+    _want_dims("kv_cache", kv_cache, torch.bfloat16, 2, D_QK)
+    return _key_weights("mla_key_weights", (q, kv_cache), kv_cache.shape[0], q, slot_table, seq_lens, draft_mask,
+                        scale, lse, softcap, slopes, key_pos, window, prefix_lens, key_doc, weights, decay, counted, out,
+                        stream)
+
+
+class Evicted(NamedTuple):
+    """What kv_evict leaves: the tables of the kept keys, and the slots that it hands back."""
+    slot_table: torch.Tensor
+    seq_lens: torch.Tensor
+    weights: torch.Tensor
+    key_pos: Optional[torch.Tensor]
+    key_doc: Optional[torch.Tensor]
+    freed: torch.Tensor
+    n_freed: torch.Tensor
+
+
+def kv_evict(slot_table: torch.Tensor, seq_lens: torch.Tensor, weights: torch.Tensor,
+             budget: Union[int, torch.Tensor], *, sink: int = 0, recent: int = 0,
+             key_pos: Optional[torch.Tensor] = None, key_doc: Optional[torch.Tensor] = None,
+             table_out: Optional[torch.Tensor] = None, lens_out: Optional[torch.Tensor] = None,
+             weights_out: Optional[torch.Tensor] = None, pos_out: Optional[torch.Tensor] = None,
+             doc_out: Optional[torch.Tensor] = None, freed: Optional[torch.Tensor] = None,
+             n_freed: Optional[torch.Tensor] = None, stream=None) -> Evicted:
+    """mla_kv_evict: keeps each stream's first ``sink``, last ``recent`` and otherwise heaviest keys, ``budget``
+    in all (an int, or int32 [B] on the device), and moves their entries of slot_table, weights, key_pos and
+    key_doc [B, stride] together.  By default in place; an ``_out`` tensor takes the result instead.
+    Without key_pos a key's position is its index (pos_out, where given, gets it).  The evicted slots are in
+    freed [B, stride], n_freed [B] of them."""
+    _want_dims("slot_table", slot_table, torch.int32, 2)
+    shape = slot_table.shape
+    B, stride = shape
+    _want("seq_lens", seq_lens, torch.int32, (B,))
+    _want("weights", weights, torch.float32, shape)
+    each = isinstance(budget, torch.Tensor)
+    if each:
+        _want("budget", budget, torch.int32, (B,))
+    else:
+        _want_int("budget", budget)
+    _want_int("sink", sink)
+    _want_int("recent", recent)
+    if key_pos is not None:
+        _want("key_pos", key_pos, torch.int32, shape)
+    if key_doc is not None:
+        _want("key_doc", key_doc, torch.int32, shape)
+    elif doc_out is not None:
+        raise ValueError("doc_out goes with key_doc")
+    table_out = slot_table if table_out is None else table_out
+    lens_out = seq_lens if lens_out is None else lens_out
+    weights_out = weights if weights_out is None else weights_out
+    pos_out = key_pos if pos_out is None else pos_out
+    doc_out = key_doc if doc_out is None else doc_out
+    _want("table_out", table_out, torch.int32, shape)
+    _want("lens_out", lens_out, torch.int32, (B,))
+    _want("weights_out", weights_out, torch.float32, shape)
+    if pos_out is not None:
+        _want("pos_out", pos_out, torch.int32, shape)
+    if doc_out is not None:
+        _want("doc_out", doc_out, torch.int32, shape)
+    if freed is not None:
+        _want("freed", freed, torch.int32, shape)
+    if n_freed is not None:
+        _want("n_freed", n_freed, torch.int32, (B,))
+    dev = _device_of(slot_table, seq_lens, weights, key_pos, key_doc, budget if each else None, table_out, lens_out,
+                     weights_out, pos_out, doc_out, freed, n_freed)
+    with _on(dev):
+        at = _stream_on(stream, dev)
+        if freed is None:
+            freed = _empty_like(slot_table, torch.int32, stream)
+        if n_freed is None:
+            n_freed = _empty_like(seq_lens, torch.int32, stream)
+        _check("mla_kv_evict", _call("mla_kv_evict")(
+            slot_table.data_ptr(), seq_lens.data_ptr(), weights.data_ptr(), _addr(key_pos), _addr(key_doc), B, stride,
+            budget.data_ptr() if each else 0, 0 if each else budget, sink, recent, table_out.data_ptr(),
+            lens_out.data_ptr(), weights_out.data_ptr(), _addr(pos_out), _addr(doc_out), freed.data_ptr(),
+            n_freed.data_ptr(), at))
+    return Evicted(table_out, lens_out, weights_out, pos_out, doc_out, freed, n_freed)
 
 
 def draft_verify(target_probs: torch.Tensor, draft_probs: Optional[torch.Tensor], draft_tokens: torch.Tensor,

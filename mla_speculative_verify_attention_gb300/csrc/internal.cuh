@@ -66,6 +66,34 @@ __host__ __device__ inline void split_range(int n, int S, int s, int tile, int* 
     *end = (int)(e < n ? e : n);
 }
 
+// The keys of a stream that a sliding window leaves visible to some draft, where a key's position is its
+// index: with p = n - q_len, draft 0 sees keys from p - window + 1 on, the others start later, and the
+// first prefix_lens[b] keys stay visible; between them is a gap that no kernel has to read.
+// window 0: all keys.
+struct KeySpan {
+    int window = 0;
+    const int32_t* prefix_lens = nullptr;
+
+    __device__ __forceinline__ void gap(int b, int n, int q_len, int* at, int* len) const {
+        *at = *len = 0;
+        if (window > 0) {
+            const int lo = max(0, n - q_len - window + 1);
+            *at = prefix_lens ? min(max(__ldg(prefix_lens + b), 0), lo) : 0;
+            *len = lo - *at;
+        }
+    }
+    __device__ __forceinline__ int seen(int b, int n, int q_len) const {   // n: a valid length
+        int at, len;
+        gap(b, n, q_len, &at, &len);
+        return n - len;
+    }
+    // Keys of the longest stream to plan for (a prefix's length is known on the device only).
+    int most(int slot_stride, int q_len) const {
+        const long long w = (long long)window - 1 + q_len;
+        return window > 0 && w < slot_stride ? (int)w : slot_stride;
+    }
+};
+
 // Balanced key split of one launch over B <= 64 streams of unequal length, decided on
 // the device (the host does not know the lengths): with T the sum of the valid lengths,
 // the keys are cut into chunks of chunk = max(least, ceil(T / G)) keys, rounded up to `unit`, the
@@ -76,13 +104,13 @@ __host__ __device__ inline void split_range(int n, int S, int s, int tile, int* 
 // i + 32), so no barrier or shared memory is needed.
 struct BalancedPlan {
     int chunk;
-    int n[2];       // lengths of streams lane and lane + 32 (0 past B)
+    int n[2];       // lengths (visible keys, KeySpan) of streams lane and lane + 32 (0 past B)
     int ns[2];      // split slots of streams lane and lane + 32
     int incl[2];    // inclusive prefix sums of the slot counts at those streams
 };
 
 __device__ inline BalancedPlan balanced_plan(const int32_t* seq_lens, int B, int q_len, int slot_stride, int G,
-                                             int unit = 32, int least = 128) {
+                                             int unit = 32, int least = 128, const KeySpan span = KeySpan{}) {
     const int lane = threadIdx.x & 31;
     BalancedPlan P;
     int* n = P.n;
@@ -93,6 +121,7 @@ __device__ inline BalancedPlan balanced_plan(const int32_t* seq_lens, int B, int
         const int i = lane + 32 * h;
         n[h] = i < B ? seq_lens[i] : 0;
         ok[h] = i < B && n[h] >= q_len && n[h] <= slot_stride;
+        if (ok[h]) n[h] = span.seen(i, n[h], q_len);
         if (ok[h]) t += n[h];
     }
 #pragma unroll
@@ -197,6 +226,7 @@ cudaError_t launch_combine_bf16(const float* part_out, const float* part_lse, lo
 // Combine of a balanced split (slot-major partials of VerifyArgs::balanced).
 cudaError_t launch_combine_balanced(const VerifyArgs& a, cudaStream_t stream);
 // The same with a bf16 output and chunks of whole tiles of `unit` keys.
-cudaError_t launch_combine_balanced_bf16(const VerifyArgs& a, __nv_bfloat16* out, int unit, cudaStream_t stream);
+cudaError_t launch_combine_balanced_bf16(const VerifyArgs& a, __nv_bfloat16* out, int unit, const KeySpan& span,
+                                         cudaStream_t stream);
 
 }  // namespace mla

@@ -92,6 +92,7 @@ struct CombineBalanced {
     int on;
     const int32_t* seq_lens;
     int B, q_len, slot_stride, G, rows, unit, least;
+    KeySpan span;
 };
 
 // The merged sums are fp32; a bf16 output rounds each of them once.
@@ -120,7 +121,7 @@ __global__ void __launch_bounds__(CB_THREADS) combine_kernel(const float* __rest
     long long po = row * (long long)S_all * D_V;
     if (bal.on) {
         const BalancedPlan P = balanced_plan(bal.seq_lens, bal.B, bal.q_len, bal.slot_stride, bal.G,
-                                             bal.unit, bal.least);
+                                             bal.unit, bal.least, bal.span);
         const int b = (int)(row / bal.rows), r = (int)(row % bal.rows);
         int first, count;
         balanced_stream(P, b, &first, &count);
@@ -231,23 +232,23 @@ cudaError_t launch_combine_any(const float* part_out, const float* part_lse, lon
 
 cudaError_t launch_combine(const float* part_out, const float* part_lse, long long n_rows, int S,
                            float* out, float* lse, cudaStream_t stream) {
-    CombineBalanced off;
-    memset(&off, 0, sizeof off);
+    CombineBalanced off{};
     return launch_combine_any(part_out, part_lse, n_rows, S, out, lse, off, stream);
 }
 
 cudaError_t launch_combine_bf16(const float* part_out, const float* part_lse, long long n_rows, int S,
                                 __nv_bfloat16* out, float* lse, cudaStream_t stream) {
-    CombineBalanced off;
-    memset(&off, 0, sizeof off);
+    CombineBalanced off{};
     return launch_combine_any(part_out, part_lse, n_rows, S, out, lse, off, stream);
 }
 
 // S here bounds the slots of one stream (nsplit slots in all): the weights' shared memory.
 namespace {
 template <typename Out>
-cudaError_t combine_balanced(const VerifyArgs& a, Out* out, int unit, int least, cudaStream_t stream) {
-    CombineBalanced bal;
+cudaError_t combine_balanced(const VerifyArgs& a, Out* out, int unit, int least, const KeySpan& span,
+                             cudaStream_t stream) {
+    CombineBalanced bal{};
+    bal.span = span;
     bal.on = 1;
     bal.seq_lens = a.seq_lens;
     bal.B = a.B; bal.q_len = a.q_len; bal.slot_stride = a.slot_stride; bal.G = a.bal_G;
@@ -259,11 +260,12 @@ cudaError_t combine_balanced(const VerifyArgs& a, Out* out, int unit, int least,
 }  // namespace
 
 cudaError_t launch_combine_balanced(const VerifyArgs& a, cudaStream_t stream) {
-    return combine_balanced(a, a.out, 32, 128, stream);
+    return combine_balanced(a, a.out, 32, 128, KeySpan{}, stream);
 }
 
-cudaError_t launch_combine_balanced_bf16(const VerifyArgs& a, __nv_bfloat16* out, int unit, cudaStream_t stream) {
-    return combine_balanced(a, out, unit, unit, stream);
+cudaError_t launch_combine_balanced_bf16(const VerifyArgs& a, __nv_bfloat16* out, int unit, const KeySpan& span,
+                                         cudaStream_t stream) {
+    return combine_balanced(a, out, unit, unit, span, stream);
 }
 
 }  // namespace mla

@@ -1,0 +1,174 @@
+"""verify_attn_fp8_rules against its float64 form: caps, distance biases, windows, prefixes, documents, and
+what they do together, at tile and split borders and where rows see nothing."""
+import numpy as np
+import pytest
+import torch
+
+import long_ref as lr
+import step_ref as ref
+import workloads as w
+
+pytestmark = pytest.mark.gpu
+SCALE = w.default_scale()
+
+
+def check(mv, s, rules, **kw):
+    out, lse = mv.verify_attn_fp8_rules(*s.on("cuda"), SCALE, **rules.on("cuda"), **kw)
+    torch.cuda.synchronize()
+    assert mv.device_status() == 0
+    o, l, t_out, t_lse = lr.attention(ref.f64(s.q), s.keys_of, s.seq, s.mask, SCALE, rules)
+    got_o, got_l = ref.f64(out), ref.f64(lse)
+    none = np.isneginf(l)
+    assert np.array_equal(np.isneginf(got_l), none) and np.all(got_o[none] == 0)
+    assert np.all(np.abs(got_o - o) <= t_out), float(np.max(np.abs(got_o - o) - t_out))
+    assert np.all(np.abs(got_l[~none] - l[~none]) <= t_lse[~none])
+    return out, lse
+
+
+def rules_of(kind, s):
+    B, st, H = s.B, s.stride, s.H
+    r = np.random.default_rng(7)
+    docs = np.sort(r.integers(-1, 3, (B, st)), 1).astype(np.int32)
+    return {
+        "cap": lambda: lr.Rules(softcap=5.0),
+        "bias": lambda: lr.Rules(slopes=lr.slopes(H)),
+        "window": lambda: lr.Rules(window=50),
+        "window-prefix": lambda: lr.Rules(window=33, prefix_lens=r.integers(0, 40, B).astype(np.int32)),
+        "window-pos": lambda: lr.Rules(window=50, key_pos=lr.gaps(1, B, st)),
+        "prefix": lambda: lr.Rules(prefix_lens=(s.seq - 1).astype(np.int32)),
+        "docs": lambda: lr.Rules(key_doc=docs),
+        "all": lambda: lr.Rules(softcap=30.0, slopes=lr.slopes(H), key_pos=lr.gaps(2, B, st), window=90,
+                                prefix_lens=r.integers(0, 20, B).astype(np.int32), key_doc=docs),
+    }[kind]()
+
+
+KINDS = ("cap", "bias", "window", "window-prefix", "window-pos", "prefix", "docs", "all")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("lens,q_len,H,mask,nsplit", [
+    ([1], 1, 1, "chain", 0), ([48, 49, 7], 5, 3, "tree", 1), ([265], 9, 8, "packed", 0), ([97, 300, 193], 9, 8, "tree", 3),
+    ([150, 600], 1, 64, "chain", 0), ([130], 17, 24, "packed", 2), ([144, 145], 64, 2, "tree", 0), ([200], 6, 16, "chain", 0)])
+def test_rules(cuda_lib, kind, lens, q_len, H, mask, nsplit):
+    s = lr.Step(3 + len(lens), lens, q_len, H, mask=mask)
+    check(cuda_lib, s, rules_of(kind, s), nsplit=nsplit)
+
+
+def test_no_rules_is_the_plain_attention(cuda_lib):
+    """Every rule off: bit for bit verify_attn_fp8."""
+    s = lr.Step(1, [500, 77, 260], 9, 8, mask="tree")
+    args = s.on("cuda")
+    a = cuda_lib.verify_attn_fp8(*args, SCALE)
+    b = cuda_lib.verify_attn_fp8_rules(*args, SCALE)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("cap", [0.05, 1.0, 1e4, 1e30])
+def test_caps(cuda_lib, cap):
+    """Small caps flatten every score, huge ones leave them: tanh is right near zero and far out."""
+    check(cuda_lib, lr.Step(9, [130, 60], 4, 8, q_size=4.0), lr.Rules(softcap=cap))
+
+
+@pytest.mark.parametrize("window", [1, 2, 47, 48, 49, 96, 1000, 2 ** 31 - 1])
+@pytest.mark.parametrize("prefix", [None, 0, 1, 48, 5000])
+def test_windows(cuda_lib, window, prefix):
+    """Windows and prefixes at tile borders; keys between them are skipped, whatever their rows hold."""
+    s = lr.Step(11, [400, 150, 9], 3, 4)
+    rules = lr.Rules(window=window, prefix_lens=None if prefix is None else np.full(3, prefix, np.int32))
+    check(cuda_lib, s, rules)
+    check(cuda_lib, s, lr.Rules(window=window, prefix_lens=rules.prefix_lens,
+                                key_pos=np.broadcast_to(np.arange(s.stride, dtype=np.int32), (3, s.stride))))
+
+
+def test_rows_that_see_nothing(cuda_lib):
+    """A draft whose mask shows no draft and whose document has no key: out 0, lse -inf, its neighbours right."""
+    s = lr.Step(13, [100, 60], 4, 2, mask="tree")
+    s.mask[0, 2] = 0
+    doc = np.zeros((2, s.stride), np.int32)
+    doc[0, 100 - 4 + 2] = 9
+    _, lse = check(cuda_lib, s, lr.Rules(key_doc=doc))
+    assert torch.isneginf(lse[0, 2]).all() and torch.isfinite(lse[1]).all()
+
+
+def test_masked_rows_may_hold_anything(cuda_lib):
+    """NaN codes, infinite scales and NaN rotated parts in keys that no draft sees change nothing."""
+    s = lr.Step(17, [300], 5, 8)
+    doc = np.zeros((1, s.stride), np.int32)
+    doc[0, 20:200] = 1
+    rules = lr.Rules(key_doc=doc, softcap=20.0, slopes=lr.slopes(8))
+    want = check(cuda_lib, s, rules)
+    bad = s.table[0, 20:200].long()
+    s.lat[bad[::2]] = 0x7F
+    s.scale[bad[1::3]] = float("inf")
+    s.rope[bad[::5]] = float("nan")
+    out, lse = cuda_lib.verify_attn_fp8_rules(*s.on("cuda"), SCALE, **rules.on("cuda"))
+    assert torch.equal(lse, want[1]) and torch.equal(out, want[0])
+
+
+def test_far_positions(cuda_lib):
+    """Positions near 2^31 and negative ones: differences and the window's edge stay exact."""
+    s = lr.Step(19, [200, 90], 4, 4)
+    for start in (2 ** 31 - 1 - 2 * 200, -2 ** 31):
+        pos = lr.gaps(3, 2, s.stride, start=start)
+        check(cuda_lib, s, lr.Rules(slopes=lr.slopes(4), key_pos=pos, window=60))
+        check(cuda_lib, s, lr.Rules(slopes=-lr.slopes(4), key_pos=pos, window=2 ** 31 - 1))
+
+
+def test_positions_in_any_order(cuda_lib):
+    s = lr.Step(21, [170], 9, 8, mask="packed")
+    pos = np.random.default_rng(1).permutation(170).astype(np.int32)[None]
+    check(cuda_lib, s, lr.Rules(slopes=lr.slopes(8), key_pos=pos, window=40, prefix_lens=np.array([12], np.int32)))
+
+
+def test_wide_table_many_streams_and_a_stream(cuda_lib):
+    """More streams than the balanced split takes, a table wider than any, another stream, out and lse given."""
+    lens = [4 + 7 * (i % 30) for i in range(70)]
+    s = lr.Step(23, lens, 4, 4, stride=400)
+    out = torch.empty((70, 4, 4, 512), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((70, 4, 4), device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    a, b = check(cuda_lib, s, lr.Rules(window=64, slopes=lr.slopes(4)), out=out, lse=lse, stream=side)
+    assert a is out and b is lse
+
+
+def test_bad_lengths_and_slots(cuda_lib):
+    mv = cuda_lib
+    s = lr.Step(25, [100, 60, 80], 4, 4)
+    rules = lr.Rules(window=30, prefix_lens=np.array([3, 3, 3], np.int32), slopes=lr.slopes(4))
+    q, lat, sc, rope, table, seq, _ = s.on("cuda")
+    seq[0], seq[1] = 3, s.stride + 1
+    out, lse = mv.verify_attn_fp8_rules(q, lat, sc, rope, table, seq, None, SCALE, **rules.on("cuda"))
+    assert mv.device_status() == 2
+    assert torch.isnan(lse[:2]).all() and (out[:2] == 0).all() and torch.isfinite(lse[2]).all()
+    seq.copy_(torch.from_numpy(s.seq))
+    table[1, 58] = s.lat.shape[0]
+    table[2, 79] = -1
+    mv.verify_attn_fp8_rules(q, lat, sc, rope, table, seq, None, SCALE, **rules.on("cuda"))
+    assert mv.device_status() == 1
+
+
+def test_captured(cuda_lib):
+    """Captured once, replayed on other lengths and rules' contents."""
+    mv = cuda_lib
+    s = lr.Step(27, [300, 200], 5, 8)
+    args = s.on("cuda")
+    rules = lr.Rules(softcap=20.0, slopes=lr.slopes(8), window=100, prefix_lens=np.array([5, 9], np.int32))
+    dev = rules.on("cuda")
+    out, lse = torch.empty((2, 5, 8, 512), dtype=torch.bfloat16, device="cuda"), torch.empty((2, 5, 8), device="cuda")
+    ws = torch.empty(32 << 20, dtype=torch.uint8, device="cuda")
+    call = lambda: mv.verify_attn_fp8_rules(*args, SCALE, **dev, out=out, lse=lse, workspace=ws)
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for lens, prefix in (([300, 200], [5, 9]), ([120, 7], [60, 0])):
+        s.seq[:] = lens
+        args[5].copy_(torch.from_numpy(s.seq))
+        rules.prefix_lens = np.array(prefix, np.int32)
+        dev["prefix_lens"].copy_(torch.from_numpy(rules.prefix_lens))
+        g.replay()
+        torch.cuda.synchronize()
+        o, l, t_out, t_lse = lr.attention(ref.f64(s.q), s.keys_of, s.seq, None, SCALE, rules)
+        assert np.all(np.abs(ref.f64(out) - o) <= t_out) and np.all(np.abs(ref.f64(lse) - l) <= t_lse)
