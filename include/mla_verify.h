@@ -362,6 +362,7 @@ int mla_verify_attn_fp8_rules(const void* q, const uint8_t* kv_lat, const float*
  *   counted  uint8 [B, q_len], or NULL: every draft counts (else e.g. only the accepted ones)
  *   weights  fp32 [B, slot_stride], or NULL: zeros;  decay finite
  *   out      fp32 [B, slot_stride], may be `weights`; entries from seq_lens[b] on stay as they were
+ *   workspace  device scratch of ws_bytes >= mla_key_weights_workspace_bytes(); NULL where that is 0
  *   q, the cache, table, lengths, masks, rules, limits and errors as for mla_verify_attn_fp8_rules();
  *   of a stream with a bad length nothing is written.  slot_stride is at most MLA_MAX_FP8_KEYS.
  * mla_key_weights() is the same over the bf16 cache [n_pool, 576] of mla_verify_attn().
@@ -371,12 +372,20 @@ int mla_key_weights_fp8(const void* q, const uint8_t* kv_lat, const float* kv_sc
                         const uint8_t* draft_mask, const uint64_t* draft_mask_bits, int B, int q_len, int H,
                         float scale, float softcap, const float* slopes, const int32_t* key_pos, int window,
                         const int32_t* prefix_lens, const int32_t* key_doc, const float* lse, const uint8_t* counted,
-                        const float* weights, float decay, float* out, mla_stream_t stream);
+                        const float* weights, float decay, float* out, void* workspace, size_t ws_bytes,
+                        mla_stream_t stream);
 int mla_key_weights(const void* q, const void* kv_cache, int64_t n_pool, const int32_t* slot_table, int slot_stride,
                     const int32_t* seq_lens, const uint8_t* draft_mask, const uint64_t* draft_mask_bits, int B,
                     int q_len, int H, float scale, float softcap, const float* slopes, const int32_t* key_pos,
                     int window, const int32_t* prefix_lens, const int32_t* key_doc, const float* lse,
-                    const uint8_t* counted, const float* weights, float decay, float* out, mla_stream_t stream);
+                    const uint8_t* counted, const float* weights, float decay, float* out, void* workspace,
+                    size_t ws_bytes, mla_stream_t stream);
+
+/*
+ * Bytes of workspace that mla_key_weights_fp8() and mla_key_weights() need: 0 up to 128 rows (q_len * H), else
+ * 4 bytes a key and 128 rows.  Pure host function; 0 where an argument is out of range.
+ */
+size_t mla_key_weights_workspace_bytes(int B, int q_len, int H, int slot_stride);
 
 /*
  * Eviction: of each stream's n = seq_lens[b] keys, K = min(n, max(budget, sink + recent)) stay: the first

@@ -37,7 +37,8 @@ EXPORTS = ("mla_verify_workspace_bytes", "mla_verify_auto_nsplit", "mla_verify_a
            "mla_sparse_fp8_decode", "mla_sparse_fp8_partials", "mla_verify_attn_packed", "mla_kv_append", "mla_kv_append_fp8",
            "mla_debug_stall_next_launch", "mla_debug_rescale_count", "mla_qk_norm_rope", "mla_kv_append_quant",
            "mla_kv_read_fp8", "mla_verify_attn_fp8", "mla_draft_verify", "mla_verify_fp8_workspace_bytes",
-           "mla_verify_attn_fp8_rules", "mla_key_weights_fp8", "mla_key_weights", "mla_kv_evict")
+           "mla_verify_attn_fp8_rules", "mla_key_weights_fp8", "mla_key_weights", "mla_kv_evict",
+           "mla_key_weights_workspace_bytes")
 STATIC_SCRATCH_BYTES = 64 << 20
 
 _lib = None
@@ -94,10 +95,12 @@ def load():
     rules = [F, P, P, I, P, P]
     L.mla_verify_attn_fp8_rules.argtypes = [P, P, P, P, I64, P, I, P, P, P, I, I, I, F] + rules + [P, P, I, P, SZ, P]
     L.mla_verify_attn_fp8_rules.restype = I
-    L.mla_key_weights_fp8.argtypes = [P, P, P, P, I64, P, I, P, P, P, I, I, I, F] + rules + [P, P, P, F, P, P]
+    L.mla_key_weights_fp8.argtypes = [P, P, P, P, I64, P, I, P, P, P, I, I, I, F] + rules + [P, P, P, F, P, P, SZ, P]
     L.mla_key_weights_fp8.restype = I
-    L.mla_key_weights.argtypes = [P, P, I64, P, I, P, P, P, I, I, I, F] + rules + [P, P, P, F, P, P]
+    L.mla_key_weights.argtypes = [P, P, I64, P, I, P, P, P, I, I, I, F] + rules + [P, P, P, F, P, P, SZ, P]
     L.mla_key_weights.restype = I
+    L.mla_key_weights_workspace_bytes.argtypes = [I, I, I, I]
+    L.mla_key_weights_workspace_bytes.restype = SZ
     L.mla_kv_evict.argtypes = [P, P, P, P, P, I, I, P, I, I, I, P, P, P, P, P, P, P, P]
     L.mla_kv_evict.restype = I
     L.mla_verify_fp8_workspace_bytes.argtypes = [I, I, I, I, I]
@@ -666,7 +669,7 @@ def verify_attn_fp8_rules(q: torch.Tensor, kv_lat: torch.Tensor, kv_scale: torch
 
 
 def _key_weights(fn, cache, n_pool, q, slot_table, seq_lens, draft_mask, scale, lse, softcap, slopes, key_pos, window,
-                 prefix_lens, key_doc, weights, decay, counted, out, stream):
+                 prefix_lens, key_doc, weights, decay, counted, out, workspace, stream):
     _want_dims("q", q, torch.bfloat16, 4, D_QK)
     B, q_len, H, _ = q.shape
     _want_dims("slot_table", slot_table, torch.int32, 2)
@@ -682,8 +685,10 @@ def _key_weights(fn, cache, n_pool, q, slot_table, seq_lens, draft_mask, scale, 
         _want("weights", weights, torch.float32, (B, stride))
     if out is not None:
         _want("out", out, torch.float32, (B, stride))
+    if workspace is not None:
+        _want_dims("workspace", workspace, torch.uint8, 1)
     dev = _device_of(*cache, q, slot_table, seq_lens, lse, draft_mask, slopes, key_pos, prefix_lens, key_doc, weights,
-                     counted, out)
+                     counted, out, workspace)
     with _on(dev):
         at = _stream_on(stream, dev)
         if out is None:
@@ -693,10 +698,14 @@ def _key_weights(fn, cache, n_pool, q, slot_table, seq_lens, draft_mask, scale, 
                     out.zero_()
             else:
                 out = weights
+        if workspace is None and q_len * H > 128:
+            need = int(load().mla_key_weights_workspace_bytes(B, q_len, H, stride))
+            workspace = _empty(lse, (max(need, 256),), torch.uint8, stream)
         _check(fn, _call(fn)(
             *(t.data_ptr() for t in cache), n_pool, slot_table.data_ptr(), stride, seq_lens.data_ptr(), mask, bits, B,
             q_len, H, float(scale), float(softcap), _addr(slopes), _addr(key_pos), window, _addr(prefix_lens),
-            _addr(key_doc), lse.data_ptr(), _addr(counted), _addr(weights), float(decay), out.data_ptr(), at))
+            _addr(key_doc), lse.data_ptr(), _addr(counted), _addr(weights), float(decay), out.data_ptr(),
+            _addr(workspace), workspace.numel() if workspace is not None else 0, at))
     return out
 
 
@@ -707,15 +716,16 @@ def key_weights_fp8(q: torch.Tensor, kv_lat: torch.Tensor, kv_scale: torch.Tenso
                     prefix_lens: Optional[torch.Tensor] = None, key_doc: Optional[torch.Tensor] = None,
                     weights: Optional[torch.Tensor] = None, decay: float = 1.0,
                     counted: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
-                    stream=None) -> torch.Tensor:
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """mla_key_weights_fp8: adds to decay * weights [B, stride] (fp32) what weight every key got from the
     step's rows, given the attention's lse and under the same rules.  ``counted`` uint8 [B, q_len]: the
     drafts that count (None: all).  Writes ``out``, by default ``weights`` itself (a new tensor where
-    that is None), and returns it."""
+    that is None), and returns it.  ``workspace`` is a byte (uint8) CUDA tensor, allocated here where the
+    call needs one (mla_key_weights_workspace_bytes) and none is given."""
     n_pool = _want_fp8_cache(kv_lat, kv_scale, kv_rope)
     return _key_weights("mla_key_weights_fp8", (q, kv_lat, kv_scale, kv_rope), n_pool, q, slot_table, seq_lens,
                         draft_mask, scale, lse, softcap, slopes, key_pos, window, prefix_lens, key_doc, weights, decay,
-                        counted, out, stream)
+                        counted, out, workspace, stream)
 
 
 def key_weights(q: torch.Tensor, kv_cache: torch.Tensor, slot_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -723,12 +733,13 @@ def key_weights(q: torch.Tensor, kv_cache: torch.Tensor, slot_table: torch.Tenso
                 slopes: Optional[torch.Tensor] = None, key_pos: Optional[torch.Tensor] = None, window: int = 0,
                 prefix_lens: Optional[torch.Tensor] = None, key_doc: Optional[torch.Tensor] = None,
                 weights: Optional[torch.Tensor] = None, decay: float = 1.0, counted: Optional[torch.Tensor] = None,
-                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
     """mla_key_weights: key_weights_fp8 over the bf16 cache [n_pool, 576] of verify_attn."""
     _want_dims("kv_cache", kv_cache, torch.bfloat16, 2, D_QK)
     return _key_weights("mla_key_weights", (q, kv_cache), kv_cache.shape[0], q, slot_table, seq_lens, draft_mask,
                         scale, lse, softcap, slopes, key_pos, window, prefix_lens, key_doc, weights, decay, counted, out,
-                        stream)
+                        workspace, stream)
 
 
 class Evicted(NamedTuple):

@@ -53,11 +53,10 @@
 
 #include "../../include/mla_verify.h"
 #include "internal.cuh"
+#include "query_rows.cuh"
 #include "score_rules.cuh"
 #include "tc_ptx.cuh"
 
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <math.h>
 #include <string.h>
 
@@ -161,36 +160,6 @@ __device__ __forceinline__ void give_up(const Misc& m, unsigned* status) {
     if (atomicExch(const_cast<int*>(m.abort), 1) == 0) atomicOr(status, DEV_TIMEOUT);
 }
 
-// Four e4m3 codes (byte i = code i) as four fp16 values; exact, NaN stays NaN.
-__device__ __forceinline__ uint2 widen4(uint32_t w) {
-    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
-    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-    return make_uint2((uint32_t)lo.x | ((uint32_t)lo.y << 16), (uint32_t)hi.x | ((uint32_t)hi.y << 16));
-}
-
-// Two bf16 values (one word) times f, a power of two, as two fp16 values.
-__device__ __forceinline__ uint32_t q_to_f16(uint32_t w, float f) {
-    const __half2 h = __floats2half2_rn(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t q_to_bf16(uint32_t w, float f) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-// N query rows, a row a warp: rows first, first + step, ..; rows past nrows are zeros.
-template <int N>
-__device__ __forceinline__ void load_q_rows(uint4 (&v)[N][3], const __nv_bfloat16* q0, int first, int step, int nrows) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int u = 0; u < N; ++u) {
-        const int rr = first + u * step;
-        const uint4* src = reinterpret_cast<const uint4*>(q0 + (int64_t)rr * D_QK);
-#pragma unroll
-        for (int c = 0; c < 3; ++c)
-            v[u][c] = rr < nrows && c * 32 + lane < 72 ? __ldg(src + c * 32 + lane) : make_uint4(0, 0, 0, 0);
-    }
-}
-
 // Those rows in fp16 (the rope chunk in bf16), each divided by row_exp, the power of two that brings
 // its largest element into [2^14, 2^15): chunks below NQT to q_tmp (bound for TMEM), the others to q_s;
 // rows of 128 B, 128-byte swizzle, RQ rows a chunk.
@@ -198,32 +167,12 @@ template <int N, int NQT>
 __device__ __forceinline__ void store_q_rows(const uint4 (&v)[N][3], uint8_t* q_s, uint8_t* q_tmp, float* row_exp,
                                              int first, int step, int end, int RQ) {
     const int lane = threadIdx.x & 31;
-    __nv_bfloat162 top[N];
-#pragma unroll
-    for (int u = 0; u < N; ++u) {
-        __nv_bfloat162 m[3];
-#pragma unroll
-        for (int c = 0; c < 3; ++c) {
-            const uint32_t w[4] = {v[u][c].x & 0x7fff7fffu, v[u][c].y & 0x7fff7fffu, v[u][c].z & 0x7fff7fffu,
-                                   v[u][c].w & 0x7fff7fffu};
-            const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(w);
-            m[c] = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
-        }
-        top[u] = __hmax2(__hmax2(m[0], m[1]), m[2]);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-        for (int u = 0; u < N; ++u) {
-            const uint32_t w = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<const uint32_t*>(&top[u]), o);
-            top[u] = __hmax2(top[u], *reinterpret_cast<const __nv_bfloat162*>(&w));
-        }
+    int exps[N];
+    row_exponents<N>(v, exps);
 #pragma unroll
     for (int u = 0; u < N; ++u) {
         const int rr = first + u * step;
-        // exponent of the row's largest element, within what keeps both factors finite
-        const float big = fmaxf(__low2float(top[u]), __high2float(top[u]));
-        const int e = min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 127);
+        const int e = exps[u];
         const float mul = __int_as_float((14 - e + 127) << 23);
         if (rr >= end) continue;
         if (lane == 0) row_exp[rr] = __int_as_float((e - 14 + 127) << 23);

@@ -30,7 +30,7 @@ def test_attn_rules_refusals(lib):
 
 
 def test_key_weights_refusals(lib):
-    tail = dict(lse=16, counted=None, w=None, decay=1.0, out=16, st=None)
+    tail = dict(lse=16, counted=None, w=None, decay=1.0, out=16, ws=None, wsb=0, st=None)
     common = dict(pool=10, table=16, stride=16, seq=16, mask=None, bits=None, B=1, q_len=9, H=8, scale=0.1, **RULES, **tail)
     f = caller(lib, "mla_key_weights_fp8", q=16, lat=16, sc=16, rope=16, **common)
     g = caller(lib, "mla_key_weights", q=16, kv=16, **common)
@@ -40,6 +40,16 @@ def test_key_weights_refusals(lib):
         assert f(**{name: None}) == -1 and f(**{name: 18}) == -3
     assert g(kv=None) == -1 and g(kv=24) == -3
     assert f(B=0, q=None) == 0 and g(B=0, q=None) == 0
+    for kw in (dict(), dict(ws=256, wsb=2 * 3 * 16 * 4 - 1)):          # 130 rows: two tiles
+        assert f(B=3, q_len=13, H=10, **kw) == -4 and g(B=3, q_len=13, H=10, **kw) == -4
+    assert f(B=3, q_len=13, H=10, ws=258, wsb=1 << 20) == -3
+
+
+def test_key_weights_workspace(lib):
+    ws = lib.mla_key_weights_workspace_bytes
+    assert ws(4, 16, 8, 1000) == 0 and ws(4, 1, 128, 1000) == 0
+    assert ws(4, 17, 8, 1000) == 2 * 4 * 1000 * 4 and ws(1, 64, 128, 1 << 20) == 64 << 22
+    assert ws(0, 64, 128, 10) == ws(1, 0, 128, 10) == ws(1, 65, 128, 10) == ws(1, 64, 129, 10) == ws(1, 64, 128, 0) == 0
 
 
 def test_evict_refusals(lib):
