@@ -4,14 +4,23 @@
 // The attention's log-sum-exp is given, so there is no softmax to run: every (row, key) pair stands for
 // itself, and a key's sum needs nothing of another key.
 //
-// One CTA handles up to 128 query rows of one stream over one range of its keys, in tiles of 48 keys, on
+// Scores over the fp8 cache.  The codes are operands of the 8-bit matrix products as they lie in the cache,
+// nothing is widened.  A bf16 query, its row brought to [2^7, 2^8) by a power of two, goes in two e4m3 pieces:
+// h = e4m3(q), then l = e4m3(2^5 (q - h)), whose four bits each hold the eight of a bf16 number.  That is
+// exact down to 2^-14 of the row's largest element, and within 2^-22 of the largest below.  With the
+// pieces' sums over the latent dims H and L and the rotated part's C in three fp32 accumulators,
+//     z_j = scale 2^e (s_j (H + 2^-5 L) + C)
+// so neither keys nor scales are rounded.  (Measured on the products: 512 terms are summed to 2^-25 of the
+// sum of their magnitudes, as with fp16 operands.)  The bf16 cache takes one sum over 576 dims.
+//
+// One CTA handles up to 128 query rows of one stream over one range of its keys, in tiles of 32 keys, on
 // the 5th-generation tensor cores: all of Q sits in TMEM (288 columns), the scores of two tiles beside it.
-//   gather   16 warps, three keys of a tile each.  fp8 cache: rows into registers, two tiles ahead, and as
-//            exact fp16 values into a 128-byte-swizzled stage; bf16 cache: 16-byte cp.async into the stage
-//   A, C     tcgen05.mma M=128 (query rows) x N=48 (keys) x K=576; over the fp8 cache the latent's sum A and the
-//            rotated part's C apart, as in verify_fp8.cuh: z = s_j A + C needs no rounding of a key
-//   weights  one thread a query row: exp2(c z - lse), then the sum over a warp's 32 rows by halving exchanges
-//            (16 keys in 16 shuffles), the four warps' sums in shared memory
+//   gather   four warps, eight keys of a tile each: 16-byte cp.async from the slot table's rows into
+//            128-byte-swizzled stages, ten of them (fp8; 200 KB under way) or six (bf16)
+//   scores   tcgen05.mma M=128 (query rows) x N=32 (keys), Q from TMEM
+//   weights  sixteen warps, a thread a query row and 16 keys, in two sets that take tiles in turn:
+//            exp2(c z - lse), then the sum over a warp's 32 rows by halving exchanges (16 keys in 16
+//            shuffles), the four warps' sums in shared memory
 // More than 128 rows: a row tile a CTA, whose sums meet in the workspace (4 bytes a key and row tile; a
 // second small kernel adds them in order).  Sums have a fixed order: equal calls give equal bits.
 #include "../../include/mla_verify.h"
@@ -30,23 +39,28 @@ namespace {
 using namespace tc;
 
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr int NK = 48;                               // keys per tile
+constexpr int NK = 32;                               // keys per tile
 constexpr int MAX_R = 128;                           // query rows per CTA
 constexpr int NT = 768;
-constexpr int GATHER0 = 8, GATHER_WARPS = 16;        // warps 0-3 weights, 4 products, 0-7 Q to TMEM, 8-23 gather
+constexpr int SCORE_WARPS = 16, MMA_WARP = 16, GATHER0 = 20, GATHER_WARPS = 4;   // (17 to 19 only bring Q)
 constexpr int WK = NK / GATHER_WARPS;                // keys of a tile per gather warp
-constexpr int STAGES = 4;
-constexpr int RING = STAGES + 2;                     // key scales outlive their stage by the two tiles of scores
-constexpr int NCHUNK = D_QK / 64;
-constexpr int REGION = NK * 128;                     // one 64-dim chunk of a stage
-constexpr int STAGE_BYTES = NCHUNK * REGION;         // 55296 B
-constexpr int Q_CHUNK = MAX_R * 128;                 // Q on its way to TMEM lies in stages 1 to 3
+constexpr int MAX_STAGES = 10;
+constexpr int RING = MAX_STAGES + 2;                 // what belongs to a key outlives its stage by the two tiles of scores
+constexpr int REGION = NK * 128;                     // one 128-byte chunk of a stage's rows
+constexpr int Q_CHUNKS = 9, Q_CHUNK = MAX_R * 128;   // Q on its way to TMEM lies in the stages from the third on
+constexpr int Q_STAGE = 2;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int D_COL = NCHUNK * 32, D_STEP = 2 * NK;  // scores of tile i at D_COL + (i & 1) D_STEP: A, then C
+constexpr int D_COL = Q_CHUNKS * 32, D_STEP = 3 * NK;  // scores of tile i at D_COL + (i & 1) D_STEP: H, L, C
 static_assert(D_COL + 2 * D_STEP <= (int)TMEM_COLS, "TMEM");
-static_assert(NCHUNK * Q_CHUNK <= (STAGES - 1) * STAGE_BYTES, "Q's way station");
 
-enum { B_KV_FULL = 0, B_KV_EMPTY = B_KV_FULL + STAGES, B_S_FULL = B_KV_EMPTY + STAGES, B_S_FREE = B_S_FULL + 2,
+// A stage: fp8 four chunks of 128 codes and one of the rotated part, bf16 nine of 64 dims.
+template <bool FP8>
+struct Shape {
+    static constexpr int CHUNKS = FP8 ? 5 : 9, STAGES = FP8 ? MAX_STAGES : 6, STAGE_BYTES = CHUNKS * REGION;
+    static_assert(Q_CHUNKS * Q_CHUNK <= (STAGES - Q_STAGE) * STAGE_BYTES, "Q's way station");
+};
+
+enum { B_KV_FULL = 0, B_KV_EMPTY = B_KV_FULL + MAX_STAGES, B_S_FULL = B_KV_EMPTY + MAX_STAGES, B_S_FREE = B_S_FULL + 2,
        B_Q_FULL = B_S_FREE + 2, B_COUNT };
 
 struct Misc {
@@ -56,10 +70,11 @@ struct Misc {
     float row_exp[MAX_R];                            // the power of two that a query row was divided by
     float key_scale[RING][NK];
     int key_pos[RING][NK], key_doc[RING][NK];
-    float sums[2][4][NK];                            // a tile's sums over the rows of each weights warp
+    float sums[2][2][4][NK];                         // of a set's two last tiles: sums over each quadrant's rows
 };
-constexpr int SMEM = STAGES * STAGE_BYTES + (int)sizeof(Misc);
-static_assert(SMEM <= 232448, "opt-in shared memory per block on sm_103");
+template <bool FP8>
+constexpr int smem_bytes() { return Shape<FP8>::STAGES * Shape<FP8>::STAGE_BYTES + (int)sizeof(Misc); }
+static_assert(smem_bytes<true>() <= 232448 && smem_bytes<false>() <= 232448, "opt-in shared memory per block on sm_103");
 
 struct WeightArgs {
     const __nv_bfloat16* q;
@@ -162,12 +177,27 @@ __device__ __forceinline__ void give_up(Misc* M, unsigned* status) {
     if (atomicExch(const_cast<int*>(&M->abort), 1) == 0) atomicOr(status, DEV_TIMEOUT);
 }
 
+// Two bf16 values (one word) of a row times f, a power of two, as two e4m3 pieces: the bytes of h in the low
+// half, those of l = 2^5 (q - h) in the high half.  What is not finite becomes NaN.
+__device__ __forceinline__ uint32_t q_pieces(uint32_t w, float f) {
+    const float x0 = __uint_as_float(w << 16) * f, x1 = __uint_as_float(w & 0xffff0000u) * f;
+    const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+    const __half2 back = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h, __NV_E4M3));
+    const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2((x0 - __low2float(back)) * 32.f, (x1 - __high2float(back)) * 32.f),
+                                                __NV_SATFINITE, __NV_E4M3);
+    uint32_t both = h | (l << 16);
+    if (!(fabsf(x0) < 448.f)) both |= 0x007f007fu;
+    if (!(fabsf(x1) < 448.f)) both |= 0x7f007f00u;
+    return both;
+}
+
 template <bool FP8, bool RULES>
 __global__ void __launch_bounds__(NT, 1) key_weights_kernel(const WeightArgs a) {
+    using S = Shape<FP8>;
     extern __shared__ __align__(1024) uint8_t smem[];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    Misc* const M = reinterpret_cast<Misc*>(smem + STAGES * STAGE_BYTES);
+    Misc* const M = reinterpret_cast<Misc*>(smem + S::STAGES * S::STAGE_BYTES);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rows = a.q_len * a.H, row0 = blockIdx.y * a.R_step, nrows = min(a.R_step, rows - row0);
     const bool direct = gridDim.y == 1;
@@ -193,8 +223,9 @@ __global__ void __launch_bounds__(NT, 1) key_weights_kernel(const WeightArgs a) 
 
     // keys that no draft sees: their former weights decay
     if (RULES && direct) {
-        const int share = (gap + count - 1) / count, g0 = index * share, g1 = min(gap, g0 + share);
-        for (int g = g0 + tid; g < g1; g += NT)
+        const int share = (gap + count - 1) / count;
+        const long long g0 = (long long)index * share, g1 = min((long long)gap, g0 + share);
+        for (long long g = g0 + tid; g < g1; g += NT)
             a.out[stream0 + gap_at + g] = a.weights ? a.decay * a.weights[stream0 + gap_at + g] : 0.f;
     }
     if (T <= 0) return;
@@ -203,25 +234,26 @@ __global__ void __launch_bounds__(NT, 1) key_weights_kernel(const WeightArgs a) 
         return;
     }
 
-    if (warp == 4) {
+    if (warp == MMA_WARP) {
         tmem_alloc(&M->tmem, TMEM_COLS);
         tmem_relinquish();
-    } else if (tid == 5 * 32) {
-        for (int i = 0; i < STAGES; ++i) {
-            mbar_init(&M->bars[B_KV_FULL + i], FP8 ? GATHER_WARPS : 32 * GATHER_WARPS);
+    } else if (tid == (MMA_WARP + 1) * 32) {
+        for (int i = 0; i < S::STAGES; ++i) {
+            mbar_init(&M->bars[B_KV_FULL + i], 32 * GATHER_WARPS);
             mbar_init(&M->bars[B_KV_EMPTY + i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&M->bars[B_S_FULL + i], 1);
-            mbar_init(&M->bars[B_S_FREE + i], 4);
+            mbar_init(&M->bars[B_S_FULL + i], 2);
+            mbar_init(&M->bars[B_S_FREE + i], SCORE_WARPS / 2);
         }
-        mbar_init(&M->bars[B_Q_FULL], 8);
+        mbar_init(&M->bars[B_Q_FULL], SCORE_WARPS);
         M->abort = 0;
         mbar_init_fence();
     }
 
-    // ---- Q rows warp, warp + 24, warp + 48 and so on into stages 1 to 3 (chunks of 128 rows of 128 B, swizzled)
-    uint8_t* const q_tmp = smem + STAGE_BYTES;
+    // ---- Q rows warp, warp + 24, warp + 48 and so on, in chunks of 128 rows of 128 B, swizzled: fp8 four chunks
+    // of h, four of l and the rotated part in bf16, else nine chunks of 64 dims
+    uint8_t* const q_tmp = smem + Q_STAGE * S::STAGE_BYTES;
     const __nv_bfloat16* q0 = a.q + ((int64_t)b * rows + row0) * D_QK;
     for (int first = warp; first < nrows; first += 3 * (NT / 32)) {
         uint4 v[3][3];
@@ -232,16 +264,22 @@ __global__ void __launch_bounds__(NT, 1) key_weights_kernel(const WeightArgs a) 
         for (int u = 0; u < 3; ++u) {
             const int rr = first + u * (NT / 32);
             if (rr >= nrows) break;
-            const float mul = FP8 ? __int_as_float((14 - exps[u] + 127) << 23) : 1.f;
-            if (FP8 && lane == 0) M->row_exp[rr] = __int_as_float((exps[u] - 14 + 127) << 23);
+            const float mul = FP8 ? __int_as_float((7 - exps[u] + 127) << 23) : 1.f;
+            if (FP8 && lane == 0) M->row_exp[rr] = __int_as_float((exps[u] - 7 + 127) << 23);
 #pragma unroll
             for (int c = 0; c < 3; ++c) {
                 const int pc = c * 32 + lane;
                 if (pc >= 72) break;
-                uint4 o = v[u][c];
-                if (FP8 && pc < 64) o = make_uint4(q_to_f16(o.x, mul), q_to_f16(o.y, mul), q_to_f16(o.z, mul), q_to_f16(o.w, mul));
-                else if (FP8) o = make_uint4(q_to_bf16(o.x, mul), q_to_bf16(o.y, mul), q_to_bf16(o.z, mul), q_to_bf16(o.w, mul));
-                *reinterpret_cast<uint4*>(q_tmp + (pc >> 3) * Q_CHUNK + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4)) = o;
+                const uint4 o = v[u][c];
+                if (FP8 && pc < 64) {
+                    const uint32_t x = q_pieces(o.x, mul), y = q_pieces(o.y, mul), z = q_pieces(o.z, mul), w = q_pieces(o.w, mul);
+                    uint8_t* at = q_tmp + (pc >> 4) * Q_CHUNK + rr * 128 + ((((pc & 15) >> 1) ^ (rr & 7)) << 4) + (pc & 1) * 8;
+                    *reinterpret_cast<uint2*>(at) = make_uint2(__byte_perm(x, y, 0x5410), __byte_perm(z, w, 0x5410));
+                    *reinterpret_cast<uint2*>(at + 4 * Q_CHUNK) = make_uint2(__byte_perm(x, y, 0x7632), __byte_perm(z, w, 0x7632));
+                } else {
+                    *reinterpret_cast<uint4*>(q_tmp + (pc >> 3) * Q_CHUNK + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4)) =
+                        FP8 ? make_uint4(q_to_bf16(o.x, mul), q_to_bf16(o.y, mul), q_to_bf16(o.z, mul), q_to_bf16(o.w, mul)) : o;
+                }
             }
         }
     }
@@ -249,14 +287,15 @@ __global__ void __launch_bounds__(NT, 1) key_weights_kernel(const WeightArgs a) 
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = M->tmem;
+    const int quad = warp & 3;                           // TMEM lane quadrant of this warp
+    const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
 
-    if (warp < 8) {
-        // ---- Q to TMEM: warps w and w + 4 the rows of quadrant w, chunks in turn
-        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const int r = (warp & 3) * 32 + lane;
-        if ((warp & 3) * 32 < nrows) {
+    if (warp < SCORE_WARPS) {
+        // ---- Q to TMEM: a quadrant's four warps take its chunks in turn
+        const int r = quad * 32 + lane;
+        if (quad * 32 < nrows) {
 #pragma unroll 1
-            for (int c = warp >> 2; c < NCHUNK; c += 2) {
+            for (int c = warp >> 2; c < Q_CHUNKS; c += SCORE_WARPS / 4) {
                 uint32_t h[32];
                 const uint8_t* src = q_tmp + c * Q_CHUNK + r * 128;
 #pragma unroll
@@ -273,165 +312,120 @@ __global__ void __launch_bounds__(NT, 1) key_weights_kernel(const WeightArgs a) 
         if (lane == 0) mbar_arrive(&M->bars[B_Q_FULL]);
     }
 
-    if (warp == 4) {
-        // ================= A and C =================
-        const uint32_t id_a = FP8 ? idesc_f16(128, NK, false, false) : idesc_bf16(128, NK, false, false);
-        const uint32_t id_c = idesc_bf16(128, NK, false, false);
+    if (warp == MMA_WARP) {
+        // ================= scores =================
+        const uint32_t id_f8 = idesc_e4m3(128, NK), id_bf = idesc_bf16(128, NK, false, false);
         const uint64_t dk = smem_desc_sw128(smem_u32(smem), 16, 1024);
         bool ok = mbar_wait_warp(&M->bars[B_Q_FULL], 0, &M->abort);
-        int i = 0;                                       // tiles issued
+        int i = 0, st = 0;                               // tiles issued, stage
+        uint32_t round = 0;
         for (; i < T && ok; ++i) {
-            const int st = i % STAGES;
-            ok = mbar_wait_warp(&M->bars[B_KV_FULL + st], (i / STAGES) & 1, &M->abort);
-            if (ok && i >= 2) ok = mbar_wait_warp(&M->bars[B_S_FREE + (i & 1)], ((i - 2) / 2) & 1, &M->abort);
+            ok = mbar_wait_warp(&M->bars[B_KV_FULL + st], round, &M->abort);
+            if (ok && i >= 2) ok = mbar_wait_warp(&M->bars[B_S_FREE + (i & 1)], ((i - 2) >> 1) & 1, &M->abort);
             if (!ok) break;
-            fence_proxy_async_smem();                    // keys (generic proxy) -> tensor-core reads
+            fence_proxy_async_smem();                    // cp.async (generic proxy) data -> tensor-core reads
             tc_fence_after();
-            const uint64_t st16 = (uint64_t)(st * STAGE_BYTES) >> 4;
+            const uint64_t kd0 = dk + ((uint64_t)(st * S::STAGE_BYTES) >> 4);
             const uint32_t d = tmem + D_COL + (i & 1) * D_STEP;
             if (elect_one()) {
+                if (FP8) {
 #pragma unroll
-                for (int ks = 0; ks < D_QK / 16; ++ks) {
-                    const int c = ks >> 2;
-                    const uint64_t kd = dk + st16 + (uint32_t)((c * REGION + (ks & 3) * 32) >> 4);
-                    if (FP8 && c == NCHUNK - 1) mma_bf16_ta(d + NK, tmem + ks * 8, kd, id_c, (ks & 3) > 0);
-                    else mma_bf16_ta(d, tmem + ks * 8, kd, id_a, ks > 0);
+                    for (int ks = 0; ks < D_V / 32; ++ks) {
+                        const uint64_t kd = kd0 + (uint32_t)(((ks >> 2) * REGION + (ks & 3) * 32) >> 4);
+                        mma_f8_ta(d, tmem + ks * 8, kd, id_f8, ks > 0);
+                        mma_f8_ta(d + NK, tmem + 128 + ks * 8, kd, id_f8, ks > 0);
+                    }
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_bf16_ta(d + 2 * NK, tmem + 256 + ks * 8, kd0 + (uint32_t)((4 * REGION + ks * 32) >> 4), id_bf, ks > 0);
+                } else {
+#pragma unroll
+                    for (int ks = 0; ks < D_QK / 16; ++ks)
+                        mma_bf16_ta(d, tmem + ks * 8, kd0 + (uint32_t)(((ks >> 2) * REGION + (ks & 3) * 32) >> 4), id_bf, ks > 0);
                 }
                 mma_commit(&M->bars[B_KV_EMPTY + st]);
                 mma_commit(&M->bars[B_S_FULL + (i & 1)]);
+                mbar_arrive(&M->bars[B_S_FULL + (i & 1)]);   // hands on what came with the keys: scales, positions
             }
             __syncwarp();
+            if (++st == S::STAGES) { st = 0; round ^= 1; }
         }
         if (!ok) {
             if (lane == 0) give_up(M, a.status);
-            if (i > 0) mbar_drain(&M->bars[B_S_FULL + ((i - 1) & 1)], ((i - 1) / 2) & 1);
+            if (i > 0) mbar_drain(&M->bars[B_S_FULL + ((i - 1) & 1)], ((i - 1) >> 1) & 1);
         }
         __syncwarp();
     } else if (warp >= GATHER0) {
-        // ================= gather: keys WK w .. WK w + 2 of every tile =================
+        // ================= gather: keys WK w .. WK w + 7 of every tile =================
         const int w = warp - GATHER0;
         bool bad_slot = false;
         const int32_t* slot_row = a.slot + stream0;
-        // key l & 3 of tile t (past the range: its last key), and its index in the stream
+        // key l & 7 of tile t (past the range: its last key), as an index in the stream
         auto key_at = [&](int t) -> int {
-            const int v = min(k_begin + t * NK + WK * w + min(lane & 3, WK - 1), k_end - 1);
+            const int v = min(k_begin + t * NK + WK * w + (lane & 7), k_end - 1);
             return RULES && v >= gap_at ? v + gap : v;
         };
-        // lane l holds the slot of key l & 3 of tile t0 + (l >> 2), for the current group of eight tiles and
+        // lane l holds the slot of key l & 7 of tile t0 + (l >> 3), for the current group of four tiles and
         // the next; indices are checked when their group becomes current
         auto load_slots = [&](int t0) -> int {
-            const int t = t0 + (lane >> 2);
+            const int t = t0 + (lane >> 3);
             return t < T ? __ldg(slot_row + key_at(t)) : 0;
         };
-        int cur = load_slots(0), nxt = load_slots(8);
-        auto slots_of = [&](int j) -> int {
-            if ((j & 7) == 0) {
-                if (j > 0) {
+        int cur = load_slots(0), nxt = load_slots(4), st = 0, ring = 0;
+        uint32_t round = 1;                              // (the wait for a fresh stage passes at once)
+        for (int i = 0; i < T; ++i) {
+            if ((i & 3) == 0) {
+                if (i > 0) {
                     cur = nxt;
-                    nxt = load_slots(j + 8);
+                    nxt = load_slots(i + 4);
                 }
                 if (cur < 0 || (int64_t)cur >= a.n_pool) { bad_slot = true; cur = 0; }
             }
-            return __shfl_sync(0xffffffffu, cur, ((j & 7) << 2) + (lane & 3));
-        };
-        // the stage is free: its products are done, and Q has left it
-        auto stage_free = [&](int i) -> bool {
-            if ((i >= STAGES && !mbar_wait_warp(&M->bars[B_KV_EMPTY + i % STAGES], ((i - STAGES) / STAGES) & 1, &M->abort)) ||
-                (i == 1 && !mbar_wait_warp(&M->bars[B_Q_FULL], 0, &M->abort))) {
+            const int sl = __shfl_sync(0xffffffffu, cur, ((i & 3) << 3) + (lane & 7));
+            // the stage is free: its products are done, and Q has left it
+            if (!mbar_wait_warp(&M->bars[B_KV_EMPTY + st], round, &M->abort) ||
+                (i == Q_STAGE && !mbar_wait_warp(&M->bars[B_Q_FULL], 0, &M->abort))) {
                 if (lane == 0) give_up(M, a.status);
-                return false;
+                break;
             }
-            return true;
-        };
-        if constexpr (FP8) {
-            struct Raw {
-                uint4 lat[WK], rope;
-                float scale;
-                int pos, doc;                            // RULES
-            };
-            auto load_tile = [&](Raw& r, int j) {
-                if (j >= T) return;
-                const int sl = slots_of(j);
+            const uint32_t base = smem_u32(smem) + st * S::STAGE_BYTES;
+            if (FP8) {
 #pragma unroll
-                for (int it = 0; it < WK; ++it)
-                    r.lat[it] = ld_stream(reinterpret_cast<const uint4*>(a.lat + (int64_t)__shfl_sync(0xffffffffu, sl, it) * D_V) + lane);
-                const int rs = __shfl_sync(0xffffffffu, sl, lane >> 3);
-                if (lane < 8 * WK) r.rope = ld_stream(reinterpret_cast<const uint4*>(a.rope + (int64_t)rs * 64) + (lane & 7));
-                r.scale = __ldg(a.kscale + sl);
-                if (RULES) {
-                    if (a.rules.key_pos) r.pos = __ldg(a.rules.key_pos + stream0 + key_at(j));
-                    if (a.rules.key_doc) r.doc = __ldg(a.rules.key_doc + stream0 + key_at(j));
-                }
-            };
-            // lane l widens dims 16 l .. 16 l + 15: 16-byte pieces j0, j0 + 1 of region l / 4.  Lanes of odd
-            // regions store their second piece first, so each store covers all eight 16-byte bank groups.
-            const int region = lane >> 2, j0 = (lane & 3) * 2, odd = region & 1;
-            auto widen_tile = [&](const Raw& r, int i) -> bool {
-                if (!stage_free(i)) return false;
-                const int st = i % STAGES;
-                uint8_t* base = smem + st * STAGE_BYTES;
-#pragma unroll
-                for (int it = 0; it < WK; ++it) {
+                for (int it = 0; it < WK; ++it) {        // lane l takes 16-byte piece l of a row's codes
                     const int key = WK * w + it;
-                    const uint2 h0 = widen4(r.lat[it].x), h1 = widen4(r.lat[it].y), h2 = widen4(r.lat[it].z), h3 = widen4(r.lat[it].w);
-                    const uint4 lo = make_uint4(h0.x, h0.y, h1.x, h1.y), hi = make_uint4(h2.x, h2.y, h3.x, h3.y);
-                    uint8_t* row = base + region * REGION + key * 128;
-                    *reinterpret_cast<uint4*>(row + (((j0 + odd) ^ (key & 7)) << 4)) = odd ? hi : lo;
-                    *reinterpret_cast<uint4*>(row + (((j0 + 1 - odd) ^ (key & 7)) << 4)) = odd ? lo : hi;
+                    cp_async16(base + (lane >> 3) * REGION + key * 128 + (((lane & 7) ^ (key & 7)) << 4),
+                               a.lat + (int64_t)__shfl_sync(0xffffffffu, sl, it) * D_V + lane * 16);
                 }
-                if (lane < 8 * WK) {
-                    const int key = WK * w + (lane >> 3);
-                    *reinterpret_cast<uint4*>(base + (NCHUNK - 1) * REGION + key * 128 + (((lane & 7) ^ (key & 7)) << 4)) = r.rope;
-                }
-                if (lane < WK) {
-                    M->key_scale[i % RING][WK * w + lane] = r.scale >= 0.f ? r.scale : __int_as_float(0x7fc00000);
-                    if (RULES) {
-                        M->key_pos[i % RING][WK * w + lane] = a.rules.key_pos ? r.pos : key_at(i);
-                        M->key_doc[i % RING][WK * w + lane] = a.rules.key_doc ? r.doc : -1;
-                    }
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0 && !(a.debug_stall && i == 0)) mbar_arrive(&M->bars[B_KV_FULL + st]);
-                return true;
-            };
-            Raw r0, r1;
-            load_tile(r0, 0);
-            load_tile(r1, 1);
-            for (int i = 0; i < T; i += 2) {
-                if (!__all_sync(0xffffffffu, widen_tile(r0, i))) break;
-                load_tile(r0, i + 2);
-                if (i + 1 >= T) break;
-                if (!__all_sync(0xffffffffu, widen_tile(r1, i + 1))) break;
-                load_tile(r1, i + 3);
-            }
-        } else {
-            for (int i = 0; i < T; ++i) {
-                const int sl = slots_of(i), st = i % STAGES;
-                if (!__all_sync(0xffffffffu, stage_free(i))) break;
-                const uint32_t base = smem_u32(smem) + st * STAGE_BYTES;
 #pragma unroll
-                for (int it = 0; it < (WK * 72 + 31) / 32; ++it) {
-                    const int f = it * 32 + lane, kk = min(f / 72, WK - 1), pc = f % 72, key = WK * w + kk;
-                    const int row_slot = __shfl_sync(0xffffffffu, sl, kk);
-                    if (f < WK * 72)
-                        cp_async16(base + (pc >> 3) * REGION + key * 128 + (((pc & 7) ^ (key & 7)) << 4),
-                                   a.kv + (int64_t)row_slot * D_QK + pc * 8);
+                for (int it = 0; it < WK / 4; ++it) {    // and of four rows' rotated parts
+                    const int kk = it * 4 + (lane >> 3), key = WK * w + kk;
+                    cp_async16(base + 4 * REGION + key * 128 + (((lane & 7) ^ (key & 7)) << 4),
+                               a.rope + (int64_t)__shfl_sync(0xffffffffu, sl, kk) * 64 + (lane & 7) * 8);
                 }
-                if (RULES && lane < WK) {
-                    if (a.rules.key_pos) cp_async4(smem_u32(&M->key_pos[i % RING][WK * w + lane]), a.rules.key_pos + stream0 + key_at(i));
-                    if (a.rules.key_doc) cp_async4(smem_u32(&M->key_doc[i % RING][WK * w + lane]), a.rules.key_doc + stream0 + key_at(i));
+                if (lane < WK) cp_async4(smem_u32(&M->key_scale[ring][WK * w + lane]), a.kscale + sl);
+            } else {
+#pragma unroll
+                for (int it = 0; it < WK * 72 / 32; ++it) {
+                    const int f = it * 32 + lane, kk = f / 72, pc = f % 72, key = WK * w + kk;
+                    cp_async16(base + (pc >> 3) * REGION + key * 128 + (((pc & 7) ^ (key & 7)) << 4),
+                               a.kv + (int64_t)__shfl_sync(0xffffffffu, sl, kk) * D_QK + pc * 8);
                 }
-                if (!(a.debug_stall && i == 0)) cp_async_arrive_noinc(&M->bars[B_KV_FULL + st]);
             }
-            cp_async_wait_all();
+            if (RULES && lane < WK) {
+                const int64_t at = stream0 + key_at(i);
+                if (a.rules.key_pos) cp_async4(smem_u32(&M->key_pos[ring][WK * w + lane]), a.rules.key_pos + at);
+                if (a.rules.key_doc) cp_async4(smem_u32(&M->key_doc[ring][WK * w + lane]), a.rules.key_doc + at);
+            }
+            if (!(a.debug_stall && i == 0)) cp_async_arrive_noinc(&M->bars[B_KV_FULL + st]);
+            if (++st == S::STAGES) { st = 0; round ^= 1; }
+            if (++ring == RING) ring = 0;
         }
+        cp_async_wait_all();
         if (bad_slot) atomicOr(a.status, DEV_BAD_SLOT);
-    } else if (warp < 4) {
-        // ================= weights =================
-        const int r = warp * 32 + lane;                  // query row of this thread (lane of A and C)
-        const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-        const bool row_ok = r < nrows, rows_used = warp * 32 < nrows;
+    } else if (warp < SCORE_WARPS) {
+        // ================= weights: rows of quadrant `quad`, keys 16 g .. 16 g + 15 of every second tile =================
+        const int set = warp >> 3, g = (warp >> 2) & 1, r = quad * 32 + lane;
+        const bool row_ok = r < nrows, rows_used = quad * 32 < nrows, writer = (warp & 7) == 0;
         const int t = row_ok ? (row0 + r) / a.H : 0;
         const float lse = row_ok ? a.lse[(int64_t)b * rows + row0 + r] : 0.f;
         const bool live = row_ok && lse != -INFINITY && (!a.counted || a.counted[(int64_t)b * a.q_len + t]);
@@ -454,83 +448,88 @@ __global__ void __launch_bounds__(NT, 1) key_weights_kernel(const WeightArgs a) 
         if (RULES) rule = a.rules.row(b, t, row_ok ? (row0 + r) % a.H : 0, p + gap, a.slot_stride, false);
         const float cap_in = RULES && a.rules.softcap > 0.f ? 2.f * c2 / a.rules.softcap : 0.f;
         const float cap_out = RULES ? a.rules.softcap * LOG2E : 0.f;
-        for (int i = 0; i < T; ++i) {
-            const int buf = i & 1, k0 = k_begin + i * NK;
-            // the key that this thread writes, and its former weight
-            const int v = k0 + tid;
+        int ring = set;
+        for (int i = set; i < T; i += 2) {
+            const int k0 = k_begin + i * NK;
+            // the key that this lane of the set's first warp writes, and its former weight
+            const int v = k0 + lane;
             const int64_t at = stream0 + (RULES && v >= gap_at ? v + gap : v);
-            const bool mine = tid < NK && v < k_end;
-            float old = 0.f;
-            if (direct && mine && a.weights && v < p) old = a.weights[at];
-            const bool ok = mbar_wait_warp(&M->bars[B_S_FULL + buf], (i / 2) & 1, &M->abort);
+            const bool mine = writer && v < k_end, has_old = mine && direct && a.weights && v < p;
+            const float old = has_old ? a.weights[at] : 0.f;
+            float(*const sums)[NK] = M->sums[set][(i >> 1) & 1];
+            const bool ok = mbar_wait_warp(&M->bars[B_S_FULL + set], (i >> 1) & 1, &M->abort);
             tc_fence_after();
-            if (ok && rows_used) {
+            if (ok && any_live) {
+                uint32_t va[16], vl[16], vc[16];
+                const uint32_t d = tmem + lane_base + D_COL + set * D_STEP + 16 * g;
+                tmem_ld16(d, va);
+                if (FP8) {
+                    tmem_ld16(d + NK, vl);
+                    tmem_ld16(d + 2 * NK, vc);
+                }
+                tmem_ld_wait();
+                float e[16];
+                const int kg = k0 + 16 * g;
+                const float* ks = M->key_scale[ring] + 16 * g;
 #pragma unroll
-                for (int g = 0; g < NK / 16; ++g) {
-                    uint32_t va[16], vc[16];
-                    const uint32_t d = tmem + lane_base + D_COL + buf * D_STEP + 16 * g;
-                    tmem_ld16(d, va);
-                    if (FP8) tmem_ld16(d + NK, vc);
-                    tmem_ld_wait();
-                    float e[16];
-                    const int kg = k0 + 16 * g;
-                    const float* ks = M->key_scale[i % RING] + 16 * g;
+                for (int k = 0; k < 16; ++k) {
+                    float dot = __uint_as_float(va[k]);
+                    if (FP8) dot = fmaf(fmaf(__uint_as_float(vl[k]), 0.03125f, dot), ks[k], __uint_as_float(vc[k]));
+                    float x;
+                    if (RULES) {
+                        x = a.rules.softcap > 0.f ? fmaf(capped(dot * cap_in), cap_out, off) : fmaf(dot, c2, off);
+                        if (a.rules.slopes) {
+                            const int kp = a.rules.key_pos ? M->key_pos[ring][16 * g + k] : kg + k + (kg + k >= gap_at ? gap : 0);
+                            x = fmaf((float)(kp - rule.pos), rule.slope, x);
+                        }
+                    } else {
+                        x = fmaf(dot, c2, off);
+                    }
+                    e[k] = live ? ex2(x) : 0.f;
+                }
+                if (RULES && a.rules.masked) {
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        const float dot = FP8 ? fmaf(__uint_as_float(va[k]), ks[k], __uint_as_float(vc[k])) : __uint_as_float(va[k]);
-                        float x;
-                        if (RULES) {
-                            x = a.rules.softcap > 0.f ? fmaf(capped(dot * cap_in), cap_out, off) : fmaf(dot, c2, off);
-                            if (a.rules.slopes) {
-                                const int kp = FP8 || a.rules.key_pos ? M->key_pos[i % RING][16 * g + k]
-                                                                      : (kg + k >= gap_at ? kg + k + gap : kg + k);
-                                x = fmaf((float)(kp - rule.pos), rule.slope, x);
-                            }
-                        } else {
-                            x = fmaf(dot, c2, off);
-                        }
-                        e[k] = live ? ex2(x) : 0.f;
+                        const int j = kg + k - p;        // draft index, < 0: before the drafts
+                        const int kp = a.rules.key_pos ? M->key_pos[ring][16 * g + k] : kg + k + (kg + k >= gap_at ? gap : 0);
+                        const int kd = a.rules.key_doc ? M->key_doc[ring][16 * g + k] : -1;
+                        if (!rule.sees(j < 0 || ((vis >> (j & 63)) & 1ull), kp, kd)) e[k] = 0.f;
                     }
-                    if (RULES && a.rules.masked) {
+                } else if (kg + 16 > p) {
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const int j = kg + k - p;    // draft index, < 0: before the drafts
-                            const int kp = FP8 || a.rules.key_pos ? M->key_pos[i % RING][16 * g + k]
-                                                                  : (kg + k >= gap_at ? kg + k + gap : kg + k);
-                            const int kd = FP8 || a.rules.key_doc ? M->key_doc[i % RING][16 * g + k] : -1;
-                            if (!rule.sees(j < 0 || ((vis >> (j & 63)) & 1ull), kp, kd)) e[k] = 0.f;
-                        }
-                    } else if (kg + 16 > p) {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const int j = kg + k - p;
-                            if (j >= 0 && !((vis >> (j & 63)) & 1ull)) e[k] = 0.f;
-                        }
+                    for (int k = 0; k < 16; ++k) {
+                        const int j = kg + k - p;
+                        if (j >= 0 && !((vis >> (j & 63)) & 1ull)) e[k] = 0.f;
                     }
-                    const float s = any_live ? sum_rows(e) : 0.f;
-                    if ((lane & 1) == 0) M->sums[buf][warp][16 * g + (lane >> 1)] = s;
                 }
                 tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&M->bars[B_S_FREE + set]);
+                const float s = sum_rows(e);
+                if ((lane & 1) == 0) sums[quad][16 * g + (lane >> 1)] = s;
+            } else {
+                if (rows_used && (lane & 1) == 0) sums[quad][16 * g + (lane >> 1)] = 0.f;
+                __syncwarp();
+                if (ok && lane == 0) mbar_arrive(&M->bars[B_S_FREE + set]);
             }
-            __syncwarp();
-            if (ok && lane == 0) mbar_arrive(&M->bars[B_S_FREE + buf]);
-            if (bar_red_or(1, 128, !ok)) {               // the sums are there, or a warp gives up
+            if (bar_red_or(1 + set, 32 * SCORE_WARPS / 2, !ok)) {   // the sums are there, or a warp gives up
                 if (!ok && lane == 0) give_up(M, a.status);
                 break;
             }
             if (mine) {
-                float s = M->sums[buf][0][tid];
+                float s = sums[0][lane];
 #pragma unroll
                 for (int q = 1; q < 4; ++q)
-                    if (q * 32 < nrows) s += M->sums[buf][q][tid];
-                part[at] = direct && a.weights && v < p ? fmaf(a.decay, old, s) : s;
+                    if (q * 32 < nrows) s += sums[q][lane];
+                part[at] = has_old ? fmaf(a.decay, old, s) : s;
             }
+            ring = ring + 2 >= RING ? ring + 2 - RING : ring + 2;
         }
     }
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 4) {
+    if (warp == MMA_WARP) {
         tc_fence_after();
         tmem_dealloc(tmem, TMEM_COLS);
     }
@@ -578,11 +577,11 @@ cudaError_t launch_weights(const WeightArgs& a, dim3 grid, int dev, cudaStream_t
     auto* k = key_weights_kernel<FP8, RULES>;
     static std::atomic<bool> attr_set[64];
     if (!attr_set[dev].load(std::memory_order_acquire)) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<FP8>());
         if (e != cudaSuccess) return e;
         attr_set[dev].store(true, std::memory_order_release);
     }
-    return launch_dependent(k, grid, dim3(NT), (size_t)SMEM, stream, a);
+    return launch_dependent(k, grid, dim3(NT), (size_t)smem_bytes<FP8>(), stream, a);
 }
 
 template <bool FP8>
