@@ -20,7 +20,9 @@
 //   scores   tcgen05.mma M=128 (query rows) x N=32 (keys), Q from TMEM
 //   weights  sixteen warps, a thread a query row and 16 keys, in two sets that take tiles in turn:
 //            exp2(c z - lse), then the sum over a warp's 32 rows by halving exchanges (16 keys in 16
-//            shuffles), the four warps' sums in shared memory
+//            shuffles), the four warps' sums in shared memory.  Up to 64 rows stand in TMEM twice, and
+//            a thread takes 8 keys: a warp reaches one quadrant of the lanes only, the one of its own
+//            scheduler, and two of the four schedulers would have nothing to do
 // More than 128 rows: a row tile a CTA, whose sums meet in the workspace (4 bytes a key and row tile; a
 // second small kernel adds them in order).  Sums have a fixed order: equal calls give equal bits.
 #include "../../include/mla_verify.h"
@@ -42,13 +44,14 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr int NK = 32;                               // keys per tile
 constexpr int MAX_R = 128;                           // query rows per CTA
 constexpr int NT = 768;
-constexpr int SCORE_WARPS = 16, MMA_WARP = 16, GATHER0 = 20, GATHER_WARPS = 4;   // (17 to 19 only bring Q)
+constexpr int SCORE_WARPS = 16, MMA_WARP = 16, GATHER0 = 20, GATHER_WARPS = 4;   // (18 and 19 only bring Q)
 constexpr int WK = NK / GATHER_WARPS;                // keys of a tile per gather warp
 constexpr int MAX_STAGES = 10;
-constexpr int RING = MAX_STAGES + 2;                 // what belongs to a key outlives its stage by the two tiles of scores
+// What belongs to a key outlives its stage: a set reads it after it has freed the scores for the tile after
+// next, whose products let the gather go on to the tile a ring further.
+constexpr int RING = MAX_STAGES + 4;
 constexpr int REGION = NK * 128;                     // one 128-byte chunk of a stage's rows
-constexpr int Q_CHUNKS = 9, Q_CHUNK = MAX_R * 128;   // Q on its way to TMEM lies in the stages from the third on
-constexpr int Q_STAGE = 2;
+constexpr int Q_CHUNKS = 9;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int D_COL = Q_CHUNKS * 32, D_STEP = 3 * NK;  // scores of tile i at D_COL + (i & 1) D_STEP: H, L, C
 static_assert(D_COL + 2 * D_STEP <= (int)TMEM_COLS, "TMEM");
@@ -57,7 +60,12 @@ static_assert(D_COL + 2 * D_STEP <= (int)TMEM_COLS, "TMEM");
 template <bool FP8>
 struct Shape {
     static constexpr int CHUNKS = FP8 ? 5 : 9, STAGES = FP8 ? MAX_STAGES : 6, STAGE_BYTES = CHUNKS * REGION;
-    static_assert(Q_CHUNKS * Q_CHUNK <= (STAGES - Q_STAGE) * STAGE_BYTES, "Q's way station");
+    // Q on its way to TMEM lies in the stages from this one on, in chunks of whole groups of eight rows
+    static __device__ __forceinline__ int q_stage(int nrows) {
+        return STAGES - (Q_CHUNKS * ((nrows + 7) / 8) * 1024 + STAGE_BYTES - 1) / STAGE_BYTES;
+    }
+    static_assert(STAGES % 2 == 0, "two warps take them in turn");
+    static_assert(Q_CHUNKS * MAX_R * 128 <= (STAGES - 2) * STAGE_BYTES, "Q's way station");
 };
 
 enum { B_KV_FULL = 0, B_KV_EMPTY = B_KV_FULL + MAX_STAGES, B_S_FULL = B_KV_EMPTY + MAX_STAGES, B_S_FREE = B_S_FULL + 2,
@@ -158,40 +166,85 @@ __device__ __forceinline__ void balanced_range(const WeightArgs& a, int S, int x
     }
 }
 
-// Sums of e[k] over the warp's lanes: lane 2 k (and 2 k + 1) ends up with key k's.
-__device__ __forceinline__ float sum_rows(float (&e)[16]) {
+// Sums of e[k], k < N, over the warp's lanes: lane l ends up with key (l N) / 32's.
+template <int N>
+__device__ __forceinline__ float sum_rows(float (&e)[N]) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int half = 8; half > 0; half >>= 1) {
-        const bool up = lane & (2 * half);
+    for (int half = N / 2, with = 16; half > 0; half >>= 1, with >>= 1) {
+        const bool up = lane & with;
 #pragma unroll
         for (int i = 0; i < half; ++i) {
             const float send = up ? e[i] : e[i + half], keep = up ? e[i + half] : e[i];
-            e[i] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * half);
+            e[i] = keep + __shfl_xor_sync(0xffffffffu, send, with);
         }
     }
-    return e[0] + __shfl_xor_sync(0xffffffffu, e[0], 1);
+    float s = e[0];
+#pragma unroll
+    for (int with = 16 / N; with > 0; with >>= 1) s += __shfl_xor_sync(0xffffffffu, s, with);
+    return s;
 }
+
+// N (8 or 16) consecutive TMEM columns.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[8]) { tmem_ld8(taddr, r); }
 
 __device__ __forceinline__ void give_up(Misc* M, unsigned* status) {
     if (atomicExch(const_cast<int*>(&M->abort), 1) == 0) atomicOr(status, DEV_TIMEOUT);
 }
 
 // Two bf16 values (one word) of a row times f, a power of two, as two e4m3 pieces: the bytes of h in the low
-// half, those of l = 2^5 (q - h) in the high half.  What is not finite becomes NaN.
-__device__ __forceinline__ uint32_t q_pieces(uint32_t w, float f) {
-    const float x0 = __uint_as_float(w << 16) * f, x1 = __uint_as_float(w & 0xffff0000u) * f;
-    const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
-    const __half2 back = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h, __NV_E4M3));
-    const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2((x0 - __low2float(back)) * 32.f, (x1 - __high2float(back)) * 32.f),
-                                                __NV_SATFINITE, __NV_E4M3);
-    uint32_t both = h | (l << 16);
-    if (!(fabsf(x0) < 448.f)) both |= 0x007f007fu;
-    if (!(fabsf(x1) < 448.f)) both |= 0x7f007f00u;
-    return both;
+// half, those of l = 2^5 (q - h) in the high half.  On the way they are fp16, which holds them to 2^-25.
+__device__ __forceinline__ uint32_t q_pieces(uint32_t w, __nv_bfloat162 f) {
+    const __nv_bfloat162 q = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), f);
+    const __half2 x = __floats2half2_rn(__low2float(q), __high2float(q));
+    const uint32_t h = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
+    const __half2 rest = __hsub2(x, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h, __NV_E4M3)));
+    const __half2 up = __hmul2(rest, __float2half2_rn(32.f));
+    const uint32_t l = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(up), __NV_SATFINITE, __NV_E4M3);
+    return h | (l << 16);
 }
 
-template <bool FP8, bool RULES>
+// One query row in its place in shared memory, chunk c's 128 bytes at row + c * q_chunk (16-byte pieces swizzled
+// by `swz`), from nine chunks of 64 bf16 dims to four chunks of h, four of l and the rotated part; the power
+// of two that it was divided by.  Whole warp.  A row with an infinity or a NaN becomes NaN.
+__device__ __forceinline__ float convert_row(uint8_t* row, int q_chunk, int swz) {
+    const int lane = threadIdx.x & 31;
+    uint4 v[1][3];
+#pragma unroll
+    for (int c = 0; c < 3; ++c) {
+        const int pc = c * 32 + lane;
+        v[0][c] = pc < 72 ? *reinterpret_cast<const uint4*>(row + (pc >> 3) * q_chunk + (((pc & 7) ^ swz) << 4)) : make_uint4(0, 0, 0, 0);
+    }
+    int e[1];
+    row_exponents<1>(v, e);
+    const uint32_t top = (uint32_t)(7 - e[0] + 127);
+    // (an exponent of 127 is that of 2^127 or of what is not finite)
+    const bool bad = e[0] == 127 && __any_sync(0xffffffffu, not_finite(v[0][0]) || not_finite(v[0][1]) || not_finite(v[0][2]));
+    const uint32_t fw = (top << 23 | top << 7) & 0xffffff80u, spoil = bad ? 0x7f7f7f7fu : 0u;
+    const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162*>(&fw);
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const int pc = c * 32 + lane;
+        const uint4 o = v[0][c];
+        const uint32_t x = q_pieces(o.x, f) | spoil, y = q_pieces(o.y, f) | spoil, z = q_pieces(o.z, f) | spoil,
+                       w = q_pieces(o.w, f) | spoil;
+        uint8_t* at = row + (pc >> 4) * q_chunk + ((((pc & 15) >> 1) ^ swz) << 4) + (pc & 1) * 8;
+        *reinterpret_cast<uint2*>(at) = make_uint2(__byte_perm(x, y, 0x5410), __byte_perm(z, w, 0x5410));
+        *reinterpret_cast<uint2*>(at + 4 * q_chunk) = make_uint2(__byte_perm(x, y, 0x7632), __byte_perm(z, w, 0x7632));
+    }
+    if (lane < 8) {
+        const float m = __uint_as_float(top << 23);
+        const uint4 o = v[0][2];
+        *reinterpret_cast<uint4*>(row + 8 * q_chunk + ((lane ^ swz) << 4)) =
+            make_uint4(q_to_bf16(o.x, m), q_to_bf16(o.y, m), q_to_bf16(o.z, m), q_to_bf16(o.w, m));
+    }
+    return __uint_as_float((uint32_t)(e[0] - 7 + 127) << 23);
+}
+
+// KW: keys of a tile per score warp, 16, or 8 with up to 64 rows.
+template <bool FP8, bool RULES, int KW>
 __global__ void __launch_bounds__(NT, 1) key_weights_kernel(const WeightArgs a) {
     using S = Shape<FP8>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -251,108 +304,102 @@ __global__ void __launch_bounds__(NT, 1) key_weights_kernel(const WeightArgs a) 
         mbar_init_fence();
     }
 
-    // ---- Q rows warp, warp + 24, warp + 48 and so on, in chunks of 128 rows of 128 B, swizzled: fp8 four chunks
-    // of h, four of l and the rotated part in bf16, else nine chunks of 64 dims
-    uint8_t* const q_tmp = smem + Q_STAGE * S::STAGE_BYTES;
-    const __nv_bfloat16* q0 = a.q + ((int64_t)b * rows + row0) * D_QK;
-    for (int first = warp; first < nrows; first += 3 * (NT / 32)) {
-        uint4 v[3][3];
-        load_q_rows(v, q0, first, NT / 32, nrows);
-        int exps[3];
-        if (FP8) row_exponents<3>(v, exps);
-#pragma unroll
-        for (int u = 0; u < 3; ++u) {
-            const int rr = first + u * (NT / 32);
-            if (rr >= nrows) break;
-            const float mul = FP8 ? __int_as_float((7 - exps[u] + 127) << 23) : 1.f;
-            if (FP8 && lane == 0) M->row_exp[rr] = __int_as_float((exps[u] - 7 + 127) << 23);
-#pragma unroll
-            for (int c = 0; c < 3; ++c) {
-                const int pc = c * 32 + lane;
-                if (pc >= 72) break;
-                const uint4 o = v[u][c];
-                if (FP8 && pc < 64) {
-                    const uint32_t x = q_pieces(o.x, mul), y = q_pieces(o.y, mul), z = q_pieces(o.z, mul), w = q_pieces(o.w, mul);
-                    uint8_t* at = q_tmp + (pc >> 4) * Q_CHUNK + rr * 128 + ((((pc & 15) >> 1) ^ (rr & 7)) << 4) + (pc & 1) * 8;
-                    *reinterpret_cast<uint2*>(at) = make_uint2(__byte_perm(x, y, 0x5410), __byte_perm(z, w, 0x5410));
-                    *reinterpret_cast<uint2*>(at + 4 * Q_CHUNK) = make_uint2(__byte_perm(x, y, 0x7632), __byte_perm(z, w, 0x7632));
-                } else {
-                    *reinterpret_cast<uint4*>(q_tmp + (pc >> 3) * Q_CHUNK + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4)) =
-                        FP8 ? make_uint4(q_to_bf16(o.x, mul), q_to_bf16(o.y, mul), q_to_bf16(o.z, mul), q_to_bf16(o.w, mul)) : o;
-                }
-            }
-        }
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = M->tmem;
     const int quad = warp & 3;                           // TMEM lane quadrant of this warp
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+    const int r = (quad * 32 + lane) & (KW == 16 ? 127 : 63);   // query row of this lane of A and the scores
+    const int q_stage = S::q_stage(nrows);
 
-    if (warp < SCORE_WARPS) {
-        // ---- Q to TMEM: a quadrant's four warps take its chunks in turn
-        const int r = quad * 32 + lane;
-        if (quad * 32 < nrows) {
-#pragma unroll 1
-            for (int c = warp >> 2; c < Q_CHUNKS; c += SCORE_WARPS / 4) {
-                uint32_t h[32];
-                const uint8_t* src = q_tmp + c * Q_CHUNK + r * 128;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(src + ((j ^ (r & 7)) << 4));
-                    h[4 * j] = v.x; h[4 * j + 1] = v.y; h[4 * j + 2] = v.z; h[4 * j + 3] = v.w;
-                }
-                tmem_st32(tmem + lane_base + c * 32, h);
-            }
-            tmem_st_wait();
+    if (warp < GATHER0) {
+        // ---- Q's rows, in nine chunks of 64 dims, rows of 128 B, swizzled; fp8: a warp a row, in pieces
+        uint8_t* const q_tmp = smem + q_stage * S::STAGE_BYTES;
+        const int q_chunk = (nrows + 7) / 8 * 1024;
+        const __nv_bfloat16* q0 = a.q + ((int64_t)b * rows + row0) * D_QK;
+        for (int f = tid; f < nrows * 72; f += 32 * GATHER0) {
+            const int rr = f / 72, pc = f % 72;
+            cp_async16(smem_u32(q_tmp) + (pc >> 3) * q_chunk + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4), q0 + (int64_t)rr * D_QK + pc * 8);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&M->bars[B_Q_FULL]);
+        cp_async_wait_all();
+        if (FP8) {
+            bar_sync(3, 32 * GATHER0);
+#pragma unroll 1
+            for (int rr = warp; rr < nrows; rr += GATHER0) {
+                const float e = convert_row(q_tmp + rr * 128, q_chunk, rr & 7);
+                if (lane == 0) M->row_exp[rr] = e;
+            }
+        }
+        bar_sync(3, 32 * GATHER0);
+        if (warp < SCORE_WARPS) {
+            // ---- Q to TMEM: a quadrant's four warps take its chunks in turn
+            const int rr = min(r, nrows - 1);            // (lanes behind the last row: nobody reads their scores)
+            if ((r & ~31) < nrows) {
+#pragma unroll 1
+                for (int c = warp >> 2; c < Q_CHUNKS; c += SCORE_WARPS / 4) {
+                    uint32_t h[32];
+                    const uint8_t* src = q_tmp + c * q_chunk + rr * 128;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(src + ((j ^ (rr & 7)) << 4));
+                        h[4 * j] = v.x; h[4 * j + 1] = v.y; h[4 * j + 2] = v.z; h[4 * j + 3] = v.w;
+                    }
+                    tmem_st32(tmem + lane_base + c * 32, h);
+                }
+                tmem_st_wait();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&M->bars[B_Q_FULL]);
+        }
     }
 
-    if (warp == MMA_WARP) {
-        // ================= scores =================
+    if (warp == MMA_WARP || warp == MMA_WARP + 1) {
+        // ================= scores: two warps take the tiles in turn, so that one's waits pass in the other's products
         const uint32_t id_f8 = idesc_e4m3(128, NK), id_bf = idesc_bf16(128, NK, false, false);
         const uint64_t dk = smem_desc_sw128(smem_u32(smem), 16, 1024);
+        const int buf = warp - MMA_WARP;
+        const uint32_t d = tmem + D_COL + buf * D_STEP;
         bool ok = mbar_wait_warp(&M->bars[B_Q_FULL], 0, &M->abort);
-        int i = 0, st = 0;                               // tiles issued, stage
+        int i = buf, st = buf;                           // tile, stage
         uint32_t round = 0;
-        for (; i < T && ok; ++i) {
+        for (; i < T && ok; i += 2) {
             ok = mbar_wait_warp(&M->bars[B_KV_FULL + st], round, &M->abort);
-            if (ok && i >= 2) ok = mbar_wait_warp(&M->bars[B_S_FREE + (i & 1)], ((i - 2) >> 1) & 1, &M->abort);
+            if (ok && i >= 2) ok = mbar_wait_warp(&M->bars[B_S_FREE + buf], ((i - 2) >> 1) & 1, &M->abort);
             if (!ok) break;
             fence_proxy_async_smem();                    // cp.async (generic proxy) data -> tensor-core reads
             tc_fence_after();
-            const uint64_t kd0 = dk + ((uint64_t)(st * S::STAGE_BYTES) >> 4);
-            const uint32_t d = tmem + D_COL + (i & 1) * D_STEP;
+            // (the address is the descriptor's low word; shared memory's 227 KB never carry into the high one)
+            const uint32_t lo = (uint32_t)dk + (uint32_t)((st * S::STAGE_BYTES) >> 4);
+            const uint64_t hi = dk & 0xffffffff00000000ull;
             if (elect_one()) {
                 if (FP8) {
 #pragma unroll
                     for (int ks = 0; ks < D_V / 32; ++ks) {
-                        const uint64_t kd = kd0 + (uint32_t)(((ks >> 2) * REGION + (ks & 3) * 32) >> 4);
+                        const uint64_t kd = hi | (lo + (uint32_t)(((ks >> 2) * REGION + (ks & 3) * 32) >> 4));
                         mma_f8_ta(d, tmem + ks * 8, kd, id_f8, ks > 0);
                         mma_f8_ta(d + NK, tmem + 128 + ks * 8, kd, id_f8, ks > 0);
                     }
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
-                        mma_bf16_ta(d + 2 * NK, tmem + 256 + ks * 8, kd0 + (uint32_t)((4 * REGION + ks * 32) >> 4), id_bf, ks > 0);
+                        mma_bf16_ta(d + 2 * NK, tmem + 256 + ks * 8, hi | (lo + (uint32_t)((4 * REGION + ks * 32) >> 4)), id_bf, ks > 0);
                 } else {
 #pragma unroll
                     for (int ks = 0; ks < D_QK / 16; ++ks)
-                        mma_bf16_ta(d, tmem + ks * 8, kd0 + (uint32_t)(((ks >> 2) * REGION + (ks & 3) * 32) >> 4), id_bf, ks > 0);
+                        mma_bf16_ta(d, tmem + ks * 8, hi | (lo + (uint32_t)(((ks >> 2) * REGION + (ks & 3) * 32) >> 4)), id_bf, ks > 0);
                 }
                 mma_commit(&M->bars[B_KV_EMPTY + st]);
-                mma_commit(&M->bars[B_S_FULL + (i & 1)]);
-                mbar_arrive(&M->bars[B_S_FULL + (i & 1)]);   // hands on what came with the keys: scales, positions
+                mma_commit(&M->bars[B_S_FULL + buf]);
+                mbar_arrive(&M->bars[B_S_FULL + buf]);   // hands on what came with the keys: scales, positions
             }
             __syncwarp();
-            if (++st == S::STAGES) { st = 0; round ^= 1; }
+            st += 2;
+            if (st >= S::STAGES) { st -= S::STAGES; round ^= 1; }
         }
         if (!ok) {
             if (lane == 0) give_up(M, a.status);
-            if (i > 0) mbar_drain(&M->bars[B_S_FULL + ((i - 1) & 1)], ((i - 1) >> 1) & 1);
+            if (i >= 2) mbar_drain(&M->bars[B_S_FULL + buf], ((i - 2) >> 1) & 1);
         }
         __syncwarp();
     } else if (warp >= GATHER0) {
@@ -366,25 +413,30 @@ __global__ void __launch_bounds__(NT, 1) key_weights_kernel(const WeightArgs a) 
             return RULES && v >= gap_at ? v + gap : v;
         };
         // lane l holds the slot of key l & 7 of tile t0 + (l >> 3), for the current group of four tiles and
-        // the next; indices are checked when their group becomes current
+        // the four after it (a load waits behind the stages' 200 KB that are under way); indices are
+        // checked when their group becomes current
         auto load_slots = [&](int t0) -> int {
             const int t = t0 + (lane >> 3);
             return t < T ? __ldg(slot_row + key_at(t)) : 0;
         };
-        int cur = load_slots(0), nxt = load_slots(4), st = 0, ring = 0;
+        int cur = load_slots(0), next[4], st = 0, ring = 0;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) next[g] = load_slots(4 * g + 4);
         uint32_t round = 1;                              // (the wait for a fresh stage passes at once)
         for (int i = 0; i < T; ++i) {
             if ((i & 3) == 0) {
                 if (i > 0) {
-                    cur = nxt;
-                    nxt = load_slots(i + 4);
+                    cur = next[0];
+#pragma unroll
+                    for (int g = 0; g < 3; ++g) next[g] = next[g + 1];
+                    next[3] = load_slots(i + 16);
                 }
                 if (cur < 0 || (int64_t)cur >= a.n_pool) { bad_slot = true; cur = 0; }
             }
             const int sl = __shfl_sync(0xffffffffu, cur, ((i & 3) << 3) + (lane & 7));
             // the stage is free: its products are done, and Q has left it
             if (!mbar_wait_warp(&M->bars[B_KV_EMPTY + st], round, &M->abort) ||
-                (i == Q_STAGE && !mbar_wait_warp(&M->bars[B_Q_FULL], 0, &M->abort))) {
+                (i == q_stage && !mbar_wait_warp(&M->bars[B_Q_FULL], 0, &M->abort))) {
                 if (lane == 0) give_up(M, a.status);
                 break;
             }
@@ -423,9 +475,9 @@ __global__ void __launch_bounds__(NT, 1) key_weights_kernel(const WeightArgs a) 
         cp_async_wait_all();
         if (bad_slot) atomicOr(a.status, DEV_BAD_SLOT);
     } else if (warp < SCORE_WARPS) {
-        // ================= weights: rows of quadrant `quad`, keys 16 g .. 16 g + 15 of every second tile =================
-        const int set = warp >> 3, g = (warp >> 2) & 1, r = quad * 32 + lane;
-        const bool row_ok = r < nrows, rows_used = quad * 32 < nrows, writer = (warp & 7) == 0;
+        // ================= weights: keys g .. g + KW - 1 of every second tile =================
+        const int set = warp >> 3, g = KW * (((warp >> 2) & 1) + (KW == 16 ? 0 : quad & 2)), rq = r >> 5;
+        const bool row_ok = r < nrows, rows_used = rq * 32 < nrows, writer = (warp & 7) == 0;
         const int t = row_ok ? (row0 + r) / a.H : 0;
         const float lse = row_ok ? a.lse[(int64_t)b * rows + row0 + r] : 0.f;
         const bool live = row_ok && lse != -INFINITY && (!a.counted || a.counted[(int64_t)b * a.q_len + t]);
@@ -460,26 +512,29 @@ __global__ void __launch_bounds__(NT, 1) key_weights_kernel(const WeightArgs a) 
             const bool ok = mbar_wait_warp(&M->bars[B_S_FULL + set], (i >> 1) & 1, &M->abort);
             tc_fence_after();
             if (ok && any_live) {
-                uint32_t va[16], vl[16], vc[16];
-                const uint32_t d = tmem + lane_base + D_COL + set * D_STEP + 16 * g;
-                tmem_ld16(d, va);
+                uint32_t va[KW], vl[KW], vc[KW];
+                const uint32_t d = tmem + lane_base + D_COL + set * D_STEP + g;
+                tmem_ld(d, va);
                 if (FP8) {
-                    tmem_ld16(d + NK, vl);
-                    tmem_ld16(d + 2 * NK, vc);
+                    tmem_ld(d + NK, vl);
+                    tmem_ld(d + 2 * NK, vc);
                 }
                 tmem_ld_wait();
-                float e[16];
-                const int kg = k0 + 16 * g;
-                const float* ks = M->key_scale[ring] + 16 * g;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&M->bars[B_S_FREE + set]);
+                float e[KW];
+                const int kg = k0 + g;
+                const float* ks = M->key_scale[ring] + g;
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
+                for (int k = 0; k < KW; ++k) {
                     float dot = __uint_as_float(va[k]);
                     if (FP8) dot = fmaf(fmaf(__uint_as_float(vl[k]), 0.03125f, dot), ks[k], __uint_as_float(vc[k]));
                     float x;
                     if (RULES) {
                         x = a.rules.softcap > 0.f ? fmaf(capped(dot * cap_in), cap_out, off) : fmaf(dot, c2, off);
                         if (a.rules.slopes) {
-                            const int kp = a.rules.key_pos ? M->key_pos[ring][16 * g + k] : kg + k + (kg + k >= gap_at ? gap : 0);
+                            const int kp = a.rules.key_pos ? M->key_pos[ring][g + k] : kg + k + (kg + k >= gap_at ? gap : 0);
                             x = fmaf((float)(kp - rule.pos), rule.slope, x);
                         }
                     } else {
@@ -489,27 +544,23 @@ __global__ void __launch_bounds__(NT, 1) key_weights_kernel(const WeightArgs a) 
                 }
                 if (RULES && a.rules.masked) {
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
+                    for (int k = 0; k < KW; ++k) {
                         const int j = kg + k - p;        // draft index, < 0: before the drafts
-                        const int kp = a.rules.key_pos ? M->key_pos[ring][16 * g + k] : kg + k + (kg + k >= gap_at ? gap : 0);
-                        const int kd = a.rules.key_doc ? M->key_doc[ring][16 * g + k] : -1;
+                        const int kp = a.rules.key_pos ? M->key_pos[ring][g + k] : kg + k + (kg + k >= gap_at ? gap : 0);
+                        const int kd = a.rules.key_doc ? M->key_doc[ring][g + k] : -1;
                         if (!rule.sees(j < 0 || ((vis >> (j & 63)) & 1ull), kp, kd)) e[k] = 0.f;
                     }
-                } else if (kg + 16 > p) {
+                } else if (kg + KW > p) {
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
+                    for (int k = 0; k < KW; ++k) {
                         const int j = kg + k - p;
                         if (j >= 0 && !((vis >> (j & 63)) & 1ull)) e[k] = 0.f;
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&M->bars[B_S_FREE + set]);
-                const float s = sum_rows(e);
-                if ((lane & 1) == 0) sums[quad][16 * g + (lane >> 1)] = s;
+                const float s = sum_rows<KW>(e);
+                if (lane % (32 / KW) == 0) sums[rq][g + lane / (32 / KW)] = s;
             } else {
-                if (rows_used && (lane & 1) == 0) sums[quad][16 * g + (lane >> 1)] = 0.f;
-                __syncwarp();
+                if (rows_used && lane < KW) sums[rq][g + lane] = 0.f;
                 if (ok && lane == 0) mbar_arrive(&M->bars[B_S_FREE + set]);
             }
             if (bar_red_or(1 + set, 32 * SCORE_WARPS / 2, !ok)) {   // the sums are there, or a warp gives up
@@ -572,9 +623,9 @@ int weight_nsplit(int B, int n_tiles, int max_seq, int num_sms) {
     return (int)best;
 }
 
-template <bool FP8, bool RULES>
+template <bool FP8, bool RULES, int KW>
 cudaError_t launch_weights(const WeightArgs& a, dim3 grid, int dev, cudaStream_t stream) {
-    auto* k = key_weights_kernel<FP8, RULES>;
+    auto* k = key_weights_kernel<FP8, RULES, KW>;
     static std::atomic<bool> attr_set[64];
     if (!attr_set[dev].load(std::memory_order_acquire)) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<FP8>());
@@ -618,8 +669,10 @@ int key_weights_call(WeightArgs a, const uint64_t* bits, void* workspace, size_t
     const dim3 grid(a.nsplit, n_tiles, a.balanced ? 1 : a.B);
     const ScoreRules& r = a.rules;
     const bool ruled = r.softcap > 0.f || r.slopes || r.masked;
-    if ((ruled ? launch_weights<FP8, true>(a, grid, dev, stream) : launch_weights<FP8, false>(a, grid, dev, stream)) != cudaSuccess)
-        return MLA_ERR_LAUNCH;
+    const bool twice = a.R_step <= 64;
+    const cudaError_t e = ruled ? twice ? launch_weights<FP8, true, 8>(a, grid, dev, stream) : launch_weights<FP8, true, 16>(a, grid, dev, stream)
+                                : twice ? launch_weights<FP8, false, 8>(a, grid, dev, stream) : launch_weights<FP8, false, 16>(a, grid, dev, stream);
+    if (e != cudaSuccess) return MLA_ERR_LAUNCH;
     if (n_tiles > 1) {
         const int blocks = (int)min(((long long)a.slot_stride + 255) / 256, max(1ll, 16ll * num_sms / a.B));
         if (launch_dependent(key_weights_join, dim3(blocks, a.B), dim3(256), 0, stream, a, n_tiles) != cudaSuccess)
