@@ -6,10 +6,10 @@
 //
 // Scores over the fp8 cache.  The codes are operands of the 8-bit matrix products as they lie in the cache,
 // nothing is widened.  A bf16 query, its row brought to [2^7, 2^8) by a power of two, goes in two e4m3 pieces:
-// h = e4m3(q), then l = e4m3(2^5 (q - h)), whose four bits each hold the eight of a bf16 number.  That is
-// exact down to 2^-14 of the row's largest element, and within 2^-22 of the largest below.  With the
-// pieces' sums over the latent dims H and L and the rotated part's C in three fp32 accumulators,
-//     z_j = scale 2^e (s_j (H + 2^-5 L) + C)
+// h, its first four bits, and l = 2^4 (q - h), the other four.  That is exact down to 2^-13 of the row's
+// largest element, and within 2^-20 of the largest below.  With the pieces' sums over the latent dims H and
+// L and the rotated part's C in three fp32 accumulators,
+//     z_j = scale 2^e (s_j (H + 2^-4 L) + C)
 // so neither keys nor scales are rounded.  (Measured on the products: 512 terms are summed to 2^-25 of the
 // sum of their magnitudes, as with fp16 operands.)  The bf16 cache takes one sum over 576 dims.
 //
@@ -30,6 +30,7 @@
 #include "query_rows.cuh"
 #include "score_rules.cuh"
 #include "tc_ptx.cuh"
+#include "tmap.h"
 
 #include <math.h>
 
@@ -193,16 +194,17 @@ __device__ __forceinline__ void give_up(Misc* M, unsigned* status) {
     if (atomicExch(const_cast<int*>(&M->abort), 1) == 0) atomicOr(status, DEV_TIMEOUT);
 }
 
-// Two bf16 values (one word) of a row times f, a power of two, as two e4m3 pieces: the bytes of h in the low
-// half, those of l = 2^5 (q - h) in the high half.  On the way they are fp16, which holds them to 2^-25.
-__device__ __forceinline__ uint32_t q_pieces(uint32_t w, __nv_bfloat162 f) {
-    const __nv_bfloat162 q = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), f);
-    const __half2 x = __floats2half2_rn(__low2float(q), __high2float(q));
-    const uint32_t h = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
-    const __half2 rest = __hsub2(x, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h, __NV_E4M3)));
-    const __half2 up = __hmul2(rest, __float2half2_rn(32.f));
-    const uint32_t l = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(up), __NV_SATFINITE, __NV_E4M3);
-    return h | (l << 16);
+// Two bf16 values (one word) of a row times f, a power of two that brings the row below 1, as the e4m3 pieces of
+// 2^8 times that: h in the two high bytes of the halves of .x, l in those of .y.  A half of fp16 below 1 has
+// e4m3's exponent of 2^8 times the number in its lower four exponent bits, denormals alike, so the piece is the
+// half's first bits.
+__device__ __forceinline__ uint2 q_pieces(uint32_t w, float f) {
+    const __half2 x = __floats2half2_rn(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f);
+    const uint32_t hw = *reinterpret_cast<const uint32_t*>(&x) & 0xff80ff80u;
+    const __half2 l = __hmul2(__hsub2(x, *reinterpret_cast<const __half2*>(&hw)), __float2half2_rn(16.f));
+    const uint32_t lw = *reinterpret_cast<const uint32_t*>(&l);
+    auto bits = [](uint32_t v) { return ((v << 1) & 0x7fff7fffu) | (v & 0x80008000u); };
+    return make_uint2(bits(hw), bits(lw));
 }
 
 // One query row in its place in shared memory, chunk c's 128 bytes at row + c * q_chunk (16-byte pieces swizzled
@@ -218,24 +220,21 @@ __device__ __forceinline__ float convert_row(uint8_t* row, int q_chunk, int swz)
     }
     int e[1];
     row_exponents<1>(v, e);
-    const uint32_t top = (uint32_t)(7 - e[0] + 127);
-    // (an exponent of 127 is that of 2^127 or of what is not finite)
-    const bool bad = e[0] == 127 && __any_sync(0xffffffffu, not_finite(v[0][0]) || not_finite(v[0][1]) || not_finite(v[0][2]));
-    const uint32_t fw = (top << 23 | top << 7) & 0xffffff80u, spoil = bad ? 0x7f7f7f7fu : 0u;
-    const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162*>(&fw);
+    const bool odd = __any_sync(0xffffffffu, not_finite(v[0][0]) || not_finite(v[0][1]) || not_finite(v[0][2]));
+    const uint32_t spoil = odd ? 0x7f7f7f7fu : 0u;
+    const float f = __uint_as_float(e[0] < 126 ? (uint32_t)(126 - e[0]) << 23 : 0x00400000u >> (e[0] - 126));   // 2^(-1 - e)
     __syncwarp();
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
         const int pc = c * 32 + lane;
         const uint4 o = v[0][c];
-        const uint32_t x = q_pieces(o.x, f) | spoil, y = q_pieces(o.y, f) | spoil, z = q_pieces(o.z, f) | spoil,
-                       w = q_pieces(o.w, f) | spoil;
+        const uint2 x = q_pieces(o.x, f), y = q_pieces(o.y, f), z = q_pieces(o.z, f), w = q_pieces(o.w, f);
         uint8_t* at = row + (pc >> 4) * q_chunk + ((((pc & 15) >> 1) ^ swz) << 4) + (pc & 1) * 8;
-        *reinterpret_cast<uint2*>(at) = make_uint2(__byte_perm(x, y, 0x5410), __byte_perm(z, w, 0x5410));
-        *reinterpret_cast<uint2*>(at + 4 * q_chunk) = make_uint2(__byte_perm(x, y, 0x7632), __byte_perm(z, w, 0x7632));
+        *reinterpret_cast<uint2*>(at) = make_uint2(__byte_perm(x.x, y.x, 0x7531) | spoil, __byte_perm(z.x, w.x, 0x7531) | spoil);
+        *reinterpret_cast<uint2*>(at + 4 * q_chunk) = make_uint2(__byte_perm(x.y, y.y, 0x7531) | spoil, __byte_perm(z.y, w.y, 0x7531) | spoil);
     }
     if (lane < 8) {
-        const float m = __uint_as_float(top << 23);
+        const float m = __uint_as_float((uint32_t)(7 - e[0] + 127) << 23);
         const uint4 o = v[0][2];
         *reinterpret_cast<uint4*>(row + 8 * q_chunk + ((lane ^ swz) << 4)) =
             make_uint4(q_to_bf16(o.x, m), q_to_bf16(o.y, m), q_to_bf16(o.z, m), q_to_bf16(o.w, m));
@@ -529,7 +528,7 @@ __global__ void __launch_bounds__(NT, 1) key_weights_kernel(const WeightArgs a) 
 #pragma unroll
                 for (int k = 0; k < KW; ++k) {
                     float dot = __uint_as_float(va[k]);
-                    if (FP8) dot = fmaf(fmaf(__uint_as_float(vl[k]), 0.03125f, dot), ks[k], __uint_as_float(vc[k]));
+                    if (FP8) dot = fmaf(fmaf(__uint_as_float(vl[k]), 0.0625f, dot), ks[k], __uint_as_float(vc[k]));
                     float x;
                     if (RULES) {
                         x = a.rules.softcap > 0.f ? fmaf(capped(dot * cap_in), cap_out, off) : fmaf(dot, c2, off);
