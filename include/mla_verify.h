@@ -407,7 +407,15 @@ size_t mla_key_weights_workspace_bytes(int B, int q_len, int H, int slot_stride)
 int mla_kv_evict(const int32_t* slot_table, const int32_t* seq_lens, const float* weights, const int32_t* key_pos,
                  const int32_t* key_doc, int B, int slot_stride, const int32_t* budgets, int budget, int sink,
                  int recent, int32_t* table_out, int32_t* lens_out, float* weights_out, int32_t* pos_out,
-                 int32_t* doc_out, int32_t* freed, int32_t* n_freed, mla_stream_t stream);
+                 int32_t* doc_out, int32_t* freed, int32_t* n_freed, void* workspace, size_t ws_bytes,
+                 mla_stream_t stream);
+
+/*
+ * Bytes of workspace with which mla_kv_evict() takes the keys of long streams with all SMs (0: it needs none).
+ * Without it, and where a table is compacted in place, a cluster of SMs takes a stream alone, to the same
+ * result.  Pure host function; num_sms of the device.
+ */
+size_t mla_kv_evict_workspace_bytes(int B, int slot_stride, int num_sms);
 
 /*
  * Acceptance of drafted tokens from given random numbers, the step after a verify pass:

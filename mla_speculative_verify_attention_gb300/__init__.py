@@ -38,7 +38,7 @@ EXPORTS = ("mla_verify_workspace_bytes", "mla_verify_auto_nsplit", "mla_verify_a
            "mla_debug_stall_next_launch", "mla_debug_rescale_count", "mla_qk_norm_rope", "mla_kv_append_quant",
            "mla_kv_read_fp8", "mla_verify_attn_fp8", "mla_draft_verify", "mla_verify_fp8_workspace_bytes",
            "mla_verify_attn_fp8_rules", "mla_key_weights_fp8", "mla_key_weights", "mla_kv_evict",
-           "mla_key_weights_workspace_bytes")
+           "mla_key_weights_workspace_bytes", "mla_kv_evict_workspace_bytes")
 STATIC_SCRATCH_BYTES = 64 << 20
 
 _lib = None
@@ -101,7 +101,9 @@ def load():
     L.mla_key_weights.restype = I
     L.mla_key_weights_workspace_bytes.argtypes = [I, I, I, I]
     L.mla_key_weights_workspace_bytes.restype = SZ
-    L.mla_kv_evict.argtypes = [P, P, P, P, P, I, I, P, I, I, I, P, P, P, P, P, P, P, P]
+    L.mla_kv_evict_workspace_bytes.argtypes = [I, I, I]
+    L.mla_kv_evict_workspace_bytes.restype = SZ
+    L.mla_kv_evict.argtypes = [P, P, P, P, P, I, I, P, I, I, I, P, P, P, P, P, P, P, P, SZ, P]
     L.mla_kv_evict.restype = I
     L.mla_verify_fp8_workspace_bytes.argtypes = [I, I, I, I, I]
     L.mla_verify_fp8_workspace_bytes.restype = SZ
@@ -759,12 +761,14 @@ def kv_evict(slot_table: torch.Tensor, seq_lens: torch.Tensor, weights: torch.Te
              table_out: Optional[torch.Tensor] = None, lens_out: Optional[torch.Tensor] = None,
              weights_out: Optional[torch.Tensor] = None, pos_out: Optional[torch.Tensor] = None,
              doc_out: Optional[torch.Tensor] = None, freed: Optional[torch.Tensor] = None,
-             n_freed: Optional[torch.Tensor] = None, stream=None) -> Evicted:
+             n_freed: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+             stream=None) -> Evicted:
     """mla_kv_evict: keeps each stream's first ``sink``, last ``recent`` and otherwise heaviest keys, ``budget``
     in all (an int, or int32 [B] on the device), and moves their entries of slot_table, weights, key_pos and
     key_doc [B, stride] together.  By default in place; an ``_out`` tensor takes the result instead.
     Without key_pos a key's position is its index (pos_out, where given, gets it).  The evicted slots are in
-    freed [B, stride], n_freed [B] of them."""
+    freed [B, stride], n_freed [B] of them.  ``workspace`` is a byte (uint8) CUDA tensor for long streams whose
+    tables are not compacted in place (mla_kv_evict_workspace_bytes), allocated here when omitted."""
     _want_dims("slot_table", slot_table, torch.int32, 2)
     shape = slot_table.shape
     B, stride = shape
@@ -799,19 +803,25 @@ def kv_evict(slot_table: torch.Tensor, seq_lens: torch.Tensor, weights: torch.Te
         _want("freed", freed, torch.int32, shape)
     if n_freed is not None:
         _want("n_freed", n_freed, torch.int32, (B,))
+    if workspace is not None:
+        _want_dims("workspace", workspace, torch.uint8, 1)
     dev = _device_of(slot_table, seq_lens, weights, key_pos, key_doc, budget if each else None, table_out, lens_out,
-                     weights_out, pos_out, doc_out, freed, n_freed)
+                     weights_out, pos_out, doc_out, freed, n_freed, workspace)
     with _on(dev):
         at = _stream_on(stream, dev)
         if freed is None:
             freed = _empty_like(slot_table, torch.int32, stream)
         if n_freed is None:
             n_freed = _empty_like(seq_lens, torch.int32, stream)
+        if workspace is None and stride > 8192 and table_out is not slot_table:
+            need = int(load().mla_kv_evict_workspace_bytes(B, stride, num_sms(dev)))
+            if need:
+                workspace = _empty(weights, (need,), torch.uint8, stream)
         _check("mla_kv_evict", _call("mla_kv_evict")(
             slot_table.data_ptr(), seq_lens.data_ptr(), weights.data_ptr(), _addr(key_pos), _addr(key_doc), B, stride,
             budget.data_ptr() if each else 0, 0 if each else budget, sink, recent, table_out.data_ptr(),
             lens_out.data_ptr(), weights_out.data_ptr(), _addr(pos_out), _addr(doc_out), freed.data_ptr(),
-            n_freed.data_ptr(), at))
+            n_freed.data_ptr(), _addr(workspace), workspace.numel() if workspace is not None else 0, at))
     return Evicted(table_out, lens_out, weights_out, pos_out, doc_out, freed, n_freed)
 
 

@@ -1,13 +1,15 @@
 // Eviction from a cache by accumulated weight (mla_kv_evict): K of a stream's n keys stay, their table
 // entries move together.
 //
-// A cluster of up to sixteen CTAs a stream.  Weights are compared as 32-bit integers in the order of the
-// numbers; the K-th largest is found from histograms in shared memory (integer counts: no order of additions)
+// A cluster of up to sixteen CTAs a stream.  Weights are compared as 32-bit integers in the opposite order of the
+// numbers; the K-th smallest is found from histograms in shared memory (integer counts: no order of additions)
 // over its first 13 bits, the next 11 and the last 8, as many of them as it takes.  The first pass keeps the
-// integers in shared memory, up to 49152 a CTA, for the others.  Then the keys are taken in order, 8192 a CTA
-// and round, the CTAs one behind the other, each key with its place from ballots and the counts of the warps
-// and CTAs before it.  A round is read before anything of it is written, by all CTAs, and its places are not
-// behind its own, so tables may be compacted in place.
+// integers in shared memory, up to 45056 a CTA, for the others; the second lists the few that the third has to
+// look at.  Then the keys are taken in order, each with its place from ballots and the counts of the keys
+// before it, 8192 a CTA and round, the CTAs one behind the other.  A round is read before anything of it is
+// written, by all CTAs, and its places are not behind its own, so tables may be compacted in place.
+// Where several rounds are needed and no table is compacted in place, the cluster only leaves the border and
+// each warp's counts in the workspace, and a second kernel over all SMs takes the keys.
 #include "../../include/mla_verify.h"
 #include "internal.cuh"
 
@@ -27,7 +29,8 @@ constexpr int CHUNK = NT * ITEMS;
 constexpr int MAX_CLUSTER = 16;
 constexpr int BITS0 = 13, BITS1 = 11, BITS2 = 8;
 constexpr int BINS = 1 << BITS0;
-constexpr int MAX_KEPT = 49152;                      // integers that a CTA keeps in shared memory
+constexpr int MAX_HELD = 45056;                      // integers that a CTA keeps in shared memory
+constexpr int MAX_LIST = 4096;                       // and those of them that it lists
 
 struct EvictArgs {
     const int32_t* slot;
@@ -46,18 +49,92 @@ struct EvictArgs {
     int32_t* freed;
     int32_t* n_freed;
     unsigned* status;
+    struct Border* border;                           // workspace, or null: one kernel does it all
+    int32_t* warp_counts;                            // [B][chunks * 32]: keys that stay | ties << 16, a warp's 256 keys
+    int32_t* chunk_counts;                           // [B][chunks]: the same of a chunk of 8192
 };
 
-// The number's place in the order: NaN above all, -0 beside 0.
+// What the first kernel leaves of a stream: a key j of lo .. hi - 1 stays if its integer is below `top`, and of
+// those equal to it the first `want`; all others of the n keys stay.
+struct Border {
+    int n, lo, hi, want;
+    uint32_t top;
+};
+
+// The number's place in the opposite order: NaN before all, -0 beside 0.
 __device__ __forceinline__ uint32_t order_of(float w) {
     const uint32_t u = __float_as_uint(w + 0.f);
-    return w != w ? 0xffffffffu : (u & 0x80000000u) ? ~u : u | 0x80000000u;
+    return w != w ? 0u : (u & 0x80000000u) ? u : ~(u | 0x80000000u);
 }
+
+// A thread's keys j0 + 32 i of the stream, and which of the warp's keys stay or tie.
+struct Keys {
+    float w[ITEMS];
+    int slot[ITEMS], pos[ITEMS], doc[ITEMS];
+    unsigned stay[ITEMS], tie[ITEMS];
+
+    // Returns the warp's counts: stay | ties << 16.
+    __device__ __forceinline__ int load(const EvictArgs& a, const Border& o, int64_t row, int j0) {
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const int j = j0 + 32 * i;
+            w[i] = 0.f;
+            slot[i] = doc[i] = 0;
+            pos[i] = j;
+            if (j < o.n) {
+                w[i] = a.weights[row + j];
+                slot[i] = a.slot[row + j];
+                if (a.pos_out && a.key_pos) pos[i] = a.key_pos[row + j];
+                if (a.doc_out) doc[i] = a.key_doc[row + j];
+            }
+        }
+        int all = 0;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const int j = j0 + 32 * i;
+            const uint32_t u = order_of(w[i]);
+            const bool mid = j >= o.lo && j < o.hi;
+            stay[i] = __ballot_sync(0xffffffffu, j < o.n && (!mid || u < o.top));
+            tie[i] = __ballot_sync(0xffffffffu, mid && u == o.top);
+            all += __popc(stay[i]) | __popc(tie[i]) << 16;
+        }
+        return all;
+    }
+    // `before`, `equal`: keys before the warp's that stay for sure, and ties.
+    __device__ __forceinline__ void write(const EvictArgs& a, const Border& o, int64_t row, int j0, int before, int equal) const {
+        const int lane = threadIdx.x & 31;
+        const unsigned lower = (1u << lane) - 1u;
+        before += min(equal, o.want);                    // with the ties that stay
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const int j = j0 + 32 * i;
+            if (j - lane >= o.n) break;
+            unsigned keep = stay[i];
+            if (tie[i]) {                                // the first of them, as many as are wanted
+                const int room = o.want - min(equal, o.want), m = __popc(tie[i]);
+                equal += m;
+                if (room >= m) keep |= tie[i];
+                else if (room > 0) keep |= __ballot_sync(0xffffffffu, ((tie[i] >> lane) & 1u) && __popc(tie[i] & lower) < room);
+            }
+            const int to = before + __popc(keep & lower);
+            before += __popc(keep);
+            if ((keep >> lane) & 1u) {
+                a.table_out[row + to] = slot[i];
+                a.weights_out[row + to] = w[i];
+                if (a.pos_out) a.pos_out[row + to] = pos[i];
+                if (a.doc_out) a.doc_out[row + to] = doc[i];
+            } else if (j < o.n && a.freed) {
+                a.freed[row + j - to] = slot[i];
+            }
+        }
+    }
+};
 
 struct Shared {
     int warp_sums[32];
     int slice[MAX_CLUSTER];                          // keys in every CTA's slice of the bins
     int found[3];                                    // bin, keys wanted of it, keys in it
+    int listed;                                      // keys of the bin, as many as MAX_LIST in the list
     int totals[2][MAX_CLUSTER];                      // of every CTA's chunk: keys that stay | ties << 16
 };
 
@@ -94,50 +171,74 @@ __device__ __forceinline__ void count(int* hist, bool counts, uint32_t bin) {
     }
 }
 
-// The bin, from the last one down, in which the cluster's `want`-th key lies; CTA r adds the r-th part of the
-// bins up.  All histograms are zero afterwards.
-__device__ __forceinline__ void find_bin(cg::cluster_group& cluster, int C, int rank, int* hist, int bins, Shared& s, int want) {
+// The bin in which the cluster's `want`-th key lies; CTA r adds the r-th part of the bins up.  All
+// histograms are zero afterwards.
+template <int BINS_>
+__device__ __forceinline__ void find_bin(cg::cluster_group& cluster, int C, int rank, int* hist, Shared& s, int want) {
+    constexpr int PER = (BINS_ + NT - 1) / NT;           // a thread's bins with one CTA, enough with more
     const int tid = threadIdx.x;
-    if (C > 1) cluster.sync();                           // every CTA has counted
-    else __syncthreads();
-    const int part = bins / C, per = (part + NT - 1) / NT, first = bins - 1 - rank * part;   // a thread's bins
-    int mine[BINS / NT], sum = 0;
+    const int part = BINS_ / C, per = (part + NT - 1) / NT, first = rank * part + tid * per;
+    int mine[PER], sum = 0;
 #pragma unroll
-    for (int q = 0; q < BINS / NT; ++q) {
-        mine[q] = 0;
-        const int at = tid * per + q;
-        if (q < per && at < part) {
-            if (C == 1) mine[q] = hist[first - at];
-            else
-                for (int r = 0; r < C; ++r) mine[q] += *cluster.map_shared_rank(hist + first - at, r);
+    for (int q = 0; q < PER; ++q) mine[q] = 0;
+    if (C == 1) {
+        __syncthreads();                                 // every warp has counted
+        if (PER >= 4) {
+#pragma unroll
+            for (int q = 0; q < PER; q += 4) {
+                const int4 v = *reinterpret_cast<const int4*>(hist + first + q);
+                mine[q] = v.x;
+                if (q + 1 < PER) mine[q + 1] = v.y;
+                if (q + 2 < PER) mine[q + 2] = v.z;
+                if (q + 3 < PER) mine[q + 3] = v.w;
+            }
+        } else if (tid * per < part) {
+#pragma unroll
+            for (int q = 0; q < PER; ++q) mine[q] = hist[first + q];
         }
-        sum += mine[q];
+    } else {
+        cluster.sync();                                  // every CTA has counted
+        if (tid * per < part) {
+#pragma unroll
+            for (int q = 0; q < (PER + 1) / 2; ++q) {    // (two CTAs or more)
+                if (q >= per) break;
+                int v[MAX_CLUSTER];
+#pragma unroll
+                for (int r = 0; r < MAX_CLUSTER; ++r) v[r] = r < C ? *cluster.map_shared_rank(hist + first + q, r) : 0;
+#pragma unroll
+                for (int r = 0; r < MAX_CLUSTER; ++r) mine[q] += v[r];
+            }
+        }
     }
+#pragma unroll
+    for (int q = 0; q < PER; ++q) sum += mine[q];
     int total, upto = block_scan(sum, s.warp_sums, &total);
     if (C > 1) {
         if (tid < C) *cluster.map_shared_rank(&s.slice[rank], tid) = total;
         cluster.sync();
-        int before = 0;
-        for (int r = 0; r < rank; ++r) before += s.slice[r];
-        upto += before;
+        for (int r = 0; r < rank; ++r) upto += s.slice[r];
     }
     if (upto >= want && upto - sum < want) {             // one thread of the cluster
-        int left = want - (upto - sum), q = 0;
+        int left = want - (upto - sum), at = 0, in = 0;
+        bool done = false;
 #pragma unroll
-        for (int k = 0; k < BINS / NT; ++k)
-            if (k == q && left > mine[k]) { left -= mine[k]; ++q; }
-        int in = 0;
-#pragma unroll
-        for (int k = 0; k < BINS / NT; ++k)
-            if (k == q) in = mine[k];
+        for (int q = 0; q < PER; ++q) {
+            if (!done) {
+                in = mine[q];
+                at = q;
+                done = left <= in;
+                if (!done) left -= in;
+            }
+        }
         for (int r = 0; r < C; ++r) {
             int* f = C == 1 ? s.found : cluster.map_shared_rank(s.found, r);
-            f[0] = first - (tid * per + q);
+            f[0] = first + at;
             f[1] = left;
             f[2] = in;
         }
     }
-    for (int i = tid; i < bins; i += NT) hist[i] = 0;    // (read by now: behind the barriers of the scan or the cluster)
+    // (read by now: behind the barriers of the scan or the cluster)
+    for (int i = tid; i < BINS_ / 4; i += NT) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
     if (C > 1) cluster.sync();
     else __syncthreads();
 }
@@ -146,13 +247,16 @@ __global__ void __launch_bounds__(NT, 1) kv_evict_kernel(const EvictArgs a, int 
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ Shared s;
     int* const hist = reinterpret_cast<int*>(smem);
-    uint32_t* const held = reinterpret_cast<uint32_t*>(smem) + BINS;
+    uint32_t* const list = reinterpret_cast<uint32_t*>(smem) + BINS;
+    uint32_t* const held = list + MAX_LIST;
     cg::cluster_group cluster = cg::this_cluster();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = C > 1 ? (int)cluster.block_rank() : 0, b = blockIdx.x / C;
     const int n = a.seq_lens[b];
-    for (int i = tid; i < BINS; i += NT) hist[i] = 0;
+    const int budget = max(0, a.budgets ? a.budgets[b] : a.budget);
+    for (int i = tid; i < BINS / 4; i += NT) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
+    if (tid == 0) s.listed = 0;
     if (C > 1) cluster.sync();                           // every CTA runs, and has read the length
     else __syncthreads();
     if (n < 0 || n > a.slot_stride) {
@@ -160,151 +264,150 @@ __global__ void __launch_bounds__(NT, 1) kv_evict_kernel(const EvictArgs a, int 
             atomicOr(a.status, DEV_BAD_LEN);
             a.lens_out[b] = n;
             if (a.n_freed) a.n_freed[b] = 0;
+            if (a.border) a.border[b] = Border{};
         }
         return;
     }
     const int64_t row = (int64_t)b * a.slot_stride;
-    const int budget = max(0, a.budgets ? a.budgets[b] : a.budget);
+    const float* const weights = a.weights + row;
     const int K = (int)min((long long)n, max((long long)budget, (long long)a.sink + a.recent));
-    // of the keys lo .. hi - 1 the `want` largest stay
+    // of the keys lo .. hi - 1 the `want` heaviest stay
     const int lo = min(a.sink, n), hi = max(lo, (int)max((long long)n - a.recent, 0ll));
     int want = K - lo - (n - hi);
-    // key i of the thread in round k, in the order of the stream: warps, then items, then lanes
-    const int rounds = (int)(((long long)n + (long long)C * CHUNK - 1) / ((long long)C * CHUNK));
-    const int mine0 = rank * CHUNK + warp * 32 * ITEMS + lane;
-    // a key stays if its weight is above `top`, and of those equal to it the first `want`
+    // The thread's keys of round k are j0 + 32 i, in the order of the stream by warps, then items, then lanes.
+    // (n + a round stays below 2^31: the table's width is at most 2^30.)
+    const int step = C * CHUNK, rounds = (n + step - 1) / step, mine0 = rank * CHUNK + warp * 32 * ITEMS + lane;
+    // a key stays if its integer is below `top`, and of those equal to it the first `want`
     uint32_t top = 0;
-    if (want > 0 && want < hi - lo) {
-        for (int k = 0; k < rounds; ++k) {
-            const long long j0 = (long long)k * C * CHUNK + mine0;
-            float w[ITEMS];
+    const bool formed = want > 0 && want < hi - lo;      // there is a choice: the integers are formed
+    if (formed) {
+        float w[ITEMS], next[ITEMS];
 #pragma unroll
-            for (int i = 0; i < ITEMS; ++i) w[i] = j0 + 32 * i < n ? a.weights[row + j0 + 32 * i] : 0.f;
+        for (int i = 0; i < ITEMS; ++i) next[i] = mine0 + 32 * i < n ? weights[mine0 + 32 * i] : 0.f;
+        for (int k = 0; k < rounds; ++k) {
+            const int j0 = k * step + mine0;
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i) {
-                const long long j = j0 + 32 * i;
+                w[i] = next[i];
+                const int j = j0 + step + 32 * i;
+                next[i] = k + 1 < rounds && j < n ? weights[j] : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i) {
+                const int j = j0 + 32 * i, at = k * CHUNK + i * NT + tid;
+                if (j - lane >= n) break;
                 const uint32_t u = order_of(w[i]);
-                const int at = k * CHUNK + i * NT + tid;
                 if (at < cap) held[at] = u;
                 count(hist, j >= lo && j < hi, u >> (32 - BITS0));
             }
         }
+        find_bin<BINS>(cluster, C, rank, hist, s, want);
         int shift = 32 - BITS0;
-        find_bin(cluster, C, rank, hist, BINS, s, want);
+        bool listed = false;
 #pragma unroll 1
         for (;;) {
             top |= (uint32_t)s.found[0] << shift;
             want = s.found[1];
-            const bool whole = want == s.found[2];
-            if (whole) {                                 // the bin stays as a whole
-                want = top ? 0 : INT_MAX;
-                top = top ? top - 1 : 0;
+            if (want == s.found[2]) {                    // the bin stays as a whole
+                top |= (1u << shift) - 1u;
+                want = INT_MAX;
+                break;
             }
-            if (whole || shift == 0) break;
+            if (shift == 0) break;
             const int bits = shift == 32 - BITS0 ? BITS1 : BITS2, above = shift;
             shift -= bits;
-            for (int k = 0; k < rounds; ++k) {
-                const long long j0 = (long long)k * C * CHUNK + mine0;
+            auto put = [&](uint32_t u) { atomicAdd(&hist[(u >> shift) & ((1u << bits) - 1u)], 1); };
+            if (listed) {
+                const int m = s.listed;
+                for (int i = tid; i < m; i += NT)
+                    if ((list[i] >> above) == (top >> above)) put(list[i]);
+            } else {
+                for (int k = 0; k < rounds; ++k) {
+                    const int j0 = k * step + mine0;
 #pragma unroll
-                for (int i = 0; i < ITEMS; ++i) {
-                    const long long j = j0 + 32 * i;
-                    const int at = k * CHUNK + i * NT + tid;
-                    const uint32_t u = at < cap ? held[at] : j < n ? order_of(a.weights[row + j]) : 0u;
-                    if (j >= lo && j < hi && (u >> above) == (top >> above)) atomicAdd(&hist[(u >> shift) & ((1u << bits) - 1u)], 1);
+                    for (int i = 0; i < ITEMS; ++i) {
+                        const int j = j0 + 32 * i, at = k * CHUNK + i * NT + tid;
+                        if (j - lane >= n) break;
+                        const uint32_t u = at < cap ? held[at] : j < n ? order_of(weights[j]) : ~0u;
+                        const bool in = j >= lo && j < hi && (u >> above) == (top >> above);
+                        const unsigned m = __ballot_sync(0xffffffffu, in);
+                        if (m == 0) continue;
+                        int base = 0;
+                        if (lane == 0) base = s.listed <= MAX_LIST ? atomicAdd(&s.listed, __popc(m)) : MAX_LIST;
+                        base = __shfl_sync(0xffffffffu, base, 0) + __popc(m & ((1u << lane) - 1u));
+                        if (in) {
+                            if (base < MAX_LIST) list[base] = u;
+                            put(u);
+                        }
+                    }
                 }
             }
-            __syncthreads();                             // (found has been read)
-            find_bin(cluster, C, rank, hist, 1 << bits, s, want);
+            __syncthreads();                             // (found has been read, the list is there)
+            listed = s.listed <= MAX_LIST;
+            if (bits == BITS1) find_bin<1 << BITS1>(cluster, C, rank, hist, s, want);
+            else find_bin<1 << BITS2>(cluster, C, rank, hist, s, want);
         }
     } else if (want <= 0) {
-        top = 0xffffffffu;                               // none, not even of the largest
-        want = 0;
+        want = 0;                                        // none, not even of the first
     } else {
-        want = INT_MAX;                                  // all
+        top = ~0u;                                       // all
+        want = INT_MAX;
     }
-    int kept = 0, tied = 0;                              // before this round: keys above, ties
-    for (int k = 0; k < rounds; ++k) {
-        const long long j0 = (long long)k * C * CHUNK + mine0;
-        float w[ITEMS];
-        int slot[ITEMS], pos[ITEMS], doc[ITEMS];
-        unsigned stay[ITEMS], tie[ITEMS];                // the warp's keys of item i
+    const Border o = {n, lo, hi, want, top};
+    if (a.border) {
+        // each warp's counts of its 256 keys, for the second kernel
+        const int chunks = (a.slot_stride + CHUNK - 1) / CHUNK;
+        for (int k = 0; k < rounds; ++k) {
+            const int j0 = k * step + mine0, g = k * C + rank;
+            int all = 0;
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            const long long j = j0 + 32 * i;
-            w[i] = 0.f;
-            slot[i] = doc[i] = 0;
-            pos[i] = (int)j;
-            if (j < n) {
-                w[i] = a.weights[row + j];
-                slot[i] = a.slot[row + j];
-                if (a.pos_out && a.key_pos) pos[i] = a.key_pos[row + j];
-                if (a.doc_out) doc[i] = a.key_doc[row + j];
+            for (int i = 0; i < ITEMS; ++i) {
+                const int j = j0 + 32 * i, at = k * CHUNK + i * NT + tid;
+                if (j - lane >= n) break;
+                const uint32_t u = j >= n ? ~0u : formed && at < cap ? held[at] : order_of(weights[j]);
+                const bool mid = j >= lo && j < hi;
+                all += __popc(__ballot_sync(0xffffffffu, j < n && (!mid || u < top))) |
+                       __popc(__ballot_sync(0xffffffffu, mid && u == top)) << 16;
             }
-        }
-        int all = 0;                                     // the warp's: stay | ties << 16
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            const long long j = j0 + 32 * i;
-            const uint32_t u = order_of(w[i]);
-            const bool mid = j >= lo && j < hi;
-            stay[i] = __ballot_sync(0xffffffffu, j < n && (!mid || u > top));
-            tie[i] = __ballot_sync(0xffffffffu, mid && u == top);
-            all += __popc(stay[i]) | __popc(tie[i]) << 16;
-        }
-        __syncthreads();                                 // the sums of the round before have been read
-        if (lane == 0) s.warp_sums[warp] = all;
-        __syncthreads();
-        int upto = s.warp_sums[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += y;
-        }
-        const int total = __shfl_sync(0xffffffffu, upto, 31);
-        const int before_warp = __shfl_sync(0xffffffffu, upto, warp) - all;
-        int before = 0, whole = total;
-        if (C > 1) {
-            if (tid < C) *cluster.map_shared_rank(&s.totals[k & 1][rank], tid) = total;
-            cluster.sync();
-            const int t = lane < C ? s.totals[k & 1][lane] : 0;
-            // (sixteen chunks' counts pass 16 bits: added apart)
-            int st = t & 0xffff, ti = t >> 16;
-            int st_b = lane < rank ? st : 0, ti_b = lane < rank ? ti : 0;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                st += __shfl_xor_sync(0xffffffffu, st, o);
-                ti += __shfl_xor_sync(0xffffffffu, ti, o);
-                st_b += __shfl_xor_sync(0xffffffffu, st_b, o);
-                ti_b += __shfl_xor_sync(0xffffffffu, ti_b, o);
+            if (g >= chunks) break;
+            if (lane == 0) {
+                s.warp_sums[warp] = all;
+                a.warp_counts[((int64_t)b * chunks + g) * 32 + warp] = all;
             }
-            int up = kept + st_b + (before_warp & 0xffff), eq = tied + ti_b + (before_warp >> 16);
-            kept += st;
-            tied += ti;
-            before = up;
-            whole = eq;
-        } else {
-            before = kept + (before_warp & 0xffff);
-            whole = tied + (before_warp >> 16);
-            kept += total & 0xffff;
-            tied += total >> 16;
-        }
-        const unsigned lower = (1u << lane) - 1u;
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            const long long j = j0 + 32 * i;
-            const int eq = whole + __popc(tie[i] & lower);
-            const int to = before + __popc(stay[i] & lower) + min(eq, want);
-            const bool is_tie = (tie[i] >> lane) & 1u;
-            if (((stay[i] >> lane) & 1u) || (is_tie && eq < want)) {
-                a.table_out[row + to] = slot[i];
-                a.weights_out[row + to] = w[i];
-                if (a.pos_out) a.pos_out[row + to] = pos[i];
-                if (a.doc_out) a.doc_out[row + to] = doc[i];
-            } else if (j < n && a.freed) {
-                a.freed[row + j - to] = slot[i];
+            __syncthreads();
+            if (warp == 0) {
+                const int sum = __reduce_add_sync(0xffffffffu, s.warp_sums[lane]);
+                if (lane == 0) a.chunk_counts[(int64_t)b * chunks + g] = sum;
             }
-            before += __popc(stay[i]);
-            whole += __popc(tie[i]);
+            __syncthreads();
+        }
+        if (rank == 0 && tid == 0) a.border[b] = o;
+    } else {
+        int kept = 0, tied = 0;                          // before this round: keys that stay, ties
+        for (int k = 0; k < rounds; ++k) {
+            const int j0 = k * step + mine0;
+            Keys keys;
+            const int all = keys.load(a, o, row, j0);
+            __syncthreads();                             // the sums of the round before have been read
+            if (lane == 0) s.warp_sums[warp] = all;
+            __syncthreads();
+            const int t = s.warp_sums[lane], total = __reduce_add_sync(0xffffffffu, t);
+            const int before_warp = __reduce_add_sync(0xffffffffu, lane < warp ? t : 0);
+            int before = kept + (before_warp & 0xffff), equal = tied + (before_warp >> 16);
+            if (C > 1) {
+                if (tid < C) *cluster.map_shared_rank(&s.totals[k & 1][rank], tid) = total;
+                cluster.sync();
+                // (sixteen chunks' counts pass 16 bits: added apart)
+                const int c = lane < C ? s.totals[k & 1][lane] : 0, c_b = lane < rank ? c : 0;
+                kept += __reduce_add_sync(0xffffffffu, c & 0xffff);
+                tied += __reduce_add_sync(0xffffffffu, c >> 16);
+                before += __reduce_add_sync(0xffffffffu, c_b & 0xffff);
+                equal += __reduce_add_sync(0xffffffffu, c_b >> 16);
+            } else {
+                kept += total & 0xffff;
+                tied += total >> 16;
+            }
+            keys.write(a, o, row, j0, before, equal);
         }
     }
     if (rank == 0 && tid == 0) {
@@ -313,24 +416,69 @@ __global__ void __launch_bounds__(NT, 1) kv_evict_kernel(const EvictArgs a, int 
     }
 }
 
+// The second kernel: a CTA 2048 keys, a warp 256.
+constexpr int TAKE_NT = 256, TAKE_KEYS = TAKE_NT * ITEMS;
+__global__ void __launch_bounds__(TAKE_NT) kv_evict_take(const EvictArgs a) {
+    __shared__ int sums[2][TAKE_NT / 32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.y;
+    const Border o = a.border[b];
+    const int first = blockIdx.x * TAKE_KEYS;
+    if (first >= o.n) return;                            // (a bad length: 0 keys)
+    const int64_t row = (int64_t)b * a.slot_stride;
+    const int chunks = (a.slot_stride + CHUNK - 1) / CHUNK, chunk = first / CHUNK;
+    Keys keys;
+    const int j0 = first + warp * 32 * ITEMS + lane;
+    keys.load(a, o, row, j0);
+    int before = 0, equal = 0;
+    for (int g = tid; g < chunk; g += TAKE_NT) {
+        const int c = a.chunk_counts[(int64_t)b * chunks + g];
+        before += c & 0xffff;
+        equal += c >> 16;
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    equal = __reduce_add_sync(0xffffffffu, equal);
+    if (lane == 0) {
+        sums[0][warp] = before;
+        sums[1][warp] = equal;
+    }
+    __syncthreads();
+    before = equal = 0;
+#pragma unroll
+    for (int w = 0; w < TAKE_NT / 32; ++w) {
+        before += sums[0][w];
+        equal += sums[1][w];
+    }
+    const int me = (first - chunk * CHUNK) / (32 * ITEMS) + warp;   // the warp's place in its chunk
+    const int c = lane < me ? a.warp_counts[((int64_t)b * chunks + chunk) * 32 + lane] : 0;
+    before += __reduce_add_sync(0xffffffffu, c & 0xffff);
+    equal += __reduce_add_sync(0xffffffffu, c >> 16);
+    if (j0 - lane < o.n) keys.write(a, o, row, j0, before, equal);
+}
+
 // CTAs a stream: up to sixteen while they have a round each and the launch stays within one wave.
-cudaError_t launch_kv_evict(const EvictArgs& a, int B, int num_sms, int dev, cudaStream_t stream) {
+int evict_cluster(int B, int slot_stride, int num_sms) {
+    int C = 1;
+    while (C < MAX_CLUSTER && (long long)C * CHUNK < slot_stride && 2ll * C * B <= num_sms) C *= 2;
+    return C;
+}
+
+cudaError_t launch_kv_evict(const EvictArgs& a, int B, int C, int dev, cudaStream_t stream) {
     static std::atomic<bool> attr_set[64];
     if (!attr_set[dev].load(std::memory_order_acquire)) {
         cudaError_t e = cudaFuncSetAttribute(kv_evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(kv_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (BINS + MAX_KEPT) * 4);
+            e = cudaFuncSetAttribute(kv_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (BINS + MAX_LIST + MAX_HELD) * 4);
         if (e != cudaSuccess) return e;
         attr_set[dev].store(true, std::memory_order_release);
     }
-    int C = 1;
-    while (C < MAX_CLUSTER && (long long)C * CHUNK < a.slot_stride && 2ll * C * B <= num_sms) C *= 2;
     const long long per_round = (long long)C * CHUNK, rounds = (a.slot_stride + per_round - 1) / per_round;
-    const int cap = (int)min(rounds * CHUNK, (long long)MAX_KEPT);
+    const int cap = (int)min(rounds * CHUNK, (long long)MAX_HELD);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(B * C));
     cfg.blockDim = dim3(NT);
-    cfg.dynamicSmemBytes = (size_t)(BINS + cap) * 4;
+    cfg.dynamicSmemBytes = (size_t)(BINS + MAX_LIST + cap) * 4;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -341,7 +489,14 @@ cudaError_t launch_kv_evict(const EvictArgs& a, int B, int num_sms, int dev, cud
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kv_evict_kernel, a, C, cap);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_evict_kernel, a, C, cap);
+    if (e != cudaSuccess || !a.border) return e;
+    return launch_dependent(kv_evict_take, dim3((a.slot_stride + TAKE_KEYS - 1) / TAKE_KEYS, B), dim3(TAKE_NT), 0, stream, a);
+}
+
+size_t evict_workspace(int B, int slot_stride) {
+    const size_t chunks = ((size_t)slot_stride + CHUNK - 1) / CHUNK;
+    return align256((size_t)B * sizeof(Border)) + (size_t)B * chunks * 33 * 4;
 }
 
 }  // namespace
@@ -353,7 +508,7 @@ extern "C" int mla_kv_evict(const int32_t* slot_table, const int32_t* seq_lens, 
                             const int32_t* key_pos, const int32_t* key_doc, int B, int slot_stride,
                             const int32_t* budgets, int budget, int sink, int recent, int32_t* table_out,
                             int32_t* lens_out, float* weights_out, int32_t* pos_out, int32_t* doc_out, int32_t* freed,
-                            int32_t* n_freed, mla_stream_t stream) {
+                            int32_t* n_freed, void* workspace, size_t ws_bytes, mla_stream_t stream) {
     if (B < 0 || B > 65535 || slot_stride < 1 || slot_stride > MLA_MAX_FP8_KEYS) return MLA_ERR_SHAPE;
     if (sink < 0 || recent < 0) return MLA_ERR_ARG;
     if (B == 0) return MLA_OK;
@@ -364,11 +519,25 @@ extern "C" int mla_kv_evict(const int32_t* slot_table, const int32_t* seq_lens, 
                          lens_out, weights_out, pos_out, doc_out, freed, n_freed};
     for (const void* p : all)
         if (!aligned(p, 4)) return MLA_ERR_ALIGN;
+    if (!aligned(workspace, 4)) return MLA_ERR_ALIGN;
     EvictArgs a = {slot_table, seq_lens, weights, key_pos, key_doc, slot_stride, budgets, budget, sink, recent, table_out,
-                   lens_out, weights_out, pos_out, doc_out, freed, n_freed, nullptr};
+                   lens_out, weights_out, pos_out, doc_out, freed, n_freed, nullptr, nullptr, nullptr, nullptr};
     int num_sms = 0, dev = 0;
     const int rc = device_state(&dev, &a.status, &num_sms);
     if (rc != MLA_OK) return rc;
-    if (launch_kv_evict(a, B, num_sms, dev, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_LAUNCH;
+    const int C = evict_cluster(B, slot_stride, num_sms);
+    const bool in_place = table_out == slot_table || weights_out == weights || (pos_out && pos_out == key_pos) || (doc_out && doc_out == key_doc);
+    if ((long long)C * CHUNK < slot_stride && !in_place && workspace && ws_bytes >= evict_workspace(B, slot_stride)) {
+        const size_t chunks = ((size_t)slot_stride + CHUNK - 1) / CHUNK;
+        a.border = static_cast<Border*>(workspace);
+        a.chunk_counts = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + align256((size_t)B * sizeof(Border)));
+        a.warp_counts = a.chunk_counts + (size_t)B * chunks;
+    }
+    if (launch_kv_evict(a, B, C, dev, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_LAUNCH;
     return MLA_OK;
+}
+
+extern "C" size_t mla_kv_evict_workspace_bytes(int B, int slot_stride, int num_sms) {
+    if (B <= 0 || B > 65535 || slot_stride < 1 || slot_stride > MLA_MAX_FP8_KEYS || num_sms < 1) return 0;
+    return (long long)evict_cluster(B, slot_stride, num_sms) * CHUNK < slot_stride ? evict_workspace(B, slot_stride) : 0;
 }

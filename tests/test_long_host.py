@@ -54,15 +54,24 @@ def test_key_weights_workspace(lib):
 
 def test_evict_refusals(lib):
     f = caller(lib, "mla_kv_evict", table=16, seq=16, w=16, pos=None, doc=None, B=2, stride=100, budgets=None, budget=10, sink=1,
-               recent=1, to=16, lo=16, wo=16, po=None, do=None, freed=None, nf=None, st=None)
+               recent=1, to=16, lo=16, wo=16, po=None, do=None, freed=None, nf=None, ws=None, wsb=0, st=None)
     for kw, code in [(dict(B=-1), -2), (dict(B=65536), -2), (dict(stride=0), -2), (dict(stride=(1 << 30) + 1), -2),
                      (dict(sink=-1), -8), (dict(recent=-1), -8), (dict(do=16), -8), (dict(freed=16), -1), (dict(nf=16), -1)]:
         assert f(**kw) == code, kw
     for name in ("table", "seq", "w", "to", "lo", "wo"):
         assert f(**{name: None}) == -1 and f(**{name: 18}) == -3, name
-    for name in ("pos", "doc", "budgets", "po"):
+    for name in ("pos", "doc", "budgets", "po", "ws"):
         assert f(**{name: 18}) == -3, name
     assert f(B=0, table=None) == 0
+
+
+def test_evict_workspace(lib):
+    """Only streams of several rounds of their cluster take one."""
+    ws = lib.mla_kv_evict_workspace_bytes
+    assert ws(1, 8192, 152) == 0 and ws(1, 16 * 8192, 152) == 0 and ws(64, 16384, 152) == 0
+    assert ws(64, 16385, 152) == 64 * 20 + 64 * 3 * 33 * 4
+    assert ws(2, 1 << 20, 152) == 256 + 2 * 128 * 33 * 4
+    assert ws(0, 1 << 20, 152) == ws(65536, 1 << 20, 152) == ws(2, 0, 152) == ws(2, (1 << 30) + 1, 152) == ws(2, 1 << 20, 0) == 0
 
 
 def test_binding_refusals():
