@@ -4,7 +4,7 @@
 // A cluster of up to sixteen CTAs a stream.  Weights are compared as 32-bit integers in the opposite order of the
 // numbers; the K-th smallest is found from histograms in shared memory (integer counts: no order of additions)
 // over its first 13 bits, the next 11 and the last 8, as many of them as it takes.  The first pass keeps the
-// integers in shared memory, up to 45056 a CTA, for the others; the second lists the few that the third has to
+// integers in shared memory, up to 40960 a CTA, for the others; the second lists the few that the third has to
 // look at.  Then the keys are taken in order, each with its place from ballots and the counts of the keys
 // before it, 8192 a CTA and round, the CTAs one behind the other.  A round is read before anything of it is
 // written, by all CTAs, and its places are not behind its own, so tables may be compacted in place.
@@ -28,8 +28,9 @@ constexpr int ITEMS = 8;                             // keys of a thread and rou
 constexpr int CHUNK = NT * ITEMS;
 constexpr int MAX_CLUSTER = 16;
 constexpr int BITS0 = 13, BITS1 = 11, BITS2 = 8;
-constexpr int BINS = 1 << BITS0;
-constexpr int MAX_HELD = 45056;                      // integers that a CTA keeps in shared memory
+constexpr int BINS = 1 << BITS0, ALL_BINS = BINS + (1 << BITS1) + (1 << BITS2);   // a pass its own
+constexpr int GROUPS = 64;                           // of a pass's bins
+constexpr int MAX_HELD = 40960;                      // integers that a CTA keeps in shared memory
 constexpr int MAX_LIST = 4096;                       // and those of them that it lists
 
 struct EvictArgs {
@@ -66,6 +67,9 @@ __device__ __forceinline__ uint32_t order_of(float w) {
     const uint32_t u = __float_as_uint(w + 0.f);
     return w != w ? 0u : (u & 0x80000000u) ? u : ~(u | 0x80000000u);
 }
+
+constexpr uint32_t ZERO = 0x7fffffffu;               // order_of(0)
+constexpr uint32_t NONE = 0xffffffffu;               // no number's: the last is that of -infinity, 0xff800000
 
 // A thread's keys j0 + 32 i of the stream, and which of the warp's keys stay or tie.
 struct Keys {
@@ -132,122 +136,110 @@ struct Keys {
 
 struct Shared {
     int warp_sums[32];
-    int slice[MAX_CLUSTER];                          // keys in every CTA's slice of the bins
+    int groups[3][GROUPS];                           // a pass's keys in every sixty-fourth of the bins
     int found[3];                                    // bin, keys wanted of it, keys in it
     int listed;                                      // keys of the bin, as many as MAX_LIST in the list
     int totals[2][MAX_CLUSTER];                      // of every CTA's chunk: keys that stay | ties << 16
 };
 
-// Inclusive sum over the block of x, and the block's total.
-__device__ __forceinline__ int block_scan(int x, int* warp_sums, int* total) {
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+// A warp's search for the `want`-th of N <= 64 numbers in order, N / 32 (or 1) consecutive ones a lane: its
+// index, what is wanted of it, and the number.  Any lane may have found it: the caller looks at `here`.
+template <int PER>
+__device__ __forceinline__ bool find_in_warp(const int (&v)[PER], int want, int* at, int* left, int* in) {
+    const int lane = threadIdx.x & 31;
+    int sum = 0;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) sum += v[q];
+    int upto = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
     }
-    __syncthreads();                                     // the sums of the scan before have been read
-    if (lane == 31) warp_sums[w] = x;
-    __syncthreads();
-    int s = warp_sums[lane];
+    int rest = want - (upto - sum);
+    const bool here = rest > 0 && upto >= want;
+    bool done = false;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += y;
+    for (int q = 0; q < PER; ++q) {
+        if (!done) {
+            *at = lane * PER + q;
+            *in = v[q];
+            done = rest <= v[q];
+            if (!done) rest -= v[q];
+        }
     }
-    *total = __shfl_sync(0xffffffffu, s, 31);
-    const int before = __shfl_sync(0xffffffffu, s, (w + 31) & 31);
-    return x + (w ? before : 0);
+    *left = rest;
+    return here;
 }
 
-// Adds the lane's key to its bin, where it counts.  Weights that are all alike (zeros, say) meet in one bin: a
-// warp of those adds once.
-__device__ __forceinline__ void count(int* hist, bool counts, uint32_t bin) {
-    const uint32_t first = __shfl_sync(0xffffffffu, bin, 0);
-    if (__all_sync(0xffffffffu, counts && bin == first)) {
-        if ((threadIdx.x & 31) == 0) atomicAdd(&hist[bin], 32);
-    } else if (counts) {
-        atomicAdd(&hist[bin], 1);
-    }
-}
-
-// The bin in which the cluster's `want`-th key lies; CTA r adds the r-th part of the bins up.  All
-// histograms are zero afterwards.
+// The bin in which the cluster's `want`-th key lies.  Every CTA looks for itself: at all CTAs' sums of the 64
+// groups of bins, then at the group's bins.  One cluster barrier: nobody writes these bins again.
 template <int BINS_>
-__device__ __forceinline__ void find_bin(cg::cluster_group& cluster, int C, int rank, int* hist, Shared& s, int want) {
-    constexpr int PER = (BINS_ + NT - 1) / NT;           // a thread's bins with one CTA, enough with more
-    const int tid = threadIdx.x;
-    const int part = BINS_ / C, per = (part + NT - 1) / NT, first = rank * part + tid * per;
-    int mine[PER], sum = 0;
+__device__ __forceinline__ void find_bin(cg::cluster_group& cluster, int C, int pass, int* hist, Shared& s, int want) {
+    constexpr int G = BINS_ / GROUPS;                    // bins of a group: 128, 32 or 4
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    __syncthreads();                                     // every warp has counted
+    // two groups a warp
 #pragma unroll
-    for (int q = 0; q < PER; ++q) mine[q] = 0;
-    if (C == 1) {
-        __syncthreads();                                 // every warp has counted
-        if (PER >= 4) {
+    for (int h = 0; h < 2; ++h) {
+        const int g = warp * 2 + h;
+        int sum = 0;
 #pragma unroll
-            for (int q = 0; q < PER; q += 4) {
-                const int4 v = *reinterpret_cast<const int4*>(hist + first + q);
-                mine[q] = v.x;
-                if (q + 1 < PER) mine[q + 1] = v.y;
-                if (q + 2 < PER) mine[q + 2] = v.z;
-                if (q + 3 < PER) mine[q + 3] = v.w;
-            }
-        } else if (tid * per < part) {
-#pragma unroll
-            for (int q = 0; q < PER; ++q) mine[q] = hist[first + q];
-        }
-    } else {
-        cluster.sync();                                  // every CTA has counted
-        if (tid * per < part) {
-#pragma unroll
-            for (int q = 0; q < (PER + 1) / 2; ++q) {    // (two CTAs or more)
-                if (q >= per) break;
-                int v[MAX_CLUSTER];
-#pragma unroll
-                for (int r = 0; r < MAX_CLUSTER; ++r) v[r] = r < C ? *cluster.map_shared_rank(hist + first + q, r) : 0;
-#pragma unroll
-                for (int r = 0; r < MAX_CLUSTER; ++r) mine[q] += v[r];
-            }
-        }
+        for (int q = 0; q < (G + 31) / 32; ++q)
+            if (lane + 32 * q < G) sum += hist[g * G + 32 * q + lane];
+        sum = __reduce_add_sync(0xffffffffu, sum);
+        if (lane == 0) s.groups[pass][g] = sum;
     }
-#pragma unroll
-    for (int q = 0; q < PER; ++q) sum += mine[q];
-    int total, upto = block_scan(sum, s.warp_sums, &total);
-    if (C > 1) {
-        if (tid < C) *cluster.map_shared_rank(&s.slice[rank], tid) = total;
-        cluster.sync();
-        for (int r = 0; r < rank; ++r) upto += s.slice[r];
-    }
-    if (upto >= want && upto - sum < want) {             // one thread of the cluster
-        int left = want - (upto - sum), at = 0, in = 0;
-        bool done = false;
-#pragma unroll
-        for (int q = 0; q < PER; ++q) {
-            if (!done) {
-                in = mine[q];
-                at = q;
-                done = left <= in;
-                if (!done) left -= in;
-            }
-        }
-        for (int r = 0; r < C; ++r) {
-            int* f = C == 1 ? s.found : cluster.map_shared_rank(s.found, r);
-            f[0] = first + at;
-            f[1] = left;
-            f[2] = in;
-        }
-    }
-    // (read by now: behind the barriers of the scan or the cluster)
-    for (int i = tid; i < BINS_ / 4; i += NT) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
     if (C > 1) cluster.sync();
     else __syncthreads();
+    if (warp == 0) {
+        int v[2] = {0, 0}, at = 0, left = 0, in = 0;
+        if (C == 1) {
+            v[0] = s.groups[pass][2 * lane];
+            v[1] = s.groups[pass][2 * lane + 1];
+        } else {
+            int x[MAX_CLUSTER][2];
+#pragma unroll
+            for (int r = 0; r < MAX_CLUSTER; ++r) {
+                const int2 y = r < C ? *reinterpret_cast<const int2*>(cluster.map_shared_rank(&s.groups[pass][2 * lane], r)) : make_int2(0, 0);
+                x[r][0] = y.x;
+                x[r][1] = y.y;
+            }
+#pragma unroll
+            for (int r = 0; r < MAX_CLUSTER; ++r) {
+                v[0] += x[r][0];
+                v[1] += x[r][1];
+            }
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, find_in_warp(v, want, &at, &left, &in));
+        const int src = __ffs(hit) - 1;
+        const int group = __shfl_sync(0xffffffffu, at, src), rest = __shfl_sync(0xffffffffu, left, src);
+        constexpr int PER = (G + 31) / 32;
+        int u[PER];
+#pragma unroll
+        for (int q = 0; q < PER; ++q) u[q] = 0;
+        if (lane * PER < G) {
+            const int* bins = hist + group * G + lane * PER;
+            for (int r = 0; r < C; ++r) {
+                const int* p = C == 1 ? bins : cluster.map_shared_rank(const_cast<int*>(bins), r);
+#pragma unroll
+                for (int q = 0; q < PER; ++q) u[q] += p[q];
+            }
+        }
+        if (find_in_warp(u, rest, &at, &left, &in)) {
+            s.found[0] = group * G + at;
+            s.found[1] = left;
+            s.found[2] = in;
+        }
+    }
+    __syncthreads();
 }
 
 __global__ void __launch_bounds__(NT, 1) kv_evict_kernel(const EvictArgs a, int C, int cap) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ Shared s;
     int* const hist = reinterpret_cast<int*>(smem);
-    uint32_t* const list = reinterpret_cast<uint32_t*>(smem) + BINS;
+    uint32_t* const list = reinterpret_cast<uint32_t*>(smem) + ALL_BINS;
     uint32_t* const held = list + MAX_LIST;
     cg::cluster_group cluster = cg::this_cluster();
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -255,7 +247,7 @@ __global__ void __launch_bounds__(NT, 1) kv_evict_kernel(const EvictArgs a, int 
     const int rank = C > 1 ? (int)cluster.block_rank() : 0, b = blockIdx.x / C;
     const int n = a.seq_lens[b];
     const int budget = max(0, a.budgets ? a.budgets[b] : a.budget);
-    for (int i = tid; i < BINS / 4; i += NT) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
+    for (int i = tid; i < ALL_BINS / 4; i += NT) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
     if (tid == 0) s.listed = 0;
     if (C > 1) cluster.sync();                           // every CTA runs, and has read the length
     else __syncthreads();
@@ -280,29 +272,53 @@ __global__ void __launch_bounds__(NT, 1) kv_evict_kernel(const EvictArgs a, int 
     // a key stays if its integer is below `top`, and of those equal to it the first `want`
     uint32_t top = 0;
     const bool formed = want > 0 && want < hi - lo;      // there is a choice: the integers are formed
+    // Eight integers of the warp's 256 keys of round k (any eight: lane l those from 8 l on where they are held);
+    // NONE for a key that is not among the lo .. hi - 1.
+    auto eight = [&](int k, uint32_t (&u)[ITEMS]) {
+        const int at = k * CHUNK + warp * 32 * ITEMS;
+        if (at < cap) {
+#pragma unroll
+            for (int q = 0; q < ITEMS; q += 4) {
+                const uint4 v = *reinterpret_cast<const uint4*>(held + at + lane * ITEMS + q);
+                u[q] = v.x; u[q + 1] = v.y; u[q + 2] = v.z; u[q + 3] = v.w;
+            }
+        } else {
+            const int j0 = k * step + mine0;
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i) {
+                const bool mid = (unsigned)(j0 + 32 * i - lo) < (unsigned)(hi - lo);
+                u[i] = mid ? order_of(weights[j0 + 32 * i]) : NONE;
+            }
+        }
+    };
     if (formed) {
         float w[ITEMS], next[ITEMS];
+        int zeros = 0;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) next[i] = mine0 + 32 * i < n ? weights[mine0 + 32 * i] : 0.f;
         for (int k = 0; k < rounds; ++k) {
-            const int j0 = k * step + mine0;
+            const int j0 = k * step + mine0, at = k * CHUNK + warp * 32 * ITEMS + lane;
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i) {
                 w[i] = next[i];
                 const int j = j0 + step + 32 * i;
-                next[i] = k + 1 < rounds && j < n ? weights[j] : 0.f;
+                next[i] = j < n ? weights[j] : 0.f;
             }
+            // (zeros, which may be many, are counted apart: they would wait for each other)
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i) {
-                const int j = j0 + 32 * i, at = k * CHUNK + i * NT + tid;
-                if (j - lane >= n) break;
-                const uint32_t u = order_of(w[i]);
-                if (at < cap) held[at] = u;
-                count(hist, j >= lo && j < hi, u >> (32 - BITS0));
+                const bool mid = (unsigned)(j0 + 32 * i - lo) < (unsigned)(hi - lo);
+                const uint32_t u = mid ? order_of(w[i]) : NONE;
+                if (at < cap) held[at + 32 * i] = u;
+                if (u < NONE && u != ZERO) atomicAdd(&hist[u >> (32 - BITS0)], 1);
+                zeros += u == ZERO;
             }
         }
-        find_bin<BINS>(cluster, C, rank, hist, s, want);
+        zeros = __reduce_add_sync(0xffffffffu, zeros);
+        if (lane == 0 && zeros) atomicAdd(&hist[ZERO >> (32 - BITS0)], zeros);
+        find_bin<BINS>(cluster, C, 0, hist, s, want);
         int shift = 32 - BITS0;
+        int* bins = hist + BINS;
         bool listed = false;
 #pragma unroll 1
         for (;;) {
@@ -316,36 +332,39 @@ __global__ void __launch_bounds__(NT, 1) kv_evict_kernel(const EvictArgs a, int 
             if (shift == 0) break;
             const int bits = shift == 32 - BITS0 ? BITS1 : BITS2, above = shift;
             shift -= bits;
-            auto put = [&](uint32_t u) { atomicAdd(&hist[(u >> shift) & ((1u << bits) - 1u)], 1); };
+            auto put = [&](uint32_t u) { atomicAdd(&bins[(u >> shift) & ((1u << bits) - 1u)], 1); };
             if (listed) {
                 const int m = s.listed;
                 for (int i = tid; i < m; i += NT)
-                    if ((list[i] >> above) == (top >> above)) put(list[i]);
+                    if (list[i] - top < 1u << above) put(list[i]);
             } else {
                 for (int k = 0; k < rounds; ++k) {
-                    const int j0 = k * step + mine0;
+                    uint32_t u[ITEMS];
+                    eight(k, u);
+                    bool any = false;
+#pragma unroll
+                    for (int i = 0; i < ITEMS; ++i) any |= u[i] - top < 1u << above;
+                    if (!__any_sync(0xffffffffu, any)) continue;
 #pragma unroll
                     for (int i = 0; i < ITEMS; ++i) {
-                        const int j = j0 + 32 * i, at = k * CHUNK + i * NT + tid;
-                        if (j - lane >= n) break;
-                        const uint32_t u = at < cap ? held[at] : j < n ? order_of(weights[j]) : ~0u;
-                        const bool in = j >= lo && j < hi && (u >> above) == (top >> above);
+                        const bool in = u[i] - top < 1u << above;
                         const unsigned m = __ballot_sync(0xffffffffu, in);
                         if (m == 0) continue;
                         int base = 0;
                         if (lane == 0) base = s.listed <= MAX_LIST ? atomicAdd(&s.listed, __popc(m)) : MAX_LIST;
                         base = __shfl_sync(0xffffffffu, base, 0) + __popc(m & ((1u << lane) - 1u));
                         if (in) {
-                            if (base < MAX_LIST) list[base] = u;
-                            put(u);
+                            if (base < MAX_LIST) list[base] = u[i];
+                            put(u[i]);
                         }
                     }
                 }
             }
             __syncthreads();                             // (found has been read, the list is there)
             listed = s.listed <= MAX_LIST;
-            if (bits == BITS1) find_bin<1 << BITS1>(cluster, C, rank, hist, s, want);
-            else find_bin<1 << BITS2>(cluster, C, rank, hist, s, want);
+            if (bits == BITS1) find_bin<1 << BITS1>(cluster, C, 1, bins, s, want);
+            else find_bin<1 << BITS2>(cluster, C, 2, bins, s, want);
+            bins += 1 << BITS1;
         }
     } else if (want <= 0) {
         want = 0;                                        // none, not even of the first
@@ -358,17 +377,19 @@ __global__ void __launch_bounds__(NT, 1) kv_evict_kernel(const EvictArgs a, int 
         // each warp's counts of its 256 keys, for the second kernel
         const int chunks = (a.slot_stride + CHUNK - 1) / CHUNK;
         for (int k = 0; k < rounds; ++k) {
-            const int j0 = k * step + mine0, g = k * C + rank;
-            int all = 0;
+            const int g = k * C + rank, w0 = k * step + rank * CHUNK + warp * 32 * ITEMS, w1 = w0 + 32 * ITEMS;
+            int stay = 0, tie = 0;
+            uint32_t u[ITEMS];
+            if (formed) eight(k, u);
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i) {
-                const int j = j0 + 32 * i, at = k * CHUNK + i * NT + tid;
-                if (j - lane >= n) break;
-                const uint32_t u = j >= n ? ~0u : formed && at < cap ? held[at] : order_of(weights[j]);
-                const bool mid = j >= lo && j < hi;
-                all += __popc(__ballot_sync(0xffffffffu, j < n && (!mid || u < top))) |
-                       __popc(__ballot_sync(0xffffffffu, mid && u == top)) << 16;
+                stay += formed && u[i] < top;
+                tie += formed && u[i] == top;
             }
+            int all = __reduce_add_sync(0xffffffffu, stay | tie << 16);
+            // and the warp's keys outside of lo .. hi - 1; without a choice all of those inside or none
+            all += max(0, min(w1, lo) - min(w0, lo)) + max(0, min(w1, n) - max(min(w0, n), hi));
+            if (!formed && want) all += max(0, min(w1, hi) - max(w0, lo));
             if (g >= chunks) break;
             if (lane == 0) {
                 s.warp_sums[warp] = all;
@@ -414,6 +435,7 @@ __global__ void __launch_bounds__(NT, 1) kv_evict_kernel(const EvictArgs a, int 
         a.lens_out[b] = K;
         if (a.n_freed) a.n_freed[b] = n - K;
     }
+    if (C > 1) cluster.sync();                           // nobody looks at this CTA's shared memory any more
 }
 
 // The second kernel: a CTA 2048 keys, a warp 256.
@@ -469,7 +491,7 @@ cudaError_t launch_kv_evict(const EvictArgs& a, int B, int C, int dev, cudaStrea
         cudaError_t e = cudaFuncSetAttribute(kv_evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(kv_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (BINS + MAX_LIST + MAX_HELD) * 4);
+                                     (ALL_BINS + MAX_LIST + MAX_HELD) * 4);
         if (e != cudaSuccess) return e;
         attr_set[dev].store(true, std::memory_order_release);
     }
@@ -478,7 +500,7 @@ cudaError_t launch_kv_evict(const EvictArgs& a, int B, int C, int dev, cudaStrea
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(B * C));
     cfg.blockDim = dim3(NT);
-    cfg.dynamicSmemBytes = (size_t)(BINS + MAX_LIST + cap) * 4;
+    cfg.dynamicSmemBytes = (size_t)(ALL_BINS + MAX_LIST + cap) * 4;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
