@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(NT, 1) key_weights_kernel(const WeightArgs a) 
         const float off = -lse * LOG2E;
         RowRule rule;
         if (RULES) rule = a.rules.row(b, t, row_ok ? (row0 + r) % a.H : 0, p + gap, a.slot_stride, false);
-        const float cap_in = RULES && a.rules.softcap > 0.f ? 2.f * c2 / a.rules.softcap : 0.f;
+        const float cap_in = RULES && a.rules.softcap > 0.f ? c2 / (a.rules.softcap * LOG2E) : 0.f;
         const float cap_out = RULES ? a.rules.softcap * LOG2E : 0.f;
         int ring = set;
         for (int i = set; i < T; i += 2) {
@@ -529,18 +529,38 @@ __global__ void __launch_bounds__(NT, 1) key_weights_kernel(const WeightArgs a) 
                 for (int k = 0; k < KW; ++k) {
                     float dot = __uint_as_float(va[k]);
                     if (FP8) dot = fmaf(fmaf(__uint_as_float(vl[k]), 0.0625f, dot), ks[k], __uint_as_float(vc[k]));
-                    float x;
-                    if (RULES) {
-                        x = a.rules.softcap > 0.f ? fmaf(capped(dot * cap_in), cap_out, off) : fmaf(dot, c2, off);
-                        if (a.rules.slopes) {
-                            const int kp = a.rules.key_pos ? M->key_pos[ring][g + k] : kg + k + (kg + k >= gap_at ? gap : 0);
-                            x = fmaf((float)(kp - rule.pos), rule.slope, x);
+                    e[k] = RULES && a.rules.softcap > 0.f ? dot * cap_in : fmaf(dot, c2, off);
+                }
+                if (RULES && a.rules.softcap > 0.f) {
+                    float top = 0.f;
+#pragma unroll
+                    for (int k = 0; k < KW; ++k) top = fmaxf(top, fabsf(e[k]));
+                    // scores within the cap, as nearly all are, take the polynomial alone
+                    if (__all_sync(0xffffffffu, top <= 1.f)) {
+#pragma unroll
+                        for (int k = 0; k < KW; k += 2) {
+                            const float2 y = fma2(tanh_near(make_float2(e[k], e[k + 1])), both(cap_out), both(off));
+                            e[k] = y.x;
+                            e[k + 1] = y.y;
                         }
                     } else {
-                        x = fmaf(dot, c2, off);
+#pragma unroll
+                        for (int k = 0; k < KW; k += 2) {
+                            const float2 y = fma2(tanh2(make_float2(e[k], e[k + 1])), both(cap_out), both(off));
+                            e[k] = y.x;
+                            e[k + 1] = y.y;
+                        }
                     }
-                    e[k] = live ? ex2(x) : 0.f;
                 }
+                if (RULES && a.rules.slopes) {
+#pragma unroll
+                    for (int k = 0; k < KW; ++k) {
+                        const int kp = a.rules.key_pos ? M->key_pos[ring][g + k] : kg + k + (kg + k >= gap_at ? gap : 0);
+                        e[k] = fmaf((float)(kp - rule.pos), rule.slope, e[k]);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < KW; ++k) e[k] = live ? ex2(e[k]) : 0.f;
                 if (RULES && a.rules.masked) {
 #pragma unroll
                     for (int k = 0; k < KW; ++k) {

@@ -101,8 +101,8 @@ __host__ __device__ inline Layout layout_for(int R, int RQ, int nq_s, int stages
     L.kv = (nq_s * RQ * 128 + 1023) / 1024 * 1024;
     L.p = L.kv + stages * STAGE_BYTES;
     L.misc = (L.p + R * NK * 2 + 127) / 128 * 128;
-    // barriers, TMEM base and abort flag; a key's scale, log2, inverse (position, document); a row's factor
-    L.total = L.misc + BAR_BYTES + MAX_STAGES * NK * (rules ? 20 : 12) + 512;
+    // barriers, TMEM base and abort flag; a key's scale, log2, inverse (and distance); a row's factor (and spans)
+    L.total = L.misc + BAR_BYTES + MAX_STAGES * NK * (rules ? 16 : 12) + 512 + (rules ? MAX_STAGES * WIDE_WARPS * 16 : 0);
     return L;
 }
 
@@ -136,12 +136,13 @@ struct Misc {
     uint64_t* bars;
     uint32_t* tmem_slot;
     volatile int* abort;
-    float2* key_sl;               // [stage][NK]: scale (NaN: the key holds a NaN), log2 of the clamped scale
+    float2* key_sl;               // [stage][NK]: scale (NaN: the key holds a NaN), log2 of the clamped scale;
+                                  // the RULES form: [stage][2][NK], scales, then logarithms
     float* key_inv;               // [stage][NK]: 1 / clamped scale (finite: a masked key's P of 0 stays 0)
     float* row_f;                 // [128]: the power of two that a query row was divided by, alpha while the
                                   // loop runs, 1 / l in the epilogue (the row's own thread reads the first)
-    int* key_pos;                 // [stage][NK], the RULES form: position
-    int* key_doc;                 // [stage][NK]: document
+    float* key_far;               // [stage][NK], the RULES form: position less the stream's last
+    int4* key_span;               // [stage][gather warp]: least and largest position, least and largest document
 };
 __device__ __forceinline__ Misc misc_at(uint8_t* smem, int off) {
     Misc m;
@@ -151,8 +152,8 @@ __device__ __forceinline__ Misc misc_at(uint8_t* smem, int off) {
     m.key_sl = reinterpret_cast<float2*>(smem + off + BAR_BYTES);
     m.key_inv = reinterpret_cast<float*>(smem + off + BAR_BYTES + MAX_STAGES * NK * 8);
     m.row_f = reinterpret_cast<float*>(smem + off + BAR_BYTES + MAX_STAGES * NK * 12);
-    m.key_pos = reinterpret_cast<int*>(m.row_f + 128);
-    m.key_doc = m.key_pos + MAX_STAGES * NK;
+    m.key_far = m.row_f + 128;
+    m.key_span = reinterpret_cast<int4*>(m.key_far + MAX_STAGES * NK);
     return m;
 }
 
@@ -238,6 +239,9 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
     const int64_t part_row_step = a.balanced ? 1 : a.nsplit;
     const int T = misaligned ? 0 : (k_end - k_begin + NK - 1) / NK;
     const int p = n - a.q_len;                           // first draft key
+    // First key of the i-th tile.  Under a bias by distance the tiles come from the last one back: near keys
+    // usually weigh most, and from the first tile on the maximum would rise with every tile, and O^T be rescaled.
+    auto tile_at = [&](int i) -> int { return k_begin + (RULES && a.rules.slopes ? T - 1 - i : i) * NK; };
 
     // ---- set-up: barriers and TMEM
     if (warp == 0) {
@@ -357,7 +361,7 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
         auto load_slots = [&](int t0) -> int {
             const int t = t0 + (lane >> 3);
             if (t >= T) return 0;
-            const int v = min(k_begin + t * NK + WK * w + min(lane & 7, WK - 1), k_end - 1);   // past the split: a valid key
+            const int v = min(tile_at(t) + WK * w + min(lane & 7, WK - 1), k_end - 1);   // past the split: a valid key
             return __ldg(slot_row + (RULES && v >= gap_at ? v + gap : v));
         };
         int cur = load_slots(0), nxt = load_slots(4);
@@ -366,6 +370,8 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
             float scale;
             int pos, doc;                                // RULES
         };
+        const int last_pos = RULES && a.rules.key_pos && !bad_len ? __ldg(a.rules.key_pos + (int64_t)b * a.slot_stride + p + gap + a.q_len - 1)
+                                                                  : p + gap + a.q_len - 1;
         auto load_tile = [&](Raw& r, int j) {
             if (j >= T) return;
             if ((j & 3) == 0) {
@@ -386,7 +392,7 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
             }
             r.scale = __ldg(a.kscale + sl);
             if (RULES) {
-                const int v = min(k_begin + j * NK + WK * w + min(lane & 7, WK - 1), k_end - 1);
+                const int v = min(tile_at(j) + WK * w + min(lane & 7, WK - 1), k_end - 1);
                 r.pos = v >= gap_at ? v + gap : v;
                 r.doc = a.rules.key_doc ? __ldg(a.rules.key_doc + (int64_t)b * a.slot_stride + r.pos) : -1;
                 if (a.rules.key_pos) r.pos = __ldg(a.rules.key_pos + (int64_t)b * a.slot_stride + r.pos);
@@ -447,12 +453,20 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
             }
             if (lane < WK) {
                 const float cl = fmaxf(sc, MIN_SCALE);
-                M.key_sl[st * NK + WK * w + lane] = make_float2(sc, log2f(cl));
-                M.key_inv[st * NK + WK * w + lane] = 1.f / cl;
                 if (RULES) {
-                    M.key_pos[st * NK + WK * w + lane] = r.pos;
-                    M.key_doc[st * NK + WK * w + lane] = r.doc;
+                    float* sl = reinterpret_cast<float*>(M.key_sl + st * NK);
+                    sl[WK * w + lane] = sc;
+                    sl[NK + WK * w + lane] = log2f(cl);
+                    M.key_far[st * NK + WK * w + lane] = (float)((long long)r.pos - last_pos);
+                } else {
+                    M.key_sl[st * NK + WK * w + lane] = make_float2(sc, log2f(cl));
                 }
+                M.key_inv[st * NK + WK * w + lane] = 1.f / cl;
+            }
+            if (RULES && a.rules.masked) {               // (every lane holds one of the warp's keys)
+                const int4 span = make_int4(__reduce_min_sync(0xffffffffu, r.pos), __reduce_max_sync(0xffffffffu, r.pos),
+                                            __reduce_min_sync(0xffffffffu, r.doc), __reduce_max_sync(0xffffffffu, r.doc));
+                if (lane == 0) M.key_span[st * WIDE_WARPS + w] = span;
             }
             fence_proxy_async_smem();                    // generic stores -> tensor-core reads
             __syncwarp();
@@ -523,9 +537,29 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
         const int plain_end = min(p, k_end);             // keys below this need no mask (of drafts)
         RowRule rule;
         if (RULES) rule = a.rules.row(b, t, row_ok ? (row0 + r) % a.H : 0, p + gap, a.slot_stride, bad_len);
-        const float cap_in = RULES && a.rules.softcap > 0.f ? 2.f * c2 / a.rules.softcap : 0.f;
+        const float cap_in = RULES && a.rules.softcap > 0.f ? c2 / (a.rules.softcap * LOG2E) : 0.f;
         const float cap_out = RULES ? a.rules.softcap * LOG2E : 0.f;
+        // The bias is slope (key's distance from the stream's last position - the row's): the second part, the same
+        // for all of the row's keys, waits for the log-sum-exp.  Where it is large (bits would be lost beside it), or
+        // the distances are no fp32 numbers, the warp takes the differences of positions instead.
+        float bias0 = 0.f;
+        bool far = false;
+        if (RULES && a.rules.slopes && !bad_len) {
+            const int64_t last_at = (int64_t)b * a.slot_stride + p + gap + a.q_len - 1;
+            const long long off = (long long)rule.pos - (a.rules.key_pos ? __ldg(a.rules.key_pos + last_at) : p + gap + a.q_len - 1);
+            far = __any_sync(0xffffffffu, off > (1 << 24) || off < -(1 << 24) || !(fabsf((float)off * rule.slope) <= 64.f));
+            if (!far) bias0 = -(float)off * rule.slope;
+        }
         const bool rows_used = quad * 32 < R;
+        // position and document of visible key v (behind the split: of its last)
+        auto key_index = [&](int v) -> int64_t {
+            v = min(v, k_end - 1);
+            return (int64_t)b * a.slot_stride + (v >= gap_at ? v + gap : v);
+        };
+        auto key_pos = [&](int v) -> int {
+            return a.rules.key_pos ? __ldg(a.rules.key_pos + key_index(v)) : (v >= gap_at ? v + gap : v);
+        };
+        auto key_doc = [&](int v) -> int { return a.rules.key_doc ? __ldg(a.rules.key_doc + key_index(v)) : -1; };
         float m = -INFINITY, l = 0.f;
         bool ok = true;
         for (int i = 0; i < T; ++i) {
@@ -536,7 +570,7 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
             tc_fence_after();
             float x[NK];
             float mt = -INFINITY;
-            const int k0 = k_begin + i * NK;
+            const int k0 = tile_at(i);
             const float2* sl = M.key_sl + st * NK;
             const float* inv = M.key_inv + st * NK;
             if (ok && !rows_used) {                      // no row of this warp is in the tile
@@ -553,32 +587,83 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&M.bars[B_S_FREE]);
+                if constexpr (!RULES) {
 #pragma unroll
                 for (int k = 0; k < NK; k += 2) {
                     const float4 c = *reinterpret_cast<const float4*>(sl + k);
                     x[k] = fmaf(fmaf(__uint_as_float(va[k / 16][k % 16]), c.x, __uint_as_float(vc[k / 16][k % 16])), c2, c.y);
                     x[k + 1] = fmaf(fmaf(__uint_as_float(va[k / 16][k % 16 + 1]), c.z, __uint_as_float(vc[k / 16][k % 16 + 1])), c2, c.w);
                 }
-                if (RULES) {
-                    const int* kp = M.key_pos + st * NK;
-                    if (a.rules.softcap > 0.f) {
+                } else {
+                    const float* ks = reinterpret_cast<const float*>(sl);
+                    const bool cap = a.rules.softcap > 0.f;
+                    float top = 0.f;
 #pragma unroll
-                        for (int k = 0; k < NK; ++k) {
-                            const float dot = fmaf(__uint_as_float(va[k / 16][k % 16]), sl[k].x, __uint_as_float(vc[k / 16][k % 16]));
-                            x[k] = fmaf(capped(dot * cap_in), cap_out, sl[k].y);
+                    for (int k = 0; k < NK; k += 2) {
+                        float2 y = fma2(make_float2(__uint_as_float(va[k / 16][k % 16]), __uint_as_float(va[k / 16][k % 16 + 1])),
+                                        *reinterpret_cast<const float2*>(ks + k),
+                                        make_float2(__uint_as_float(vc[k / 16][k % 16]), __uint_as_float(vc[k / 16][k % 16 + 1])));
+                        if (cap) {
+                            y = mul2(y, both(cap_in));
+                            top = fmaxf(top, fmaxf(fabsf(y.x), fabsf(y.y)));
+                        } else {
+                            y = fma2(y, both(c2), *reinterpret_cast<const float2*>(ks + NK + k));
+                        }
+                        x[k] = y.x;
+                        x[k + 1] = y.y;
+                    }
+                    if (cap) {
+                        // scores within the cap, as nearly all are, take the polynomial alone
+                        if (__all_sync(0xffffffffu, top <= 1.f)) {
+#pragma unroll
+                            for (int k = 0; k < NK; k += 2) {
+                                const float2 y = fma2(tanh_near(make_float2(x[k], x[k + 1])), both(cap_out), *reinterpret_cast<const float2*>(ks + NK + k));
+                                x[k] = y.x;
+                                x[k + 1] = y.y;
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < NK; k += 2) {
+                                const float2 y = fma2(tanh2(make_float2(x[k], x[k + 1])), both(cap_out), *reinterpret_cast<const float2*>(ks + NK + k));
+                                x[k] = y.x;
+                                x[k + 1] = y.y;
+                            }
                         }
                     }
                     if (a.rules.slopes) {
+                        if (!far) {
+                            const float* kf = M.key_far + st * NK;
 #pragma unroll
-                        for (int k = 0; k < NK; ++k) x[k] = fmaf((float)(kp[k] - rule.pos), rule.slope, x[k]);
+                            for (int k = 0; k < NK; k += 2) {
+                                const float2 y = fma2(*reinterpret_cast<const float2*>(kf + k), both(rule.slope), make_float2(x[k], x[k + 1]));
+                                x[k] = y.x;
+                                x[k + 1] = y.y;
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < NK; ++k)
+                                x[k] = fmaf((float)(key_pos(k0 + k) - rule.pos), rule.slope, x[k]);
+                        }
                     }
                     if (a.rules.masked) {
-                        const int* kd = M.key_doc + st * NK;
+                        // the tile's keys as a whole, and one by one only where that does not decide
+                        int4 span = M.key_span[st * WIDE_WARPS];
 #pragma unroll
-                        for (int k = 0; k < NK; ++k) {
-                            const int j = k0 + k - p;    // draft index, < 0: before the drafts
-                            const bool draft_ok = j < 0 || ((vis >> (j & 63)) & 1ull);
-                            if (!rule.sees(draft_ok, kp[k], kd[k])) x[k] = -INFINITY;
+                        for (int g = 1; g < WIDE_WARPS; ++g) {
+                            const int4 o = M.key_span[st * WIDE_WARPS + g];
+                            span = make_int4(min(span.x, o.x), max(span.y, o.y), min(span.z, o.z), max(span.w, o.w));
+                        }
+                        const bool drafts = k0 + NK > p;
+                        const bool none = rule.none(span);
+                        if (!__all_sync(0xffffffffu, none || (!drafts && rule.all(span)))) {
+#pragma unroll
+                            for (int k = 0; k < NK; ++k) {
+                                const int j = k0 + k - p;    // draft index, < 0: before the drafts
+                                if (!rule.sees(j < 0 || ((vis >> (j & 63)) & 1ull), key_pos(k0 + k), key_doc(k0 + k))) x[k] = -INFINITY;
+                            }
+                        } else if (none) {
+#pragma unroll
+                            for (int k = 0; k < NK; ++k) x[k] = -INFINITY;
                         }
                     }
                 }
@@ -662,7 +747,7 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
 
         float rinv, lse_v;
         if (bad_len) { rinv = 0.f; lse_v = __int_as_float(0x7fc00000); }
-        else if (l != 0.f) { rinv = 1.f / l; lse_v = (m - P_SHIFT + log2f(l)) * LN2; }   // NaN stays NaN
+        else if (l != 0.f) { rinv = 1.f / l; lse_v = (m - P_SHIFT + log2f(l) + (RULES ? bias0 : 0.f)) * LN2; }   // NaN stays NaN
         else { rinv = 0.f; lse_v = -INFINITY; }
         M.row_f[r] = rinv;
         const int64_t grow0 = (int64_t)b * rows + row0;

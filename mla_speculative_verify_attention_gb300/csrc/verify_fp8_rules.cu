@@ -30,6 +30,9 @@ extern "C" int mla_verify_attn_fp8_rules(const void* q, const uint8_t* kv_lat, c
     ScoreRules rules;
     const int rc = check_rules(softcap, slopes, key_pos, window, prefix_lens, key_doc, &rules);
     if (rc != MLA_OK) return rc;
+    if (softcap == 0.f && !slopes && !rules.masked)      // no rule: positions alone change nothing
+        return mla_verify_attn_fp8(q, kv_lat, kv_scale, kv_rope, n_pool, slot_table, slot_stride, seq_lens, draft_mask,
+                                   draft_mask_bits, B, q_len, H, scale, out, lse, nsplit, workspace, ws_bytes, stream);
     return verify_fp8_call<true>(q, kv_lat, kv_scale, kv_rope, n_pool, slot_table, slot_stride, seq_lens, draft_mask,
                                  draft_mask_bits, B, q_len, H, scale, rules, out, lse, nsplit, workspace, ws_bytes,
                                  stream);

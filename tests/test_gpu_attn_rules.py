@@ -63,9 +63,9 @@ def test_no_rules_is_the_plain_attention(cuda_lib):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
-@pytest.mark.parametrize("cap", [0.05, 1.0, 1e4, 1e30])
+@pytest.mark.parametrize("cap", [0.05, 1.0, 4.0, 30.0, 1e4, 1e30])
 def test_caps(cuda_lib, cap):
-    """Small caps flatten every score, huge ones leave them: tanh is right near zero and far out."""
+    """Small caps flatten every score, huge ones leave them: tanh is right near zero, far out and between."""
     check(cuda_lib, lr.Step(9, [130, 60], 4, 8, q_size=4.0), lr.Rules(softcap=cap))
 
 
@@ -112,6 +112,17 @@ def test_far_positions(cuda_lib):
         pos = lr.gaps(3, 2, s.stride, start=start)
         check(cuda_lib, s, lr.Rules(slopes=lr.slopes(4), key_pos=pos, window=60))
         check(cuda_lib, s, lr.Rules(slopes=-lr.slopes(4), key_pos=pos, window=2 ** 31 - 1))
+
+
+@pytest.mark.parametrize("spread", [2 ** 20, 2 ** 24, 2 ** 26, 2 ** 30])
+def test_drafts_far_apart(cuda_lib, spread):
+    """Positions of keys and drafts alike all over a wide range: distances of a few next to far ones."""
+    s = lr.Step(20, [190, 70], 6, 4, mask="tree")
+    r = np.random.default_rng(3)
+    pos = (r.integers(0, 4, (2, s.stride)) * (spread // 4) + r.integers(0, 50, (2, s.stride))).astype(np.int32)
+    for slopes in (lr.slopes(4) * np.float32(8.0 / spread), lr.slopes(4)):
+        check(cuda_lib, s, lr.Rules(slopes=slopes, key_pos=pos))
+    check(cuda_lib, s, lr.Rules(slopes=slopes, key_pos=pos, window=spread // 4, prefix_lens=np.array([9, 30], np.int32)))
 
 
 def test_positions_in_any_order(cuda_lib):
