@@ -595,49 +595,54 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
                     x[k + 1] = fmaf(fmaf(__uint_as_float(va[k / 16][k % 16 + 1]), c.z, __uint_as_float(vc[k / 16][k % 16 + 1])), c2, c.w);
                 }
                 } else {
-                    const float* ks = reinterpret_cast<const float*>(sl);
+                    // (four keys a read of shared memory: its queue is the gather's too)
+                    const float4* ks = reinterpret_cast<const float4*>(sl);
+                    const float4* kl = ks + NK / 4;
                     const bool cap = a.rules.softcap > 0.f;
-                    float top = 0.f;
+                    auto pair = [&](int k) { return make_float2(x[k], x[k + 1]); };
+                    auto put = [&](int k, float2 y) { x[k] = y.x; x[k + 1] = y.y; };
+                    auto accs = [](const uint32_t (&v)[NK / 16][16], int k) {
+                        return make_float2(__uint_as_float(v[k / 16][k % 16]), __uint_as_float(v[k / 16][k % 16 + 1]));
+                    };
 #pragma unroll
-                    for (int k = 0; k < NK; k += 2) {
-                        float2 y = fma2(make_float2(__uint_as_float(va[k / 16][k % 16]), __uint_as_float(va[k / 16][k % 16 + 1])),
-                                        *reinterpret_cast<const float2*>(ks + k),
-                                        make_float2(__uint_as_float(vc[k / 16][k % 16]), __uint_as_float(vc[k / 16][k % 16 + 1])));
-                        if (cap) {
-                            y = mul2(y, both(cap_in));
-                            top = fmaxf(top, fmaxf(fabsf(y.x), fabsf(y.y)));
-                        } else {
-                            y = fma2(y, both(c2), *reinterpret_cast<const float2*>(ks + NK + k));
-                        }
-                        x[k] = y.x;
-                        x[k + 1] = y.y;
+                    for (int k = 0; k < NK; k += 4) {
+                        const float4 c = ks[k / 4];
+                        put(k, fma2(accs(va, k), make_float2(c.x, c.y), accs(vc, k)));
+                        put(k + 2, fma2(accs(va, k + 2), make_float2(c.z, c.w), accs(vc, k + 2)));
                     }
+                    float gain = c2;
                     if (cap) {
-                        // scores within the cap, as nearly all are, take the polynomial alone
-                        if (__all_sync(0xffffffffu, top <= 1.f)) {
+                        float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                            for (int k = 0; k < NK; k += 2) {
-                                const float2 y = fma2(tanh_near(make_float2(x[k], x[k + 1])), both(cap_out), *reinterpret_cast<const float2*>(ks + NK + k));
-                                x[k] = y.x;
-                                x[k + 1] = y.y;
-                            }
+                        for (int k = 0; k < NK; k += 2) {
+                            put(k, mul2(pair(k), both(cap_in)));
+                            top[k & 2] = fmaxf(top[k & 2], fabsf(x[k]));
+                            top[(k & 2) + 1] = fmaxf(top[(k & 2) + 1], fabsf(x[k + 1]));
+                        }
+                        // scores within the cap, as nearly all are, take the polynomial alone
+                        if (__all_sync(0xffffffffu, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) <= 1.f)) {
+#pragma unroll
+                            for (int k = 0; k < NK; k += 2) put(k, tanh_near(pair(k)));
                         } else {
 #pragma unroll
-                            for (int k = 0; k < NK; k += 2) {
-                                const float2 y = fma2(tanh2(make_float2(x[k], x[k + 1])), both(cap_out), *reinterpret_cast<const float2*>(ks + NK + k));
-                                x[k] = y.x;
-                                x[k + 1] = y.y;
-                            }
+                            for (int k = 0; k < NK; k += 2) put(k, tanh2(pair(k)));
                         }
+                        gain = cap_out;
+                    }
+#pragma unroll
+                    for (int k = 0; k < NK; k += 4) {
+                        const float4 c = kl[k / 4];
+                        put(k, fma2(pair(k), both(gain), make_float2(c.x, c.y)));
+                        put(k + 2, fma2(pair(k + 2), both(gain), make_float2(c.z, c.w)));
                     }
                     if (a.rules.slopes) {
                         if (!far) {
-                            const float* kf = M.key_far + st * NK;
+                            const float4* kf = reinterpret_cast<const float4*>(M.key_far + st * NK);
 #pragma unroll
-                            for (int k = 0; k < NK; k += 2) {
-                                const float2 y = fma2(*reinterpret_cast<const float2*>(kf + k), both(rule.slope), make_float2(x[k], x[k + 1]));
-                                x[k] = y.x;
-                                x[k + 1] = y.y;
+                            for (int k = 0; k < NK; k += 4) {
+                                const float4 c = kf[k / 4];
+                                put(k, fma2(make_float2(c.x, c.y), both(rule.slope), pair(k)));
+                                put(k + 2, fma2(make_float2(c.z, c.w), both(rule.slope), pair(k + 2)));
                             }
                         } else {
 #pragma unroll
@@ -647,12 +652,9 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
                     }
                     if (a.rules.masked) {
                         // the tile's keys as a whole, and one by one only where that does not decide
-                        int4 span = M.key_span[st * WIDE_WARPS];
-#pragma unroll
-                        for (int g = 1; g < WIDE_WARPS; ++g) {
-                            const int4 o = M.key_span[st * WIDE_WARPS + g];
-                            span = make_int4(min(span.x, o.x), max(span.y, o.y), min(span.z, o.z), max(span.w, o.w));
-                        }
+                        const int4 part = M.key_span[st * WIDE_WARPS + (lane & (WIDE_WARPS - 1))];
+                        const int4 span = make_int4(__reduce_min_sync(0xffffffffu, part.x), __reduce_max_sync(0xffffffffu, part.y),
+                                                    __reduce_min_sync(0xffffffffu, part.z), __reduce_max_sync(0xffffffffu, part.w));
                         const bool drafts = k0 + NK > p;
                         const bool none = rule.none(span);
                         if (!__all_sync(0xffffffffu, none || (!drafts && rule.all(span)))) {
