@@ -338,7 +338,7 @@ size_t mla_verify_fp8_workspace_bytes(int B, int q_len, int H, int max_seq, int 
  *   prefix_lens int32 [B], or NULL: no prefix.  Prefix keys are visible both ways: a draft whose own
  *               position is in the prefix is seen by every draft of its stream.
  *   key_doc     int32 [B, slot_stride], or NULL: one document.  A negative number is shared by all.
- * tanh is off by at most 2^-19 of itself.  A row that sees nothing gets out = 0, lse = -inf.  Every other
+ * tanh is off by at most 2^-21 of itself.  A row that sees nothing gets out = 0, lse = -inf.  Every other
  * argument, limit and error is that of mla_verify_attn_fp8(); with nsplit = 0 the workspace that it uses is
  * mla_verify_fp8_workspace_bytes() of max_seq = slot_stride, or of min(slot_stride, window - 1 + q_len)
  * with a window and no key_pos.
@@ -356,15 +356,18 @@ int mla_verify_attn_fp8_rules(const void* q, const uint8_t* kv_lat, const float*
  *     out[b, j] = decay * weights[b, j] + new[b, j]     j < seq_lens[b] - q_len
  *     out[b, j] = new[b, j]                             the drafts' own keys (new in the table)
  * with the scores z and the visibility of mla_verify_attn_fp8_rules(), and lse as the attention left it.
- * What mla_kv_evict() chooses by.  The keys enter the scores without a rounding of their own, the queries
- * as in mla_verify_attn_fp8().  Sums are fp32 in a fixed order: equal calls give equal bits.
+ * What mla_kv_evict() chooses by.  The keys enter the scores without a rounding of their own; so do the queries
+ * over the bf16 cache, and over the fp8 cache down to 2^-13 of a row's largest element (smaller ones to within
+ * 2^-20 of the largest; a row with an infinity or a NaN gives NaN).  Sums are fp32 in a fixed order: equal calls
+ * give equal bits.
  *   lse      fp32 [B, q_len, H]; a row with lse -inf saw nothing and adds nothing, one with NaN gives NaN
  *   counted  uint8 [B, q_len], or NULL: every draft counts (else e.g. only the accepted ones)
  *   weights  fp32 [B, slot_stride], or NULL: zeros;  decay finite
  *   out      fp32 [B, slot_stride], may be `weights`; entries from seq_lens[b] on stay as they were
  *   workspace  device scratch of ws_bytes >= mla_key_weights_workspace_bytes(); NULL where that is 0
  *   q, the cache, table, lengths, masks, rules, limits and errors as for mla_verify_attn_fp8_rules();
- *   of a stream with a bad length nothing is written.  slot_stride is at most MLA_MAX_FP8_KEYS.
+ *   of a stream with a bad length nothing is written.  slot_stride is at most MLA_MAX_FP8_KEYS.  Where a wait
+ *   expired (MLA_DEV_TIMEOUT), keys without a sum are NaN.
  * mla_key_weights() is the same over the bf16 cache [n_pool, 576] of mla_verify_attn().
  */
 int mla_key_weights_fp8(const void* q, const uint8_t* kv_lat, const float* kv_scale, const void* kv_rope,

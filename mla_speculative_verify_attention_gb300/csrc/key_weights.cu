@@ -584,6 +584,11 @@ __global__ void __launch_bounds__(NT, 1) key_weights_kernel(const WeightArgs a) 
             }
             if (bar_red_or(1 + set, 32 * SCORE_WARPS / 2, !ok)) {   // the sums are there, or a warp gives up
                 if (!ok && lane == 0) give_up(M, a.status);
+                // the set's keys from here on have no sum
+                for (; writer && i < T; i += 2) {
+                    const int u = k_begin + i * NK + lane;
+                    if (u < k_end) part[stream0 + (RULES && u >= gap_at ? u + gap : u)] = __int_as_float(0x7fc00000);
+                }
                 break;
             }
             if (mine) {

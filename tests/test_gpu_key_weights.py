@@ -209,3 +209,53 @@ def test_captured(cuda_lib, cache):
                                    None, 1.0, np.full((2, s.stride), -1.0))
         for o in outs:
             assert np.all(np.abs(ref.f64(o) - want) <= tol)
+
+
+@pytest.mark.parametrize("cache", ["fp8", "bf16"])
+@pytest.mark.parametrize("lens,q_len,H", [([1500], 9, 8), ([700, 60, 1300], 2, 4), ([400], 40, 16), ([60] * 70, 1, 8)])
+def test_expired_waits_end_the_call(cuda_lib, cache, lens, q_len, H):
+    """The first tile withheld by the test hook: the status says so, keys without a sum are NaN, and the next call
+    on the same buffers is right."""
+    mv = cuda_lib
+    s = lr.Step(55, lens, q_len, H, cache=cache)
+    lse = torch.from_numpy(true_lse(s, lr.Rules())).cuda()
+    args = s.on("cuda")
+    out = torch.zeros((s.B, s.stride), device="cuda")
+    mv.device_status(clear=True)
+    assert mv.load().mla_debug_stall_next_launch() == 0
+    call(mv, s, args, lse, out=out)
+    torch.cuda.synchronize()
+    assert mv.device_status(clear=True) == mv.DEV_TIMEOUT
+    for b, n in enumerate(lens):
+        assert torch.isnan(out[b, :n]).any() and (out[b, n:] == 0).all()
+    check(mv, s, lr.Rules())
+
+
+def test_no_streams(cuda_lib):
+    e = lambda *shape, dtype=torch.int32: torch.empty(shape, dtype=dtype, device="cuda")
+    q, kv = e(0, 3, 4, 576, dtype=torch.bfloat16), e(5, 576, dtype=torch.bfloat16)
+    assert cuda_lib.key_weights(q, kv, e(0, 9), e(0), None, 0.1, e(0, 3, 4, dtype=torch.float32)).shape == (0, 9)
+    assert cuda_lib.kv_evict(e(0, 9), e(0), e(0, 9, dtype=torch.float32), 4).n_freed.shape == (0,)
+
+
+def test_rows_of_every_size(cuda_lib):
+    """Queries whose elements differ by many orders of magnitude, tiny and huge rows: the two pieces of a query hold
+    it to 2^-20 of the row's largest element."""
+    s = lr.Step(57, [200], 4, 8)
+    g = torch.Generator().manual_seed(1)
+    spread = torch.exp2(torch.randint(-24, 1, s.q.shape, generator=g).float())
+    row = torch.exp2(torch.tensor([-120., -60., -8., -1., 0., 1., 3., 4.]))[None, None, :, None]
+    s.q = (s.q.float() * spread * row * 0.3).to(torch.bfloat16)
+    top = np.abs(ref.f64(s.q)).max(-1)
+    rules = lr.Rules()
+    lse = true_lse(s, rules)
+    k = np.abs(s.keys_of(0)[:200, :512]).sum(1).max()
+    extra = 2.0 ** -20 * top.max() * k * SCALE            # what the pieces leave out, as an error of the score
+    old = torch.zeros((1, s.stride), device="cuda")
+    got = call(cuda_lib, s, s.on("cuda"), torch.from_numpy(lse).cuda(), out=old)
+    want, tol = lr.key_weights(ref.f64(s.q), s.keys_of, s.seq, None, SCALE, rules, lse.astype(np.float64), None, None, 1.0,
+                               np.zeros((1, s.stride)))
+    assert np.all(np.abs(ref.f64(got) - want) <= tol + want * extra * 1.01)
+    s.q[0, 1, 3, 100] = float("inf")
+    got = call(cuda_lib, s, s.on("cuda"), torch.from_numpy(lse).cuda())
+    assert torch.isnan(got[0, :198]).all() and torch.isfinite(got[0, 198:200]).all()   # the keys that draft 1 sees
