@@ -650,31 +650,48 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
                                 x[k] = fmaf((float)(key_pos(k0 + k) - rule.pos), rule.slope, x[k]);
                         }
                     }
+                    // bit k: the row sees key k0 + k
+                    uint64_t see = ~0ull;
+                    if (k0 + NK > plain_end) {
+                        const int before = p - k0;       // keys of the tile before the drafts
+                        if (before < 64) see = before > 0 ? vis << before | ((1ull << before) - 1) : before > -64 ? vis >> -before : 0;
+                    }
                     if (a.rules.masked) {
                         // the tile's keys as a whole, and one by one only where that does not decide
                         const int4 part = M.key_span[st * WIDE_WARPS + (lane & (WIDE_WARPS - 1))];
                         const int4 span = make_int4(__reduce_min_sync(0xffffffffu, part.x), __reduce_max_sync(0xffffffffu, part.y),
                                                     __reduce_min_sync(0xffffffffu, part.z), __reduce_max_sync(0xffffffffu, part.w));
-                        const bool drafts = k0 + NK > p;
                         const bool none = rule.none(span);
-                        if (!__all_sync(0xffffffffu, none || (!drafts && rule.all(span)))) {
-#pragma unroll
+                        // (drafts in the prefix are seen whatever their mask says)
+                        if (__all_sync(0xffffffffu, none || (rule.all(span) && (k0 + NK <= p || span.x >= rule.prefix)))) {
+                            if (none) see = 0;
+                        } else {
+                            see = 0;
+                            // lane l holds keys l and 32 + (l & 15)
+                            const int v0 = k0 + lane, v1 = k0 + 32 + (lane & 15);
+                            const int pos0 = key_pos(v0), pos1 = key_pos(v1), doc0 = key_doc(v0), doc1 = key_doc(v1);
+#pragma unroll 1
                             for (int k = 0; k < NK; ++k) {
+                                const int kp = __shfl_sync(0xffffffffu, k < 32 ? pos0 : pos1, k & 31);
+                                const int kd = __shfl_sync(0xffffffffu, k < 32 ? doc0 : doc1, k & 31);
                                 const int j = k0 + k - p;    // draft index, < 0: before the drafts
-                                if (!rule.sees(j < 0 || ((vis >> (j & 63)) & 1ull), key_pos(k0 + k), key_doc(k0 + k))) x[k] = -INFINITY;
+                                see |= (uint64_t)rule.sees(j < 0 || ((vis >> (j & 63)) & 1ull), kp, kd) << k;
                             }
-                        } else if (none) {
-#pragma unroll
-                            for (int k = 0; k < NK; ++k) x[k] = -INFINITY;
                         }
+                    }
+                    if (k0 + NK > k_end) see &= (1ull << (k_end - k0)) - 1;
+                    if (__any_sync(0xffffffffu, (see & ((1ull << NK) - 1)) != (1ull << NK) - 1)) {
+#pragma unroll
+                        for (int k = 0; k < NK; ++k)
+                            if (!((see >> k) & 1ull)) x[k] = -INFINITY;
                     }
                 }
                 // rows past the tile need no mask of their own: nothing reads their P
-                if (k0 + NK > plain_end) {
+                if (!RULES && k0 + NK > plain_end) {
 #pragma unroll
                     for (int k = 0; k < NK; ++k) {
                         const int j = k0 + k;
-                        if (!(j < k_end && (j < p || (RULES && a.rules.masked) || ((vis >> (j - p)) & 1ull)))) x[k] = -INFINITY;
+                        if (!(j < k_end && (j < p || ((vis >> (j - p)) & 1ull)))) x[k] = -INFINITY;
                     }
                 }
                 float mx[4] = {x[0], x[1], x[2], x[3]};
