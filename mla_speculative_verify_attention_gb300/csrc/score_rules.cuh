@@ -82,7 +82,8 @@ struct ScoreRules {
     const int32_t* key_pos = nullptr;          // [B, slot_stride]; null: a key's index
     const int32_t* prefix_lens = nullptr;      // [B]
     const int32_t* key_doc = nullptr;          // [B, slot_stride]
-    int masked = 0;                            // a window, a prefix or documents
+    int masked = 0;                            // a window, a prefix or documents,
+    int spans = 0;                             // and positions or documents given key by key
 
     // The keys that have to be looked at: with given positions any of them may be visible.
     __host__ __device__ __forceinline__ KeySpan span() const {

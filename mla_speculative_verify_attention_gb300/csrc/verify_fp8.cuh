@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
                 }
                 M.key_inv[st * NK + WK * w + lane] = 1.f / cl;
             }
-            if (RULES && a.rules.masked) {               // (every lane holds one of the warp's keys)
+            if (RULES && a.rules.spans) {                // (every lane holds one of the warp's keys)
                 const int4 span = make_int4(__reduce_min_sync(0xffffffffu, r.pos), __reduce_max_sync(0xffffffffu, r.pos),
                                             __reduce_min_sync(0xffffffffu, r.doc), __reduce_max_sync(0xffffffffu, r.doc));
                 if (lane == 0) M.key_span[st * WIDE_WARPS + w] = span;
@@ -658,9 +658,15 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
                     }
                     if (a.rules.masked) {
                         // the tile's keys as a whole, and one by one only where that does not decide
-                        const int4 part = M.key_span[st * WIDE_WARPS + (lane & (WIDE_WARPS - 1))];
-                        const int4 span = make_int4(__reduce_min_sync(0xffffffffu, part.x), __reduce_max_sync(0xffffffffu, part.y),
-                                                    __reduce_min_sync(0xffffffffu, part.z), __reduce_max_sync(0xffffffffu, part.w));
+                        int4 span;
+                        if (a.rules.spans) {
+                            const int4 part = M.key_span[st * WIDE_WARPS + (lane & (WIDE_WARPS - 1))];
+                            span = make_int4(__reduce_min_sync(0xffffffffu, part.x), __reduce_max_sync(0xffffffffu, part.y),
+                                             __reduce_min_sync(0xffffffffu, part.z), __reduce_max_sync(0xffffffffu, part.w));
+                        } else {
+                            const int z = min(k0 + NK, k_end) - 1;
+                            span = make_int4(k0 >= gap_at ? k0 + gap : k0, z >= gap_at ? z + gap : z, -1, -1);
+                        }
                         const bool none = rule.none(span);
                         // (drafts in the prefix are seen whatever their mask says)
                         if (__all_sync(0xffffffffu, none || (rule.all(span) && (k0 + NK <= p || span.x >= rule.prefix)))) {

@@ -12,6 +12,7 @@ int check_rules(float softcap, const float* slopes, const int32_t* key_pos, int 
     r.softcap = softcap; r.window = window; r.slopes = slopes; r.key_pos = key_pos; r.prefix_lens = prefix_lens;
     r.key_doc = key_doc;
     r.masked = window > 0 || prefix_lens || key_doc;
+    r.spans = r.masked && (key_pos || key_doc);
     *out = r;
     return MLA_OK;
 }
