@@ -78,14 +78,14 @@ struct Keys {
     unsigned stay[ITEMS], tie[ITEMS];
 
     // Returns the warp's counts: stay | ties << 16.
-    __device__ __forceinline__ int load(const EvictArgs& a, const Border& o, int64_t row, int j0) {
+    __device__ __forceinline__ int load(const EvictArgs& a, const Border& o, int64_t row, int j0, int items) {
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
             const int j = j0 + 32 * i;
             w[i] = 0.f;
             slot[i] = doc[i] = 0;
             pos[i] = j;
-            if (j < o.n) {
+            if (i < items && j < o.n) {
                 w[i] = a.weights[row + j];
                 slot[i] = a.slot[row + j];
                 if (a.pos_out && a.key_pos) pos[i] = a.key_pos[row + j];
@@ -95,6 +95,7 @@ struct Keys {
         int all = 0;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
+            if (i >= items) break;
             const int j = j0 + 32 * i;
             const uint32_t u = order_of(w[i]);
             const bool mid = j >= o.lo && j < o.hi;
@@ -105,14 +106,14 @@ struct Keys {
         return all;
     }
     // `before`, `equal`: keys before the warp's that stay for sure, and ties.
-    __device__ __forceinline__ void write(const EvictArgs& a, const Border& o, int64_t row, int j0, int before, int equal) const {
+    __device__ __forceinline__ void write(const EvictArgs& a, const Border& o, int64_t row, int j0, int items, int before, int equal) const {
         const int lane = threadIdx.x & 31;
         const unsigned lower = (1u << lane) - 1u;
         before += min(equal, o.want);                    // with the ties that stay
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
             const int j = j0 + 32 * i;
-            if (j - lane >= o.n) break;
+            if (i >= items || j - lane >= o.n) break;
             unsigned keep = stay[i];
             if (tie[i]) {                                // the first of them, as many as are wanted
                 const int room = o.want - min(equal, o.want), m = __popc(tie[i]);
@@ -268,7 +269,9 @@ __global__ void __launch_bounds__(NT, 1) kv_evict_kernel(const EvictArgs a, int 
     int want = K - lo - (n - hi);
     // The thread's keys of round k are j0 + 32 i, in the order of the stream by warps, then items, then lanes.
     // (n + a round stays below 2^31: the table's width is at most 2^30.)
-    const int step = C * CHUNK, rounds = (n + step - 1) / step, mine0 = rank * CHUNK + warp * 32 * ITEMS + lane;
+    // A stream of one round is shared out evenly: `items` keys a thread.
+    const int items = a.border ? ITEMS : max(1, min(ITEMS, (n + C * NT - 1) / (C * NT)));
+    const int step = C * NT * items, rounds = (n + step - 1) / step, mine0 = (rank * NT + warp * 32) * items + lane;
     // a key stays if its integer is below `top`, and of those equal to it the first `want`
     uint32_t top = 0;
     const bool formed = want > 0 && want < hi - lo;      // there is a choice: the integers are formed
@@ -286,7 +289,7 @@ __global__ void __launch_bounds__(NT, 1) kv_evict_kernel(const EvictArgs a, int 
             const int j0 = k * step + mine0;
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i) {
-                const bool mid = (unsigned)(j0 + 32 * i - lo) < (unsigned)(hi - lo);
+                const bool mid = i < items && (unsigned)(j0 + 32 * i - lo) < (unsigned)(hi - lo);
                 u[i] = mid ? order_of(weights[j0 + 32 * i]) : NONE;
             }
         }
@@ -295,7 +298,7 @@ __global__ void __launch_bounds__(NT, 1) kv_evict_kernel(const EvictArgs a, int 
         float w[ITEMS], next[ITEMS];
         int zeros = 0;
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i) next[i] = mine0 + 32 * i < n ? weights[mine0 + 32 * i] : 0.f;
+        for (int i = 0; i < ITEMS; ++i) next[i] = i < items && mine0 + 32 * i < n ? weights[mine0 + 32 * i] : 0.f;
         for (int k = 0; k < rounds; ++k) {
             const int j0 = k * step + mine0, at = k * CHUNK + warp * 32 * ITEMS + lane;
 #pragma unroll
@@ -307,9 +310,10 @@ __global__ void __launch_bounds__(NT, 1) kv_evict_kernel(const EvictArgs a, int 
             // (zeros, which may be many, are counted apart: they would wait for each other)
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i) {
-                const bool mid = (unsigned)(j0 + 32 * i - lo) < (unsigned)(hi - lo);
+                const bool mid = i < items && (unsigned)(j0 + 32 * i - lo) < (unsigned)(hi - lo);
                 const uint32_t u = mid ? order_of(w[i]) : NONE;
                 if (at < cap) held[at + 32 * i] = u;
+                if (i >= items) continue;
                 if (u < NONE && u != ZERO) atomicAdd(&hist[u >> (32 - BITS0)], 1);
                 zeros += u == ZERO;
             }
@@ -377,7 +381,7 @@ __global__ void __launch_bounds__(NT, 1) kv_evict_kernel(const EvictArgs a, int 
         // each warp's counts of its 256 keys, for the second kernel
         const int chunks = (a.slot_stride + CHUNK - 1) / CHUNK;
         for (int k = 0; k < rounds; ++k) {
-            const int g = k * C + rank, w0 = k * step + rank * CHUNK + warp * 32 * ITEMS, w1 = w0 + 32 * ITEMS;
+            const int g = k * C + rank, w0 = k * step + (rank * NT + warp * 32) * items, w1 = w0 + 32 * items;
             int stay = 0, tie = 0;
             uint32_t u[ITEMS];
             if (formed) eight(k, u);
@@ -408,7 +412,7 @@ __global__ void __launch_bounds__(NT, 1) kv_evict_kernel(const EvictArgs a, int 
         for (int k = 0; k < rounds; ++k) {
             const int j0 = k * step + mine0;
             Keys keys;
-            const int all = keys.load(a, o, row, j0);
+            const int all = keys.load(a, o, row, j0, items);
             __syncthreads();                             // the sums of the round before have been read
             if (lane == 0) s.warp_sums[warp] = all;
             __syncthreads();
@@ -428,7 +432,7 @@ __global__ void __launch_bounds__(NT, 1) kv_evict_kernel(const EvictArgs a, int 
                 kept += total & 0xffff;
                 tied += total >> 16;
             }
-            keys.write(a, o, row, j0, before, equal);
+            keys.write(a, o, row, j0, items, before, equal);
         }
     }
     if (rank == 0 && tid == 0) {
@@ -451,7 +455,7 @@ __global__ void __launch_bounds__(TAKE_NT) kv_evict_take(const EvictArgs a) {
     const int chunks = (a.slot_stride + CHUNK - 1) / CHUNK, chunk = first / CHUNK;
     Keys keys;
     const int j0 = first + warp * 32 * ITEMS + lane;
-    keys.load(a, o, row, j0);
+    keys.load(a, o, row, j0, ITEMS);
     int before = 0, equal = 0;
     for (int g = tid; g < chunk; g += TAKE_NT) {
         const int c = a.chunk_counts[(int64_t)b * chunks + g];
@@ -475,7 +479,7 @@ __global__ void __launch_bounds__(TAKE_NT) kv_evict_take(const EvictArgs a) {
     const int c = lane < me ? a.warp_counts[((int64_t)b * chunks + chunk) * 32 + lane] : 0;
     before += __reduce_add_sync(0xffffffffu, c & 0xffff);
     equal += __reduce_add_sync(0xffffffffu, c >> 16);
-    if (j0 - lane < o.n) keys.write(a, o, row, j0, before, equal);
+    if (j0 - lane < o.n) keys.write(a, o, row, j0, ITEMS, before, equal);
 }
 
 // CTAs a stream: up to sixteen while they have a round each and the launch stays within one wave.

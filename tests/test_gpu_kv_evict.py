@@ -105,6 +105,15 @@ def test_long_streams(cuda_lib):
         run(cuda_lib, x, 200000, 16, 1024, inplace=inplace)
 
 
+@pytest.mark.parametrize("kind", ["spread", "ties", "odd"])
+def test_short_streams_in_a_wide_table(cuda_lib, kind):
+    """Streams of a few keys, of a round and of several beside a long one."""
+    lens = [300000, 50, 0, 9000, 131072, 131073, 1]
+    for inplace in (False, True):
+        run(cuda_lib, make(19, lens, 300000, kind), 20000, 4, 64, inplace=inplace)
+        run(cuda_lib, make(19, lens, 300000, kind), 30, 1, 2, inplace=inplace)
+
+
 def test_many_streams(cuda_lib):
     lens = [(37 * i) % 211 for i in range(700)]
     run(cuda_lib, make(11, lens, 211, "ties"), 64, 4, 8, inplace=True)
