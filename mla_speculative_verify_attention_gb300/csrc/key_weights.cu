@@ -198,8 +198,10 @@ __device__ __forceinline__ void give_up(Misc* M, unsigned* status) {
 // 2^8 times that: h in the two high bytes of the halves of .x, l in those of .y.  A half of fp16 below 1 has
 // e4m3's exponent of 2^8 times the number in its lower four exponent bits, denormals alike, so the piece is the
 // half's first bits.
-__device__ __forceinline__ uint2 q_pieces(uint32_t w, float f) {
-    const __half2 x = __floats2half2_rn(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f);
+__device__ __forceinline__ uint2 q_pieces(uint32_t w, __nv_bfloat162 f) {
+    const __nv_bfloat162 q = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), f);
+    const uint32_t qw = *reinterpret_cast<const uint32_t*>(&q);
+    const __half2 x = __floats2half2_rn(__uint_as_float(qw << 16), __uint_as_float(qw & 0xffff0000u));
     const uint32_t hw = *reinterpret_cast<const uint32_t*>(&x) & 0xff80ff80u;
     const __half2 l = __hmul2(__hsub2(x, *reinterpret_cast<const __half2*>(&hw)), __float2half2_rn(16.f));
     const uint32_t lw = *reinterpret_cast<const uint32_t*>(&l);
@@ -212,34 +214,41 @@ __device__ __forceinline__ uint2 q_pieces(uint32_t w, float f) {
 // of two that it was divided by.  Whole warp.  A row with an infinity or a NaN becomes NaN.
 __device__ __forceinline__ float convert_row(uint8_t* row, int q_chunk, int swz) {
     const int lane = threadIdx.x & 31;
-    uint4 v[1][3];
+    uint4 v[3];
 #pragma unroll
     for (int c = 0; c < 3; ++c) {
         const int pc = c * 32 + lane;
-        v[0][c] = pc < 72 ? *reinterpret_cast<const uint4*>(row + (pc >> 3) * q_chunk + (((pc & 7) ^ swz) << 4)) : make_uint4(0, 0, 0, 0);
+        v[c] = pc < 72 ? *reinterpret_cast<const uint4*>(row + (pc >> 3) * q_chunk + (((pc & 7) ^ swz) << 4)) : make_uint4(0, 0, 0, 0);
     }
-    int e[1];
-    row_exponents<1>(v, e);
-    const bool odd = __any_sync(0xffffffffu, not_finite(v[0][0]) || not_finite(v[0][1]) || not_finite(v[0][2]));
-    const uint32_t spoil = odd ? 0x7f7f7f7fu : 0u;
-    const float f = __uint_as_float(e[0] < 126 ? (uint32_t)(126 - e[0]) << 23 : 0x00400000u >> (e[0] - 126));   // 2^(-1 - e)
+    // the largest magnitude, as 16 bits of bf16: what is not finite lies above all numbers
+    uint32_t most = 0;
+#pragma unroll
+    for (int c = 0; c < 3; ++c) {
+        const uint32_t x = __vmaxu2(v[c].x & 0x7fff7fffu, v[c].y & 0x7fff7fffu);
+        most = __vmaxu2(most, __vmaxu2(x, __vmaxu2(v[c].z & 0x7fff7fffu, v[c].w & 0x7fff7fffu)));
+    }
+    most = __reduce_max_sync(0xffffffffu, max(most & 0xffffu, most >> 16));
+    const int e = min(max((int)(most >> 7) - 127, -100), 127);
+    const uint32_t spoil = most >= 0x7f80u ? 0x7f7f7f7fu : 0u;
+    const uint32_t fb = e < 126 ? (uint32_t)(126 - e) << 7 : 0x40u >> (e - 126), fw = fb | fb << 16;   // 2^(-1 - e), twice
+    const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162*>(&fw);
     __syncwarp();
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
         const int pc = c * 32 + lane;
-        const uint4 o = v[0][c];
+        const uint4 o = v[c];
         const uint2 x = q_pieces(o.x, f), y = q_pieces(o.y, f), z = q_pieces(o.z, f), w = q_pieces(o.w, f);
         uint8_t* at = row + (pc >> 4) * q_chunk + ((((pc & 15) >> 1) ^ swz) << 4) + (pc & 1) * 8;
         *reinterpret_cast<uint2*>(at) = make_uint2(__byte_perm(x.x, y.x, 0x7531) | spoil, __byte_perm(z.x, w.x, 0x7531) | spoil);
         *reinterpret_cast<uint2*>(at + 4 * q_chunk) = make_uint2(__byte_perm(x.y, y.y, 0x7531) | spoil, __byte_perm(z.y, w.y, 0x7531) | spoil);
     }
     if (lane < 8) {
-        const float m = __uint_as_float((uint32_t)(7 - e[0] + 127) << 23);
-        const uint4 o = v[0][2];
+        const float m = __uint_as_float((uint32_t)(7 - e + 127) << 23);
+        const uint4 o = v[2];
         *reinterpret_cast<uint4*>(row + 8 * q_chunk + ((lane ^ swz) << 4)) =
             make_uint4(q_to_bf16(o.x, m), q_to_bf16(o.y, m), q_to_bf16(o.z, m), q_to_bf16(o.w, m));
     }
-    return __uint_as_float((uint32_t)(e[0] - 7 + 127) << 23);
+    return __uint_as_float((uint32_t)(e - 7 + 127) << 23);
 }
 
 // KW: keys of a tile per score warp, 16, or 8 with up to 64 rows.

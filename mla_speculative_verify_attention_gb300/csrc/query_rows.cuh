@@ -40,15 +40,6 @@ __device__ __forceinline__ void load_q_rows(uint4 (&v)[N][3], const __nv_bfloat1
     }
 }
 
-// Whether one of eight bf16 values is an infinity or a NaN.
-__device__ __forceinline__ bool not_finite(const uint4& v) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) bad |= (w[i] & 0x7f800000u) == 0x7f800000u || (w[i] & 0x7f80u) == 0x7f80u;
-    return bad;
-}
-
 // The exponent of each row's largest element (the warp holds the rows as load_q_rows left them), within
 // what keeps 2^(14 - e) and 2^(e - 14) finite.
 template <int N>
