@@ -113,8 +113,9 @@ struct WeightArgs {
     unsigned* status;
 };
 
-// Key ranges of B <= 64 streams of unequal length: chunks of whole tiles, the smallest with which all
-// streams together need no more than S ranges.  Every warp finds the same; range x's stream and keys.
+// Key ranges of B <= 64 streams of unequal length: chunks of whole tiles with which all streams together need no
+// more than S ranges, from what it takes if the last chunks are half full on.  Every warp finds the same;
+// range x's stream and keys.
 __device__ __forceinline__ void balanced_range(const WeightArgs& a, int S, int x, int* b, int* begin, int* end, int* index,
                                                int* count) {
     const int lane = threadIdx.x & 31;
@@ -131,7 +132,8 @@ __device__ __forceinline__ void balanced_range(const WeightArgs& a, int S, int x
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     // a stream without keys takes a range too (its length is reported there)
-    unsigned c = total < (1ll << 30) ? ((unsigned)total + S - 1u) / S : (unsigned)((total + S - 1) / S);
+    const unsigned parts = S - a.B / 2;
+    unsigned c = total < (1ll << 30) ? ((unsigned)total + parts - 1u) / parts : (unsigned)((total + parts - 1) / parts);
     c = max(c + NK - 1u, (unsigned)NK) / NK * NK;
     int ns[2], all;
     for (;; c += max(1u, c / (64u * NK)) * NK) {         // (steps of a sixty-fourth: a few dozen at most)
@@ -326,13 +328,16 @@ __global__ void __launch_bounds__(NT, 1) key_weights_kernel(const WeightArgs a) 
         uint8_t* const q_tmp = smem + q_stage * S::STAGE_BYTES;
         const int q_chunk = (nrows + 7) / 8 * 1024;
         const __nv_bfloat16* q0 = a.q + ((int64_t)b * rows + row0) * D_QK;
-        for (int f = tid; f < nrows * 72; f += 32 * GATHER0) {
-            const int rr = f / 72, pc = f % 72;
-            cp_async16(smem_u32(q_tmp) + (pc >> 3) * q_chunk + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4), q0 + (int64_t)rr * D_QK + pc * 8);
+        for (int rr = warp; rr < nrows; rr += GATHER0) {
+            const uint32_t dst = smem_u32(q_tmp) + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4) + (lane >> 3) * q_chunk;
+            const __nv_bfloat16* src = q0 + (int64_t)rr * D_QK + lane * 8;
+            cp_async16(dst, src);
+            cp_async16(dst + 4 * q_chunk, src + 256);
+            if (lane < 8) cp_async16(dst + 8 * q_chunk, src + 512);
         }
         cp_async_wait_all();
         if (FP8) {
-            bar_sync(3, 32 * GATHER0);
+            __syncwarp();                                // (a warp converts the rows that it brought)
 #pragma unroll 1
             for (int rr = warp; rr < nrows; rr += GATHER0) {
                 const float e = convert_row(q_tmp + rr * 128, q_chunk, rr & 7);
