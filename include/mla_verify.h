@@ -405,6 +405,7 @@ size_t mla_key_weights_workspace_bytes(int B, int q_len, int H, int slot_stride)
  * An output may be its own input (in place); other overlaps are not allowed.  Entries past those named stay
  * as they were.  A length outside [0, slot_stride] sets MLA_DEV_BAD_LEN: the stream is left alone, with
  * lens_out[b] = n and n_freed[b] = 0.  No cache row moves: slots are only handed back.
+ *   workspace  device scratch of ws_bytes >= mla_kv_evict_workspace_bytes(); NULL where that is 0
  * Limits: 0 <= B <= 65535, 1 <= slot_stride <= MLA_MAX_FP8_KEYS, sink >= 0, recent >= 0.
  */
 int mla_kv_evict(const int32_t* slot_table, const int32_t* seq_lens, const float* weights, const int32_t* key_pos,
@@ -414,11 +415,11 @@ int mla_kv_evict(const int32_t* slot_table, const int32_t* seq_lens, const float
                  mla_stream_t stream);
 
 /*
- * Bytes of workspace with which mla_kv_evict() takes the keys of long streams with all SMs (0: it needs none).
- * Without it, and where a table is compacted in place, a cluster of SMs takes a stream alone, to the same
- * result.  Pure host function; num_sms of the device.
+ * Bytes of workspace that mla_kv_evict() needs: 0 for short streams (up to 8192 keys, up to 131072 where there are
+ * few of them), else 8 bytes a key and 33 KB a stream, and 16 bytes a key more where `in_place` is set: some
+ * table is its own output.  16-byte aligned.  Pure host function; num_sms of the device.
  */
-size_t mla_kv_evict_workspace_bytes(int B, int slot_stride, int num_sms);
+size_t mla_kv_evict_workspace_bytes(int B, int slot_stride, int in_place, int num_sms);
 
 /*
  * Acceptance of drafted tokens from given random numbers, the step after a verify pass:

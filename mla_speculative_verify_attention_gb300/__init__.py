@@ -101,7 +101,7 @@ def load():
     L.mla_key_weights.restype = I
     L.mla_key_weights_workspace_bytes.argtypes = [I, I, I, I]
     L.mla_key_weights_workspace_bytes.restype = SZ
-    L.mla_kv_evict_workspace_bytes.argtypes = [I, I, I]
+    L.mla_kv_evict_workspace_bytes.argtypes = [I, I, I, I]
     L.mla_kv_evict_workspace_bytes.restype = SZ
     L.mla_kv_evict.argtypes = [P, P, P, P, P, I, I, P, I, I, I, P, P, P, P, P, P, P, P, SZ, P]
     L.mla_kv_evict.restype = I
@@ -767,8 +767,8 @@ def kv_evict(slot_table: torch.Tensor, seq_lens: torch.Tensor, weights: torch.Te
     in all (an int, or int32 [B] on the device), and moves their entries of slot_table, weights, key_pos and
     key_doc [B, stride] together.  By default in place; an ``_out`` tensor takes the result instead.
     Without key_pos a key's position is its index (pos_out, where given, gets it).  The evicted slots are in
-    freed [B, stride], n_freed [B] of them.  ``workspace`` is a byte (uint8) CUDA tensor for long streams whose
-    tables are not compacted in place (mla_kv_evict_workspace_bytes), allocated here when omitted."""
+    freed [B, stride], n_freed [B] of them.  ``workspace`` is a byte (uint8) CUDA tensor for long streams
+    (mla_kv_evict_workspace_bytes), allocated here when omitted."""
     _want_dims("slot_table", slot_table, torch.int32, 2)
     shape = slot_table.shape
     B, stride = shape
@@ -813,8 +813,11 @@ def kv_evict(slot_table: torch.Tensor, seq_lens: torch.Tensor, weights: torch.Te
             freed = _empty_like(slot_table, torch.int32, stream)
         if n_freed is None:
             n_freed = _empty_like(seq_lens, torch.int32, stream)
-        if workspace is None and stride > 8192 and table_out is not slot_table:
-            need = int(load().mla_kv_evict_workspace_bytes(B, stride, num_sms(dev)))
+        if workspace is None and stride > 8192:
+            in_place = 1 if (table_out.data_ptr() == slot_table.data_ptr() or weights_out.data_ptr() == weights.data_ptr() or
+                             (key_pos is not None and pos_out.data_ptr() == key_pos.data_ptr()) or
+                             (key_doc is not None and doc_out.data_ptr() == key_doc.data_ptr())) else 0
+            need = int(load().mla_kv_evict_workspace_bytes(B, stride, in_place, num_sms(dev)))
             if need:
                 workspace = _empty(weights, (need,), torch.uint8, stream)
         _check("mla_kv_evict", _call("mla_kv_evict")(

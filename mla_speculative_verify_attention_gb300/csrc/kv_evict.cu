@@ -1,15 +1,18 @@
 // Eviction from a cache by accumulated weight (mla_kv_evict): K of a stream's n keys stay, their table
 // entries move together.
 //
-// A cluster of up to sixteen CTAs a stream.  Weights are compared as 32-bit integers in the opposite order of the
-// numbers; the K-th smallest is found from histograms in shared memory (integer counts: no order of additions)
-// over its first 13 bits, the next 11 and the last 8, as many of them as it takes.  The first pass keeps the
-// integers in shared memory, up to 40960 a CTA, for the others; the second lists the few that the third has to
-// look at.  Then the keys are taken in order, each with its place from ballots and the counts of the keys
-// before it, 8192 a CTA and round, the CTAs one behind the other.  A round is read before anything of it is
-// written, by all CTAs, and its places are not behind its own, so tables may be compacted in place.
-// Where several rounds are needed and no table is compacted in place, the cluster only leaves the border and
-// each warp's counts in the workspace, and a second kernel over all SMs takes the keys.
+// Weights are compared as 32-bit integers in the opposite order of the numbers; the K-th smallest is found from
+// histograms in shared memory (integer counts: no order of additions) over its first 13 bits, the next 11 and
+// the last 8, as many of them as it takes.  Then the keys are taken, each with its place from ballots and the
+// counts of the keys before it.
+//
+// Streams of up to 8192 keys a CTA: a cluster of up to sixteen CTAs a stream, in one kernel; a thread keeps its
+// eight integers in registers.  Everything is read before anything is written, so tables may be compacted
+// in place.
+// Longer ones: all SMs share the streams out in chunks of 8192 keys.  One kernel adds the histograms up in the
+// workspace; the next counts what stays for sure and lists the keys of the border's bin, of which each
+// stream's last CTA to finish finds the border and adds those that stay to the counts; the third takes the
+// keys.  A table that is compacted in place passes through the workspace.
 #include "../../include/mla_verify.h"
 #include "internal.cuh"
 
@@ -30,8 +33,6 @@ constexpr int MAX_CLUSTER = 16;
 constexpr int BITS0 = 13, BITS1 = 11, BITS2 = 8;
 constexpr int BINS = 1 << BITS0, ALL_BINS = BINS + (1 << BITS1) + (1 << BITS2);   // a pass its own
 constexpr int GROUPS = 64;                           // of a pass's bins
-constexpr int MAX_HELD = 40960;                      // integers that a CTA keeps in shared memory
-constexpr int MAX_LIST = 4096;                       // and those of them that it lists
 
 struct EvictArgs {
     const int32_t* slot;
@@ -50,15 +51,19 @@ struct EvictArgs {
     int32_t* freed;
     int32_t* n_freed;
     unsigned* status;
-    struct Border* border;                           // workspace, or null: one kernel does it all
-    int32_t* warp_counts;                            // [B][chunks * 32]: keys that stay | ties << 16, a warp's 256 keys
-    int32_t* chunk_counts;                           // [B][chunks]: the same of a chunk of 8192
+    // workspace of the wide form
+    int32_t* hist;                                   // [B][GROUPS + BINS], zeroed: sums of the groups of bins, the bins
+    int32_t* done;                                   // [B][2], zeroed: CTAs that have listed, keys listed
+    struct Border* border;                           // [B]
+    int32_t* chunk_counts;                           // [B][chunks]: keys that stay | ties << 16
+    int32_t* warp_counts;                            // [B][chunks * 32]: the same of a warp's 256 keys
+    uint2* list;                                     // [B][slot_stride]: integer and index of a key
 };
 
-// What the first kernel leaves of a stream: a key j of lo .. hi - 1 stays if its integer is below `top`, and of
+// How a stream's keys are chosen: a key j of lo .. hi - 1 stays if its integer is below `top`, and of
 // those equal to it the first `want`; all others of the n keys stay.
 struct Border {
-    int n, lo, hi, want;
+    int n, K, lo, hi, want;
     uint32_t top;
 };
 
@@ -71,65 +76,102 @@ __device__ __forceinline__ uint32_t order_of(float w) {
 constexpr uint32_t ZERO = 0x7fffffffu;               // order_of(0)
 constexpr uint32_t NONE = 0xffffffffu;               // no number's: the last is that of -infinity, 0xff800000
 
-// A thread's keys j0 + 32 i of the stream, and which of the warp's keys stay or tie.
+// What a stream's lengths say.
+struct Plan {
+    int n, K, lo, hi, want;                              // of the keys lo .. hi - 1 the `want` heaviest stay
+    bool bad, formed;                                    // a bad length; there is a choice
+};
+__device__ __forceinline__ Plan plan_of(const EvictArgs& a, int b) {
+    Plan p;
+    p.n = a.seq_lens[b];
+    p.bad = p.n < 0 || p.n > a.slot_stride;
+    const int n = p.bad ? 0 : p.n, budget = max(0, a.budgets ? a.budgets[b] : a.budget);
+    p.K = (int)min((long long)n, max((long long)budget, (long long)a.sink + a.recent));
+    p.lo = min(a.sink, n);
+    p.hi = max(p.lo, (int)max((long long)n - a.recent, 0ll));
+    p.want = p.K - p.lo - (n - p.hi);
+    p.formed = p.want > 0 && p.want < p.hi - p.lo;
+    return p;
+}
+// Without a choice: all of them or none.
+__device__ __forceinline__ Border without_choice(const Plan& p) {
+    return p.want <= 0 ? Border{p.bad ? 0 : p.n, p.K, p.lo, p.hi, 0, 0u} : Border{p.n, p.K, p.lo, p.hi, INT_MAX, ~0u};
+}
+__device__ __forceinline__ void write_lens(const EvictArgs& a, int b, const Plan& p) {
+    if (p.bad) atomicOr(a.status, DEV_BAD_LEN);
+    a.lens_out[b] = p.bad ? p.n : p.K;
+    if (a.n_freed) a.n_freed[b] = p.bad ? 0 : p.n - p.K;
+}
+
+// A thread's keys j0 + 32 i of the stream, and which of them stay (bit i) or tie (bit 8 + i).
 struct Keys {
     float w[ITEMS];
     int slot[ITEMS], pos[ITEMS], doc[ITEMS];
-    unsigned stay[ITEMS], tie[ITEMS];
+    unsigned mine;
 
-    // Returns the warp's counts: stay | ties << 16.
-    __device__ __forceinline__ int load(const EvictArgs& a, const Border& o, int64_t row, int j0, int items) {
+    __device__ __forceinline__ void fetch_weights(const EvictArgs& a, int n, int64_t row, int j0, int items) {
+        const float* const at = a.weights + row + j0;    // (items lie at fixed offsets from here)
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            const int j = j0 + 32 * i;
-            w[i] = 0.f;
-            slot[i] = doc[i] = 0;
-            pos[i] = j;
-            if (i < items && j < o.n) {
-                w[i] = a.weights[row + j];
-                slot[i] = a.slot[row + j];
-                if (a.pos_out && a.key_pos) pos[i] = a.key_pos[row + j];
-                if (a.doc_out) doc[i] = a.key_doc[row + j];
-            }
+        for (int i = 0; i < ITEMS; ++i) w[i] = i < items && j0 + 32 * i < n ? at[32 * i] : 0.f;
+    }
+    __device__ __forceinline__ void fetch(const EvictArgs& a, int n, int64_t row, int j0, int items) {
+        const int32_t* const slots = a.slot + row + j0;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) slot[i] = i < items && j0 + 32 * i < n ? slots[32 * i] : 0;
+        if (a.pos_out) {
+            const int32_t* const at = a.key_pos + row + j0;
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i) pos[i] = a.key_pos && i < items && j0 + 32 * i < n ? at[32 * i] : j0 + 32 * i;
         }
-        int all = 0;
+        if (a.doc_out) {
+            const int32_t* const at = a.key_doc + row + j0;
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i) doc[i] = i < items && j0 + 32 * i < n ? at[32 * i] : 0;
+        }
+    }
+    // Returns the warp's counts: stay | ties << 16.
+    __device__ __forceinline__ int choose(const Border& o, int j0, int items) {
+        mine = 0;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
-            if (i >= items) break;
             const int j = j0 + 32 * i;
             const uint32_t u = order_of(w[i]);
-            const bool mid = j >= o.lo && j < o.hi;
-            stay[i] = __ballot_sync(0xffffffffu, j < o.n && (!mid || u < o.top));
-            tie[i] = __ballot_sync(0xffffffffu, mid && u == o.top);
-            all += __popc(stay[i]) | __popc(tie[i]) << 16;
+            const bool in = i < items && j < o.n, mid = j >= o.lo && j < o.hi;
+            mine |= (unsigned)(in && (!mid || u < o.top)) << i | (unsigned)(in && mid && u == o.top) << (8 + i);
         }
-        return all;
+        return __reduce_add_sync(0xffffffffu, __popc(mine & 0xffu) | __popc(mine >> 8) << 16);
     }
     // `before`, `equal`: keys before the warp's that stay for sure, and ties.
     __device__ __forceinline__ void write(const EvictArgs& a, const Border& o, int64_t row, int j0, int items, int before, int equal) const {
         const int lane = threadIdx.x & 31;
         const unsigned lower = (1u << lane) - 1u;
         before += min(equal, o.want);                    // with the ties that stay
+        const bool ties = __any_sync(0xffffffffu, mine >> 8);
+        int32_t* const table = a.table_out + row;
+        float* const weights = a.weights_out + row;
+        int32_t *const positions = a.pos_out + row, *const docs = a.doc_out + row;   // (where there are any)
+        int32_t* const freed = a.freed + row + j0;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
             const int j = j0 + 32 * i;
             if (i >= items || j - lane >= o.n) break;
-            unsigned keep = stay[i];
-            if (tie[i]) {                                // the first of them, as many as are wanted
-                const int room = o.want - min(equal, o.want), m = __popc(tie[i]);
+            unsigned keep = __ballot_sync(0xffffffffu, (mine >> i) & 1u);
+            if (ties) {                                  // the first of them, as many as are wanted
+                const unsigned tie = __ballot_sync(0xffffffffu, (mine >> (8 + i)) & 1u);
+                const int room = o.want - min(equal, o.want), m = __popc(tie);
                 equal += m;
-                if (room >= m) keep |= tie[i];
-                else if (room > 0) keep |= __ballot_sync(0xffffffffu, ((tie[i] >> lane) & 1u) && __popc(tie[i] & lower) < room);
+                if (room >= m) keep |= tie;
+                else if (room > 0) keep |= __ballot_sync(0xffffffffu, ((tie >> lane) & 1u) && __popc(tie & lower) < room);
             }
             const int to = before + __popc(keep & lower);
             before += __popc(keep);
             if ((keep >> lane) & 1u) {
-                a.table_out[row + to] = slot[i];
-                a.weights_out[row + to] = w[i];
-                if (a.pos_out) a.pos_out[row + to] = pos[i];
-                if (a.doc_out) a.doc_out[row + to] = doc[i];
+                table[to] = slot[i];
+                weights[to] = w[i];
+                if (a.pos_out) positions[to] = pos[i];
+                if (a.doc_out) docs[to] = doc[i];
             } else if (j < o.n && a.freed) {
-                a.freed[row + j - to] = slot[i];
+                freed[32 * i - to] = slot[i];
             }
         }
     }
@@ -139,8 +181,8 @@ struct Shared {
     int warp_sums[32];
     int groups[3][GROUPS];                           // a pass's keys in every sixty-fourth of the bins
     int found[3];                                    // bin, keys wanted of it, keys in it
-    int listed;                                      // keys of the bin, as many as MAX_LIST in the list
-    int totals[2][MAX_CLUSTER];                      // of every CTA's chunk: keys that stay | ties << 16
+    int listed;                                      // the wide form: keys of the bin
+    int totals[MAX_CLUSTER];                         // of every CTA: keys that stay | ties << 16
 };
 
 // A warp's search for the `want`-th of N <= 64 numbers in order, N / 32 (or 1) consecutive ones a lane: its
@@ -236,232 +278,291 @@ __device__ __forceinline__ void find_bin(cg::cluster_group& cluster, int C, int 
     __syncthreads();
 }
 
-__global__ void __launch_bounds__(NT, 1) kv_evict_kernel(const EvictArgs a, int C, int cap) {
-    extern __shared__ __align__(16) uint8_t smem[];
+// Takes the bin that was found over the `shift` last bits into the border; true where it is known then.
+__device__ __forceinline__ bool narrow(const Shared& s, int shift, uint32_t* top, int* want) {
+    *top |= (uint32_t)s.found[0] << shift;
+    *want = s.found[1];
+    if (*want < s.found[2]) return shift == 0;
+    *top |= (1u << shift) - 1u;                          // the bin stays as a whole
+    *want = INT_MAX;
+    return true;
+}
+
+__global__ void __launch_bounds__(NT, 1) kv_evict_kernel(const EvictArgs a, int C) {
+    __shared__ __align__(16) int hist[ALL_BINS];
     __shared__ Shared s;
-    int* const hist = reinterpret_cast<int*>(smem);
-    uint32_t* const list = reinterpret_cast<uint32_t*>(smem) + ALL_BINS;
-    uint32_t* const held = list + MAX_LIST;
     cg::cluster_group cluster = cg::this_cluster();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = C > 1 ? (int)cluster.block_rank() : 0, b = blockIdx.x / C;
-    const int n = a.seq_lens[b];
-    const int budget = max(0, a.budgets ? a.budgets[b] : a.budget);
+    const Plan p = plan_of(a, b);
+    // The thread's keys are j0 + 32 i, `items` of them, in the order of the stream by warps, then items, then lanes.
+    const int64_t row = (int64_t)b * a.slot_stride;
+    const int items = p.bad ? 1 : max(1, min(ITEMS, (p.n + C * NT - 1) / (C * NT)));
+    const int j0 = (rank * NT + warp * 32) * items + lane, n = p.bad ? 0 : p.n;
+    Keys keys;
+    keys.fetch_weights(a, n, row, j0, items);
     for (int i = tid; i < ALL_BINS / 4; i += NT) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
-    if (tid == 0) s.listed = 0;
     if (C > 1) cluster.sync();                           // every CTA runs, and has read the length
     else __syncthreads();
-    if (n < 0 || n > a.slot_stride) {
-        if (rank == 0 && tid == 0) {
-            atomicOr(a.status, DEV_BAD_LEN);
-            a.lens_out[b] = n;
-            if (a.n_freed) a.n_freed[b] = 0;
-            if (a.border) a.border[b] = Border{};
-        }
+    if (p.bad) {
+        if (rank == 0 && tid == 0) write_lens(a, b, p);
         return;
     }
-    const int64_t row = (int64_t)b * a.slot_stride;
-    const float* const weights = a.weights + row;
-    const int K = (int)min((long long)n, max((long long)budget, (long long)a.sink + a.recent));
-    // of the keys lo .. hi - 1 the `want` heaviest stay
-    const int lo = min(a.sink, n), hi = max(lo, (int)max((long long)n - a.recent, 0ll));
-    int want = K - lo - (n - hi);
-    // The thread's keys of round k are j0 + 32 i, in the order of the stream by warps, then items, then lanes.
-    // (n + a round stays below 2^31: the table's width is at most 2^30.)
-    // A stream of one round is shared out evenly: `items` keys a thread.
-    const int items = a.border ? ITEMS : max(1, min(ITEMS, (n + C * NT - 1) / (C * NT)));
-    const int step = C * NT * items, rounds = (n + step - 1) / step, mine0 = (rank * NT + warp * 32) * items + lane;
-    // a key stays if its integer is below `top`, and of those equal to it the first `want`
-    uint32_t top = 0;
-    const bool formed = want > 0 && want < hi - lo;      // there is a choice: the integers are formed
-    // Eight integers of the warp's 256 keys of round k (any eight: lane l those from 8 l on where they are held);
-    // NONE for a key that is not among the lo .. hi - 1.
-    auto eight = [&](int k, uint32_t (&u)[ITEMS]) {
-        const int at = k * CHUNK + warp * 32 * ITEMS;
-        if (at < cap) {
+    Border o = without_choice(p);
+    if (p.formed) {
+        auto integer = [&](int i) -> uint32_t {          // NONE for a key that is not among the lo .. hi - 1
+            return i < items && (unsigned)(j0 + 32 * i - p.lo) < (unsigned)(p.hi - p.lo) ? order_of(keys.w[i]) : NONE;
+        };
+        int zeros = 0;                                   // (counted apart: they would wait for each other)
 #pragma unroll
-            for (int q = 0; q < ITEMS; q += 4) {
-                const uint4 v = *reinterpret_cast<const uint4*>(held + at + lane * ITEMS + q);
-                u[q] = v.x; u[q + 1] = v.y; u[q + 2] = v.z; u[q + 3] = v.w;
-            }
-        } else {
-            const int j0 = k * step + mine0;
-#pragma unroll
-            for (int i = 0; i < ITEMS; ++i) {
-                const bool mid = i < items && (unsigned)(j0 + 32 * i - lo) < (unsigned)(hi - lo);
-                u[i] = mid ? order_of(weights[j0 + 32 * i]) : NONE;
-            }
-        }
-    };
-    if (formed) {
-        float w[ITEMS], next[ITEMS];
-        int zeros = 0;
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) next[i] = i < items && mine0 + 32 * i < n ? weights[mine0 + 32 * i] : 0.f;
-        for (int k = 0; k < rounds; ++k) {
-            const int j0 = k * step + mine0, at = k * CHUNK + warp * 32 * ITEMS + lane;
-#pragma unroll
-            for (int i = 0; i < ITEMS; ++i) {
-                w[i] = next[i];
-                const int j = j0 + step + 32 * i;
-                next[i] = j < n ? weights[j] : 0.f;
-            }
-            // (zeros, which may be many, are counted apart: they would wait for each other)
-#pragma unroll
-            for (int i = 0; i < ITEMS; ++i) {
-                const bool mid = i < items && (unsigned)(j0 + 32 * i - lo) < (unsigned)(hi - lo);
-                const uint32_t u = mid ? order_of(w[i]) : NONE;
-                if (at < cap) held[at + 32 * i] = u;
-                if (i >= items) continue;
-                if (u < NONE && u != ZERO) atomicAdd(&hist[u >> (32 - BITS0)], 1);
-                zeros += u == ZERO;
-            }
+        for (int i = 0; i < ITEMS; ++i) {
+            const uint32_t u = integer(i);
+            if (u < NONE && u != ZERO) atomicAdd(&hist[u >> (32 - BITS0)], 1);
+            zeros += u == ZERO;
         }
         zeros = __reduce_add_sync(0xffffffffu, zeros);
         if (lane == 0 && zeros) atomicAdd(&hist[ZERO >> (32 - BITS0)], zeros);
-        find_bin<BINS>(cluster, C, 0, hist, s, want);
+        find_bin<BINS>(cluster, C, 0, hist, s, p.want);
+        o.top = 0;
         int shift = 32 - BITS0;
         int* bins = hist + BINS;
-        bool listed = false;
 #pragma unroll 1
-        for (;;) {
-            top |= (uint32_t)s.found[0] << shift;
-            want = s.found[1];
-            if (want == s.found[2]) {                    // the bin stays as a whole
-                top |= (1u << shift) - 1u;
-                want = INT_MAX;
-                break;
-            }
-            if (shift == 0) break;
+        while (!narrow(s, shift, &o.top, &o.want)) {
             const int bits = shift == 32 - BITS0 ? BITS1 : BITS2, above = shift;
             shift -= bits;
-            auto put = [&](uint32_t u) { atomicAdd(&bins[(u >> shift) & ((1u << bits) - 1u)], 1); };
-            if (listed) {
-                const int m = s.listed;
-                for (int i = tid; i < m; i += NT)
-                    if (list[i] - top < 1u << above) put(list[i]);
-            } else {
-                for (int k = 0; k < rounds; ++k) {
-                    uint32_t u[ITEMS];
-                    eight(k, u);
-                    bool any = false;
-#pragma unroll
-                    for (int i = 0; i < ITEMS; ++i) any |= u[i] - top < 1u << above;
-                    if (!__any_sync(0xffffffffu, any)) continue;
-#pragma unroll
-                    for (int i = 0; i < ITEMS; ++i) {
-                        const bool in = u[i] - top < 1u << above;
-                        const unsigned m = __ballot_sync(0xffffffffu, in);
-                        if (m == 0) continue;
-                        int base = 0;
-                        if (lane == 0) base = s.listed <= MAX_LIST ? atomicAdd(&s.listed, __popc(m)) : MAX_LIST;
-                        base = __shfl_sync(0xffffffffu, base, 0) + __popc(m & ((1u << lane) - 1u));
-                        if (in) {
-                            if (base < MAX_LIST) list[base] = u[i];
-                            put(u[i]);
-                        }
-                    }
-                }
-            }
-            __syncthreads();                             // (found has been read, the list is there)
-            listed = s.listed <= MAX_LIST;
-            if (bits == BITS1) find_bin<1 << BITS1>(cluster, C, 1, bins, s, want);
-            else find_bin<1 << BITS2>(cluster, C, 2, bins, s, want);
-            bins += 1 << BITS1;
-        }
-    } else if (want <= 0) {
-        want = 0;                                        // none, not even of the first
-    } else {
-        top = ~0u;                                       // all
-        want = INT_MAX;
-    }
-    const Border o = {n, lo, hi, want, top};
-    if (a.border) {
-        // each warp's counts of its 256 keys, for the second kernel
-        const int chunks = (a.slot_stride + CHUNK - 1) / CHUNK;
-        for (int k = 0; k < rounds; ++k) {
-            const int g = k * C + rank, w0 = k * step + (rank * NT + warp * 32) * items, w1 = w0 + 32 * items;
-            int stay = 0, tie = 0;
-            uint32_t u[ITEMS];
-            if (formed) eight(k, u);
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i) {
-                stay += formed && u[i] < top;
-                tie += formed && u[i] == top;
+                const uint32_t u = integer(i);
+                if (u - o.top < 1u << above) atomicAdd(&bins[(u >> shift) & ((1u << bits) - 1u)], 1);
             }
-            int all = __reduce_add_sync(0xffffffffu, stay | tie << 16);
-            // and the warp's keys outside of lo .. hi - 1; without a choice all of those inside or none
-            all += max(0, min(w1, lo) - min(w0, lo)) + max(0, min(w1, n) - max(min(w0, n), hi));
-            if (!formed && want) all += max(0, min(w1, hi) - max(w0, lo));
-            if (g >= chunks) break;
-            if (lane == 0) {
-                s.warp_sums[warp] = all;
-                a.warp_counts[((int64_t)b * chunks + g) * 32 + warp] = all;
-            }
-            __syncthreads();
-            if (warp == 0) {
-                const int sum = __reduce_add_sync(0xffffffffu, s.warp_sums[lane]);
-                if (lane == 0) a.chunk_counts[(int64_t)b * chunks + g] = sum;
-            }
-            __syncthreads();
-        }
-        if (rank == 0 && tid == 0) a.border[b] = o;
-    } else {
-        int kept = 0, tied = 0;                          // before this round: keys that stay, ties
-        for (int k = 0; k < rounds; ++k) {
-            const int j0 = k * step + mine0;
-            Keys keys;
-            const int all = keys.load(a, o, row, j0, items);
-            __syncthreads();                             // the sums of the round before have been read
-            if (lane == 0) s.warp_sums[warp] = all;
-            __syncthreads();
-            const int t = s.warp_sums[lane], total = __reduce_add_sync(0xffffffffu, t);
-            const int before_warp = __reduce_add_sync(0xffffffffu, lane < warp ? t : 0);
-            int before = kept + (before_warp & 0xffff), equal = tied + (before_warp >> 16);
-            if (C > 1) {
-                if (tid < C) *cluster.map_shared_rank(&s.totals[k & 1][rank], tid) = total;
-                cluster.sync();
-                // (sixteen chunks' counts pass 16 bits: added apart)
-                const int c = lane < C ? s.totals[k & 1][lane] : 0, c_b = lane < rank ? c : 0;
-                kept += __reduce_add_sync(0xffffffffu, c & 0xffff);
-                tied += __reduce_add_sync(0xffffffffu, c >> 16);
-                before += __reduce_add_sync(0xffffffffu, c_b & 0xffff);
-                equal += __reduce_add_sync(0xffffffffu, c_b >> 16);
-            } else {
-                kept += total & 0xffff;
-                tied += total >> 16;
-            }
-            keys.write(a, o, row, j0, items, before, equal);
+            if (bits == BITS1) find_bin<1 << BITS1>(cluster, C, 1, bins, s, o.want);
+            else find_bin<1 << BITS2>(cluster, C, 2, bins, s, o.want);
+            bins += 1 << BITS1;
         }
     }
-    if (rank == 0 && tid == 0) {
-        a.lens_out[b] = K;
-        if (a.n_freed) a.n_freed[b] = n - K;
+    keys.fetch(a, n, row, j0, items);
+    const int all = keys.choose(o, j0, items);
+    if (lane == 0) s.warp_sums[warp] = all;
+    __syncthreads();
+    const int t = s.warp_sums[lane], total = __reduce_add_sync(0xffffffffu, t);
+    const int before_warp = __reduce_add_sync(0xffffffffu, lane < warp ? t : 0);
+    int before = before_warp & 0xffff, equal = before_warp >> 16;
+    if (C > 1) {
+        if (tid < C) *cluster.map_shared_rank(&s.totals[rank], tid) = total;
+        cluster.sync();                                  // (and everything has been read)
+        const int c = lane < rank ? s.totals[lane] : 0;  // (sixteen CTAs' counts pass 16 bits: added apart)
+        before += __reduce_add_sync(0xffffffffu, c & 0xffff);
+        equal += __reduce_add_sync(0xffffffffu, c >> 16);
     }
-    if (C > 1) cluster.sync();                           // nobody looks at this CTA's shared memory any more
+    keys.write(a, o, row, j0, items, before, equal);
+    if (rank == 0 && tid == 0) write_lens(a, b, p);
 }
 
-// The second kernel: a CTA 2048 keys, a warp 256.
+// ---- the wide form.  Keys mine + 32 i of chunk blockIdx.x, as in the one above; integers of keys that are not
+// among the lo .. hi - 1 are NONE.
+__device__ __forceinline__ void chunk_keys(const EvictArgs& a, int b, const Plan& p, uint32_t (&u)[ITEMS]) {
+    const int j0 = blockIdx.x * CHUNK + (threadIdx.x >> 5) * 32 * ITEMS + (threadIdx.x & 31);
+    const float* const at = a.weights + (int64_t)b * a.slot_stride + j0;
+    float w[ITEMS];
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) w[i] = j0 + 32 * i < p.n ? at[32 * i] : 0.f;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) u[i] = (unsigned)(j0 + 32 * i - p.lo) < (unsigned)(p.hi - p.lo) ? order_of(w[i]) : NONE;
+}
+
+__global__ void __launch_bounds__(NT) kv_evict_count(const EvictArgs a) {
+    __shared__ __align__(16) int hist[BINS];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int tid = threadIdx.x, b = blockIdx.y;
+    const Plan p = plan_of(a, b);
+    if (!p.formed || blockIdx.x * CHUNK >= p.n) return;
+    for (int i = tid; i < BINS / 4; i += NT) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
+    uint32_t u[ITEMS];
+    chunk_keys(a, b, p, u);
+    __syncthreads();
+    int zeros = 0;                                       // (counted apart: they would wait for each other)
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        if (u[i] < NONE && u[i] != ZERO) atomicAdd(&hist[u[i] >> (32 - BITS0)], 1);
+        zeros += u[i] == ZERO;
+    }
+    zeros = __reduce_add_sync(0xffffffffu, zeros);
+    if ((tid & 31) == 0 && zeros) atomicAdd(&hist[ZERO >> (32 - BITS0)], zeros);
+    __syncthreads();
+    // a warp two groups of bins
+    int* const out = a.hist + (int64_t)b * (GROUPS + BINS);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        constexpr int G = BINS / GROUPS;
+        const int g = (tid >> 5) * 2 + h;
+        int sum = 0;
+#pragma unroll
+        for (int q = 0; q < G / 32; ++q) {
+            const int i = g * G + 32 * q + (tid & 31), c = hist[i];
+            if (c) atomicAdd(&out[GROUPS + i], c);
+            sum += c;
+        }
+        sum = __reduce_add_sync(0xffffffffu, sum);
+        if ((tid & 31) == 0 && sum) atomicAdd(&out[g], sum);
+    }
+}
+
+__global__ void __launch_bounds__(NT) kv_evict_border(const EvictArgs a) {
+    __shared__ __align__(16) int hist[ALL_BINS - BINS];
+    __shared__ uint32_t held[CHUNK];                     // the first integers of the list
+    __shared__ Shared s;
+    __shared__ int base, last;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.y;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const Plan p = plan_of(a, b);
+    if (!p.formed && blockIdx.x == 0 && tid == 0) {
+        a.border[b] = without_choice(p);
+        write_lens(a, b, p);
+    }
+    if (p.bad || blockIdx.x * CHUNK >= p.n) return;
+    uint32_t u[ITEMS];
+    chunk_keys(a, b, p, u);
+    Border o = without_choice(p);
+    int shift = 32 - BITS0;
+    bool known = true;
+    if (p.formed && tid < 32) {
+        // the border's bin: its group, then the bin
+        constexpr int PER = BINS / GROUPS / 32;
+        const int* const in = a.hist + (int64_t)b * (GROUPS + BINS);
+        int v[2] = {__ldcg(in + 2 * lane), __ldcg(in + 2 * lane + 1)}, at = 0, left = 0, keys = 0;
+        const unsigned hit = __ballot_sync(0xffffffffu, find_in_warp(v, p.want, &at, &left, &keys));
+        const int src = __ffs(hit) - 1, group = __shfl_sync(0xffffffffu, at, src), rest = __shfl_sync(0xffffffffu, left, src);
+        int w[PER];
+#pragma unroll
+        for (int q = 0; q < PER; ++q) w[q] = __ldcg(in + GROUPS + group * 32 * PER + lane * PER + q);
+        if (find_in_warp(w, rest, &at, &left, &keys)) {
+            s.found[0] = group * 32 * PER + at;
+            s.found[1] = left;
+            s.found[2] = keys;
+        }
+        if (lane == 0) s.listed = 0;
+    }
+    __syncthreads();
+    if (p.formed) {
+        o.top = 0;
+        known = narrow(s, shift, &o.top, &o.want);
+    }
+    // what stays for sure, and the ties: of the warp's keys, of the chunk's
+    const int warp = tid >> 5, w0 = blockIdx.x * CHUNK + warp * 32 * ITEMS, w1 = w0 + 32 * ITEMS;
+    int stay = 0, tie = 0;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        stay += u[i] < o.top;
+        tie += known && u[i] == o.top && u[i] != NONE;
+    }
+    int all = __reduce_add_sync(0xffffffffu, stay | tie << 16);
+    all += max(0, min(w1, p.lo) - min(w0, p.lo)) + max(0, min(w1, p.n) - max(min(w0, p.n), p.hi));
+    if (lane == 0) {
+        s.warp_sums[warp] = all;
+        a.warp_counts[((int64_t)b * gridDim.x + blockIdx.x) * 32 + warp] = all;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        all = __reduce_add_sync(0xffffffffu, s.warp_sums[lane]);
+        if (lane == 0) a.chunk_counts[(int64_t)b * gridDim.x + blockIdx.x] = all;
+    }
+    if (!p.formed) return;
+    uint2* const list = a.list + (int64_t)b * a.slot_stride;
+    if (!known) {
+        // the bin's keys go to the list, in any order
+        int mine = 0;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) mine += u[i] - o.top < 1u << shift;
+        int upto = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += y;
+        }
+        int at = 0;
+        if (lane == 31 && upto) at = atomicAdd(&s.listed, upto);
+        at = __shfl_sync(0xffffffffu, at, 31) + upto - mine;
+        __syncthreads();
+        if (tid == 0) base = s.listed ? atomicAdd(&a.done[2 * b + 1], s.listed) : 0;
+        __syncthreads();
+        at += base;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i)
+            if (u[i] - o.top < 1u << shift) list[at++] = make_uint2(u[i], w0 + 32 * i + lane);
+    }
+    // the stream's last CTA goes on (one thread's fences stand for all: the barriers order the others' accesses)
+    __syncthreads();
+    if (tid == 0) {
+        __threadfence();
+        last = atomicAdd(&a.done[2 * b], 1) == (p.n - 1) / CHUNK;
+        __threadfence();
+    }
+    __syncthreads();
+    if (!last) return;
+    if (!known) {
+        const int m = __ldcg(&a.done[2 * b + 1]);
+        int* bins = hist;
+        for (int i = tid; i < (ALL_BINS - BINS) / 4; i += NT) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
+        __syncthreads();
+#pragma unroll 1
+        do {
+            const int bits = shift == 32 - BITS0 ? BITS1 : BITS2, above = shift;
+            shift -= bits;
+#pragma unroll 4
+            for (int i = tid; i < m; i += NT) {
+                uint32_t x;
+                if (shift > 0 && i < CHUNK) held[i] = x = __ldcg(list + i).x;
+                else x = i < CHUNK ? held[i] : __ldcg(list + i).x;
+                if (x - o.top < 1u << above) atomicAdd(&bins[(x >> shift) & ((1u << bits) - 1u)], 1);
+            }
+            if (bits == BITS1) find_bin<1 << BITS1>(cluster, 1, 1, bins, s, o.want);
+            else find_bin<1 << BITS2>(cluster, 1, 2, bins, s, o.want);
+            bins += 1 << BITS1;
+        } while (!narrow(s, shift, &o.top, &o.want));
+#pragma unroll 4
+        for (int i = tid; i < m; i += NT) {
+            const uint32_t x = i < CHUNK ? held[i] : __ldcg(list + i).x;
+            if (x <= o.top) {
+                const int one = x < o.top ? 1 : 1 << 16, j = __ldcg(list + i).y;
+                atomicAdd(&a.chunk_counts[(int64_t)b * gridDim.x + j / CHUNK], one);
+                atomicAdd(&a.warp_counts[(int64_t)b * gridDim.x * 32 + j / (32 * ITEMS)], one);
+            }
+        }
+    }
+    if (tid == 0) {
+        a.border[b] = o;
+        write_lens(a, b, p);
+    }
+}
+
+// A CTA 2048 keys, a warp 256.
 constexpr int TAKE_NT = 256, TAKE_KEYS = TAKE_NT * ITEMS;
-__global__ void __launch_bounds__(TAKE_NT) kv_evict_take(const EvictArgs a) {
+__global__ void __launch_bounds__(TAKE_NT, 4) kv_evict_take(const EvictArgs a) {
     __shared__ int sums[2][TAKE_NT / 32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.y;
-    const Border o = a.border[b];
     const int first = blockIdx.x * TAKE_KEYS;
-    if (first >= o.n) return;                            // (a bad length: 0 keys)
     const int64_t row = (int64_t)b * a.slot_stride;
     const int chunks = (a.slot_stride + CHUNK - 1) / CHUNK, chunk = first / CHUNK;
+    const int me = (first - chunk * CHUNK) / (32 * ITEMS) + warp;   // the warp's place in its chunk
+    const Border o = a.border[b];
     Keys keys;
     const int j0 = first + warp * 32 * ITEMS + lane;
-    keys.load(a, o, row, j0, ITEMS);
+    const int c = lane < me ? a.warp_counts[((int64_t)b * chunks + chunk) * 32 + lane] : 0;
     int before = 0, equal = 0;
     for (int g = tid; g < chunk; g += TAKE_NT) {
-        const int c = a.chunk_counts[(int64_t)b * chunks + g];
-        before += c & 0xffff;
-        equal += c >> 16;
+        const int k = a.chunk_counts[(int64_t)b * chunks + g];
+        before += k & 0xffff;
+        equal += k >> 16;
     }
+    if (first >= o.n) return;                            // (a bad length: 0 keys)
+    keys.fetch_weights(a, o.n, row, j0, ITEMS);
+    keys.fetch(a, o.n, row, j0, ITEMS);
+    keys.choose(o, j0, ITEMS);
     before = __reduce_add_sync(0xffffffffu, before);
     equal = __reduce_add_sync(0xffffffffu, equal);
     if (lane == 0) {
@@ -475,14 +576,29 @@ __global__ void __launch_bounds__(TAKE_NT) kv_evict_take(const EvictArgs a) {
         before += sums[0][w];
         equal += sums[1][w];
     }
-    const int me = (first - chunk * CHUNK) / (32 * ITEMS) + warp;   // the warp's place in its chunk
-    const int c = lane < me ? a.warp_counts[((int64_t)b * chunks + chunk) * 32 + lane] : 0;
     before += __reduce_add_sync(0xffffffffu, c & 0xffff);
     equal += __reduce_add_sync(0xffffffffu, c >> 16);
     if (j0 - lane < o.n) keys.write(a, o, row, j0, ITEMS, before, equal);
 }
 
-// CTAs a stream: up to sixteen while they have a round each and the launch stays within one wave.
+// What was to be compacted in place comes back from the workspace (`from`: null where it was not).
+struct Back {
+    const int32_t *table, *pos, *doc;
+    const float* weights;
+};
+__global__ void __launch_bounds__(TAKE_NT) kv_evict_back(const EvictArgs a, const Back from) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int b = blockIdx.y, n = a.border[b].n, K = n ? a.border[b].K : 0;
+    const int64_t row = (int64_t)b * a.slot_stride;
+    for (int j = blockIdx.x * TAKE_KEYS + threadIdx.x, e = min(K, (int)(blockIdx.x + 1) * TAKE_KEYS); j < e; j += TAKE_NT) {
+        if (from.table) a.table_out[row + j] = from.table[row + j];
+        if (from.weights) a.weights_out[row + j] = from.weights[row + j];
+        if (from.pos) a.pos_out[row + j] = from.pos[row + j];
+        if (from.doc) a.doc_out[row + j] = from.doc[row + j];
+    }
+}
+
+// CTAs a stream: up to sixteen while that leaves them 8192 keys or more and the launch stays within one wave.
 int evict_cluster(int B, int slot_stride, int num_sms) {
     int C = 1;
     while (C < MAX_CLUSTER && (long long)C * CHUNK < slot_stride && 2ll * C * B <= num_sms) C *= 2;
@@ -492,19 +608,13 @@ int evict_cluster(int B, int slot_stride, int num_sms) {
 cudaError_t launch_kv_evict(const EvictArgs& a, int B, int C, int dev, cudaStream_t stream) {
     static std::atomic<bool> attr_set[64];
     if (!attr_set[dev].load(std::memory_order_acquire)) {
-        cudaError_t e = cudaFuncSetAttribute(kv_evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(kv_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (ALL_BINS + MAX_LIST + MAX_HELD) * 4);
+        const cudaError_t e = cudaFuncSetAttribute(kv_evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
         attr_set[dev].store(true, std::memory_order_release);
     }
-    const long long per_round = (long long)C * CHUNK, rounds = (a.slot_stride + per_round - 1) / per_round;
-    const int cap = (int)min(rounds * CHUNK, (long long)MAX_HELD);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(B * C));
     cfg.blockDim = dim3(NT);
-    cfg.dynamicSmemBytes = (size_t)(ALL_BINS + MAX_LIST + cap) * 4;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -515,14 +625,52 @@ cudaError_t launch_kv_evict(const EvictArgs& a, int B, int C, int dev, cudaStrea
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_evict_kernel, a, C, cap);
-    if (e != cudaSuccess || !a.border) return e;
-    return launch_dependent(kv_evict_take, dim3((a.slot_stride + TAKE_KEYS - 1) / TAKE_KEYS, B), dim3(TAKE_NT), 0, stream, a);
+    return cudaLaunchKernelEx(&cfg, kv_evict_kernel, a, C);
 }
 
-size_t evict_workspace(int B, int slot_stride) {
-    const size_t chunks = ((size_t)slot_stride + CHUNK - 1) / CHUNK;
-    return align256((size_t)B * sizeof(Border)) + (size_t)B * chunks * 33 * 4;
+// The wide form's workspace: what has to be zero first, and (in place) four tables at its end.
+struct Wide {
+    size_t zeroed, border, chunk_counts, warp_counts, list, tables, total;
+};
+Wide evict_workspace(int B, int slot_stride, bool in_place) {
+    const size_t chunks = ((size_t)slot_stride + CHUNK - 1) / CHUNK, table = align256((size_t)B * slot_stride * 4);
+    Wide w;
+    w.zeroed = align256((size_t)B * (GROUPS + BINS + 2) * 4);
+    w.border = w.zeroed;
+    w.chunk_counts = w.border + align256((size_t)B * sizeof(Border));
+    w.warp_counts = w.chunk_counts + align256((size_t)B * chunks * 4);
+    w.list = w.warp_counts + align256((size_t)B * chunks * 32 * 4);
+    w.tables = w.list + 2 * table;
+    w.total = w.tables + (in_place ? 4 * table : 0);
+    return w;
+}
+
+cudaError_t launch_kv_evict_wide(EvictArgs a, int B, bool in_place, void* workspace, cudaStream_t stream) {
+    const Wide w = evict_workspace(B, a.slot_stride, in_place);
+    char* const ws = static_cast<char*>(workspace);
+    a.hist = reinterpret_cast<int32_t*>(ws);
+    a.done = a.hist + (size_t)B * (GROUPS + BINS);
+    a.border = reinterpret_cast<Border*>(ws + w.border);
+    a.chunk_counts = reinterpret_cast<int32_t*>(ws + w.chunk_counts);
+    a.warp_counts = reinterpret_cast<int32_t*>(ws + w.warp_counts);
+    a.list = reinterpret_cast<uint2*>(ws + w.list);
+    cudaError_t e = cudaMemsetAsync(ws, 0, w.zeroed, stream);
+    const dim3 grid((a.slot_stride + CHUNK - 1) / CHUNK, B), take((a.slot_stride + TAKE_KEYS - 1) / TAKE_KEYS, B);
+    if (e == cudaSuccess) e = launch_dependent(kv_evict_count, grid, dim3(NT), 0, stream, a);
+    if (e == cudaSuccess) e = launch_dependent(kv_evict_border, grid, dim3(NT), 0, stream, a);
+    EvictArgs t = a;
+    Back from = {};
+    if (in_place) {
+        const size_t table = align256((size_t)B * a.slot_stride * 4);
+        char* const to = ws + w.tables;
+        if (a.table_out == a.slot) from.table = t.table_out = reinterpret_cast<int32_t*>(to);
+        if (a.weights_out == a.weights) from.weights = t.weights_out = reinterpret_cast<float*>(to + table);
+        if (a.pos_out && a.pos_out == a.key_pos) from.pos = t.pos_out = reinterpret_cast<int32_t*>(to + 2 * table);
+        if (a.doc_out && a.doc_out == a.key_doc) from.doc = t.doc_out = reinterpret_cast<int32_t*>(to + 3 * table);
+    }
+    if (e == cudaSuccess) e = launch_dependent(kv_evict_take, take, dim3(TAKE_NT), 0, stream, t);
+    if (e == cudaSuccess && in_place) e = launch_dependent(kv_evict_back, take, dim3(TAKE_NT), 0, stream, a, from);
+    return e;
 }
 
 }  // namespace
@@ -545,25 +693,25 @@ extern "C" int mla_kv_evict(const int32_t* slot_table, const int32_t* seq_lens, 
                          lens_out, weights_out, pos_out, doc_out, freed, n_freed};
     for (const void* p : all)
         if (!aligned(p, 4)) return MLA_ERR_ALIGN;
-    if (!aligned(workspace, 4)) return MLA_ERR_ALIGN;
+    if (!aligned(workspace, 16)) return MLA_ERR_ALIGN;
     EvictArgs a = {slot_table, seq_lens, weights, key_pos, key_doc, slot_stride, budgets, budget, sink, recent, table_out,
-                   lens_out, weights_out, pos_out, doc_out, freed, n_freed, nullptr, nullptr, nullptr, nullptr};
+                   lens_out, weights_out, pos_out, doc_out, freed, n_freed};
     int num_sms = 0, dev = 0;
     const int rc = device_state(&dev, &a.status, &num_sms);
     if (rc != MLA_OK) return rc;
     const int C = evict_cluster(B, slot_stride, num_sms);
     const bool in_place = table_out == slot_table || weights_out == weights || (pos_out && pos_out == key_pos) || (doc_out && doc_out == key_doc);
-    if ((long long)C * CHUNK < slot_stride && !in_place && workspace && ws_bytes >= evict_workspace(B, slot_stride)) {
-        const size_t chunks = ((size_t)slot_stride + CHUNK - 1) / CHUNK;
-        a.border = static_cast<Border*>(workspace);
-        a.chunk_counts = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + align256((size_t)B * sizeof(Border)));
-        a.warp_counts = a.chunk_counts + (size_t)B * chunks;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if ((long long)C * CHUNK >= slot_stride) {
+        if (launch_kv_evict(a, B, C, dev, st) != cudaSuccess) return MLA_ERR_LAUNCH;
+        return MLA_OK;
     }
-    if (launch_kv_evict(a, B, C, dev, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_LAUNCH;
+    if (!workspace || ws_bytes < evict_workspace(B, slot_stride, in_place).total) return MLA_ERR_WORKSPACE;
+    if (launch_kv_evict_wide(a, B, in_place, workspace, st) != cudaSuccess) return MLA_ERR_LAUNCH;
     return MLA_OK;
 }
 
-extern "C" size_t mla_kv_evict_workspace_bytes(int B, int slot_stride, int num_sms) {
+extern "C" size_t mla_kv_evict_workspace_bytes(int B, int slot_stride, int in_place, int num_sms) {
     if (B <= 0 || B > 65535 || slot_stride < 1 || slot_stride > MLA_MAX_FP8_KEYS || num_sms < 1) return 0;
-    return (long long)evict_cluster(B, slot_stride, num_sms) * CHUNK < slot_stride ? evict_workspace(B, slot_stride) : 0;
+    return (long long)evict_cluster(B, slot_stride, num_sms) * CHUNK < slot_stride ? evict_workspace(B, slot_stride, in_place != 0).total : 0;
 }
