@@ -419,10 +419,7 @@ __global__ void __launch_bounds__(NT) kv_evict_border(const EvictArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Plan p = plan_of(a, b);
-    if (!p.formed && blockIdx.x == 0 && tid == 0) {
-        a.border[b] = without_choice(p);
-        write_lens(a, b, p);
-    }
+    if (!p.formed && blockIdx.x == 0 && tid == 0) a.border[b] = without_choice(p);
     if (p.bad || blockIdx.x * CHUNK >= p.n) return;
     uint32_t u[ITEMS];
     chunk_keys(a, b, p, u);
@@ -533,10 +530,7 @@ __global__ void __launch_bounds__(NT) kv_evict_border(const EvictArgs a) {
             }
         }
     }
-    if (tid == 0) {
-        a.border[b] = o;
-        write_lens(a, b, p);
-    }
+    if (tid == 0) a.border[b] = o;
 }
 
 // A CTA 2048 keys, a warp 256.
@@ -550,6 +544,8 @@ __global__ void __launch_bounds__(TAKE_NT, 4) kv_evict_take(const EvictArgs a) {
     const int chunks = (a.slot_stride + CHUNK - 1) / CHUNK, chunk = first / CHUNK;
     const int me = (first - chunk * CHUNK) / (32 * ITEMS) + warp;   // the warp's place in its chunk
     const Border o = a.border[b];
+    // (only here, by the one thread that still reads the length: lens_out may be seq_lens)
+    if (blockIdx.x == 0 && tid == 0) write_lens(a, b, plan_of(a, b));
     Keys keys;
     const int j0 = first + warp * 32 * ITEMS + lane;
     const int c = lane < me ? a.warp_counts[((int64_t)b * chunks + chunk) * 32 + lane] : 0;

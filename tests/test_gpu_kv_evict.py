@@ -114,6 +114,14 @@ def test_short_streams_in_a_wide_table(cuda_lib, kind):
         run(cuda_lib, make(19, lens, 300000, kind), 30, 1, 2, inplace=inplace)
 
 
+def test_no_choice_in_a_wide_table(cuda_lib):
+    """Sinks and recent keys are the whole budget, in place, with more chunks than run at once: every one of them
+    needs the length that is replaced."""
+    lens = [1000000, 999999, 20, 0, 600000, 300000]
+    for budget, sink, recent in ((0, 0, 0), (0, 200001, 200000), (64, 32, 32), (5, 1000000, 0)):
+        run(cuda_lib, make(23, lens, 1000000, doc=False), budget, sink, recent, inplace=True)
+
+
 def test_many_streams(cuda_lib):
     lens = [(37 * i) % 211 for i in range(700)]
     run(cuda_lib, make(11, lens, 211, "ties"), 64, 4, 8, inplace=True)
