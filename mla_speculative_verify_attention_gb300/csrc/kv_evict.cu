@@ -54,6 +54,7 @@ struct EvictArgs {
     // workspace of the wide form
     int32_t* hist;                                   // [B][GROUPS + BINS], zeroed: sums of the groups of bins, the bins
     int32_t* done;                                   // [B][2], zeroed: CTAs that have listed, keys listed
+    int32_t* lens;                                   // [B]: keys (0: a bad length)
     struct Border* border;                           // [B]
     int32_t* chunk_counts;                           // [B][chunks]: keys that stay | ties << 16
     int32_t* warp_counts;                            // [B][chunks * 32]: the same of a warp's 256 keys
@@ -371,13 +372,24 @@ __device__ __forceinline__ void chunk_keys(const EvictArgs& a, int b, const Plan
     for (int i = 0; i < ITEMS; ++i) u[i] = (unsigned)(j0 + 32 * i - p.lo) < (unsigned)(p.hi - p.lo) ? order_of(w[i]) : NONE;
 }
 
-__global__ void __launch_bounds__(NT) kv_evict_count(const EvictArgs a) {
-    __shared__ __align__(16) int hist[BINS];
+// Each of these kernels starts while the one before it ends, and reads the call's inputs before it waits for it:
+// what came before the call has ended by then, since each lets the next one start after a wait of its own, and only
+// the last ones write outside of the workspace.
+__global__ void __launch_bounds__(256) kv_evict_zero(int4* ws, int n) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) ws[i] = make_int4(0, 0, 0, 0);
+}
+
+__global__ void __launch_bounds__(NT) kv_evict_count(const EvictArgs a) {
+    __shared__ __align__(16) int hist[BINS];
     const int tid = threadIdx.x, b = blockIdx.y;
     const Plan p = plan_of(a, b);
-    if (!p.formed || blockIdx.x * CHUNK >= p.n) return;
+    if (!p.formed || blockIdx.x * CHUNK >= p.n) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (blockIdx.x == 0 && tid == 0) a.lens[b] = p.bad ? 0 : p.n;
+        return;
+    }
     for (int i = tid; i < BINS / 4; i += NT) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
     uint32_t u[ITEMS];
     chunk_keys(a, b, p, u);
@@ -391,6 +403,9 @@ __global__ void __launch_bounds__(NT) kv_evict_count(const EvictArgs a) {
     zeros = __reduce_add_sync(0xffffffffu, zeros);
     if ((tid & 31) == 0 && zeros) atomicAdd(&hist[ZERO >> (32 - BITS0)], zeros);
     __syncthreads();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (blockIdx.x == 0 && tid == 0) a.lens[b] = p.n;
     // a warp two groups of bins
     int* const out = a.hist + (int64_t)b * (GROUPS + BINS);
 #pragma unroll
@@ -416,13 +431,13 @@ __global__ void __launch_bounds__(NT) kv_evict_border(const EvictArgs a) {
     __shared__ int base, last;
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.y;
+    const Plan p = plan_of(a, b);
+    uint32_t u[ITEMS];
+    if (!p.bad) chunk_keys(a, b, p, u);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Plan p = plan_of(a, b);
     if (!p.formed && blockIdx.x == 0 && tid == 0) a.border[b] = without_choice(p);
     if (p.bad || blockIdx.x * CHUNK >= p.n) return;
-    uint32_t u[ITEMS];
-    chunk_keys(a, b, p, u);
     Border o = without_choice(p);
     int shift = 32 - BITS0;
     bool known = true;
@@ -537,17 +552,19 @@ __global__ void __launch_bounds__(NT) kv_evict_border(const EvictArgs a) {
 constexpr int TAKE_NT = 256, TAKE_KEYS = TAKE_NT * ITEMS;
 __global__ void __launch_bounds__(TAKE_NT, 4) kv_evict_take(const EvictArgs a) {
     __shared__ int sums[2][TAKE_NT / 32];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.y;
     const int first = blockIdx.x * TAKE_KEYS;
     const int64_t row = (int64_t)b * a.slot_stride;
     const int chunks = (a.slot_stride + CHUNK - 1) / CHUNK, chunk = first / CHUNK;
     const int me = (first - chunk * CHUNK) / (32 * ITEMS) + warp;   // the warp's place in its chunk
+    const int j0 = first + warp * 32 * ITEMS + lane, n = a.lens[b];
+    Keys keys;
+    keys.fetch_weights(a, n, row, j0, ITEMS);
+    keys.fetch(a, n, row, j0, ITEMS);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const Border o = a.border[b];
     // (only here, by the one thread that still reads the length: lens_out may be seq_lens)
     if (blockIdx.x == 0 && tid == 0) write_lens(a, b, plan_of(a, b));
-    Keys keys;
-    const int j0 = first + warp * 32 * ITEMS + lane;
     const int c = lane < me ? a.warp_counts[((int64_t)b * chunks + chunk) * 32 + lane] : 0;
     int before = 0, equal = 0;
     for (int g = tid; g < chunk; g += TAKE_NT) {
@@ -556,8 +573,6 @@ __global__ void __launch_bounds__(TAKE_NT, 4) kv_evict_take(const EvictArgs a) {
         equal += k >> 16;
     }
     if (first >= o.n) return;                            // (a bad length: 0 keys)
-    keys.fetch_weights(a, o.n, row, j0, ITEMS);
-    keys.fetch(a, o.n, row, j0, ITEMS);
     keys.choose(o, j0, ITEMS);
     before = __reduce_add_sync(0xffffffffu, before);
     equal = __reduce_add_sync(0xffffffffu, equal);
@@ -626,13 +641,14 @@ cudaError_t launch_kv_evict(const EvictArgs& a, int B, int C, int dev, cudaStrea
 
 // The wide form's workspace: what has to be zero first, and (in place) four tables at its end.
 struct Wide {
-    size_t zeroed, border, chunk_counts, warp_counts, list, tables, total;
+    size_t zeroed, lens, border, chunk_counts, warp_counts, list, tables, total;
 };
 Wide evict_workspace(int B, int slot_stride, bool in_place) {
     const size_t chunks = ((size_t)slot_stride + CHUNK - 1) / CHUNK, table = align256((size_t)B * slot_stride * 4);
     Wide w;
     w.zeroed = align256((size_t)B * (GROUPS + BINS + 2) * 4);
-    w.border = w.zeroed;
+    w.lens = w.zeroed;
+    w.border = w.lens + align256((size_t)B * 4);
     w.chunk_counts = w.border + align256((size_t)B * sizeof(Border));
     w.warp_counts = w.chunk_counts + align256((size_t)B * chunks * 4);
     w.list = w.warp_counts + align256((size_t)B * chunks * 32 * 4);
@@ -646,11 +662,14 @@ cudaError_t launch_kv_evict_wide(EvictArgs a, int B, bool in_place, void* worksp
     char* const ws = static_cast<char*>(workspace);
     a.hist = reinterpret_cast<int32_t*>(ws);
     a.done = a.hist + (size_t)B * (GROUPS + BINS);
+    a.lens = reinterpret_cast<int32_t*>(ws + w.lens);
     a.border = reinterpret_cast<Border*>(ws + w.border);
     a.chunk_counts = reinterpret_cast<int32_t*>(ws + w.chunk_counts);
     a.warp_counts = reinterpret_cast<int32_t*>(ws + w.warp_counts);
     a.list = reinterpret_cast<uint2*>(ws + w.list);
-    cudaError_t e = cudaMemsetAsync(ws, 0, w.zeroed, stream);
+    const int vectors = (int)(w.zeroed / 16);            // (at most 65535 streams' 33 KB)
+    cudaError_t e = launch_dependent(kv_evict_zero, dim3((unsigned)min((vectors + 255) / 256, 1024)), dim3(256), 0, stream,
+                                     reinterpret_cast<int4*>(ws), vectors);
     const dim3 grid((a.slot_stride + CHUNK - 1) / CHUNK, B), take((a.slot_stride + TAKE_KEYS - 1) / TAKE_KEYS, B);
     if (e == cudaSuccess) e = launch_dependent(kv_evict_count, grid, dim3(NT), 0, stream, a);
     if (e == cudaSuccess) e = launch_dependent(kv_evict_border, grid, dim3(NT), 0, stream, a);
