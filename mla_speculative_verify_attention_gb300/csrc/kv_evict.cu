@@ -104,61 +104,63 @@ __device__ __forceinline__ void write_lens(const EvictArgs& a, int b, const Plan
     if (a.n_freed) a.n_freed[b] = p.bad ? 0 : p.n - p.K;
 }
 
-// A thread's keys j0 + 32 i of the stream, and which of them stay (bit i) or tie (bit 8 + i).
+// A thread's keys j0 + 32 i of the stream, and which of them stay (bit i) or tie
+// (bit 16 + i).  N: keys of a thread, up to 16; DOCS: with documents.
+template <int N, bool DOCS>
 struct Keys {
-    float w[ITEMS];
-    int slot[ITEMS], pos[ITEMS], doc[ITEMS];
+    float w[N];
+    int slot[N], pos[N], doc[N];
     unsigned mine;
 
     __device__ __forceinline__ void fetch_weights(const EvictArgs& a, int n, int64_t row, int j0, int items) {
         const float* const at = a.weights + row + j0;    // (items lie at fixed offsets from here)
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i) w[i] = i < items && j0 + 32 * i < n ? at[32 * i] : 0.f;
+        for (int i = 0; i < N; ++i) w[i] = i < items && j0 + 32 * i < n ? at[32 * i] : 0.f;
     }
     __device__ __forceinline__ void fetch(const EvictArgs& a, int n, int64_t row, int j0, int items) {
         const int32_t* const slots = a.slot + row + j0;
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i) slot[i] = i < items && j0 + 32 * i < n ? slots[32 * i] : 0;
+        for (int i = 0; i < N; ++i) slot[i] = i < items && j0 + 32 * i < n ? slots[32 * i] : 0;
         if (a.pos_out) {
             const int32_t* const at = a.key_pos + row + j0;
 #pragma unroll
-            for (int i = 0; i < ITEMS; ++i) pos[i] = a.key_pos && i < items && j0 + 32 * i < n ? at[32 * i] : j0 + 32 * i;
+            for (int i = 0; i < N; ++i) pos[i] = a.key_pos && i < items && j0 + 32 * i < n ? at[32 * i] : j0 + 32 * i;
         }
-        if (a.doc_out) {
+        if (DOCS && a.doc_out) {
             const int32_t* const at = a.key_doc + row + j0;
 #pragma unroll
-            for (int i = 0; i < ITEMS; ++i) doc[i] = i < items && j0 + 32 * i < n ? at[32 * i] : 0;
+            for (int i = 0; i < N; ++i) doc[i] = i < items && j0 + 32 * i < n ? at[32 * i] : 0;
         }
     }
     // Returns the warp's counts: stay | ties << 16.
     __device__ __forceinline__ int choose(const Border& o, int j0, int items) {
         mine = 0;
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
+        for (int i = 0; i < N; ++i) {
             const int j = j0 + 32 * i;
             const uint32_t u = order_of(w[i]);
             const bool in = i < items && j < o.n, mid = j >= o.lo && j < o.hi;
-            mine |= (unsigned)(in && (!mid || u < o.top)) << i | (unsigned)(in && mid && u == o.top) << (8 + i);
+            mine |= (unsigned)(in && (!mid || u < o.top)) << i | (unsigned)(in && mid && u == o.top) << (16 + i);
         }
-        return __reduce_add_sync(0xffffffffu, __popc(mine & 0xffu) | __popc(mine >> 8) << 16);
+        return __reduce_add_sync(0xffffffffu, __popc(mine & 0xffffu) | __popc(mine >> 16) << 16);
     }
     // `before`, `equal`: keys before the warp's that stay for sure, and ties.
     __device__ __forceinline__ void write(const EvictArgs& a, const Border& o, int64_t row, int j0, int items, int before, int equal) const {
         const int lane = threadIdx.x & 31;
         const unsigned lower = (1u << lane) - 1u;
         before += min(equal, o.want);                    // with the ties that stay
-        const bool ties = __any_sync(0xffffffffu, mine >> 8);
+        const bool ties = __any_sync(0xffffffffu, mine >> 16);
         int32_t* const table = a.table_out + row;
         float* const weights = a.weights_out + row;
         int32_t *const positions = a.pos_out + row, *const docs = a.doc_out + row;   // (where there are any)
         int32_t* const freed = a.freed + row + j0;
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
+        for (int i = 0; i < N; ++i) {
             const int j = j0 + 32 * i;
             if (i >= items || j - lane >= o.n) break;
             unsigned keep = __ballot_sync(0xffffffffu, (mine >> i) & 1u);
             if (ties) {                                  // the first of them, as many as are wanted
-                const unsigned tie = __ballot_sync(0xffffffffu, (mine >> (8 + i)) & 1u);
+                const unsigned tie = __ballot_sync(0xffffffffu, (mine >> (16 + i)) & 1u);
                 const int room = o.want - min(equal, o.want), m = __popc(tie);
                 equal += m;
                 if (room >= m) keep |= tie;
@@ -166,13 +168,12 @@ struct Keys {
             }
             const int to = before + __popc(keep & lower);
             before += __popc(keep);
-            if ((keep >> lane) & 1u) {
-                table[to] = slot[i];
+            const bool stays = (keep >> lane) & 1u;
+            if (stays || (j < o.n && a.freed)) *(stays ? table + to : freed + (32 * i - to)) = slot[i];
+            if (stays) {
                 weights[to] = w[i];
                 if (a.pos_out) positions[to] = pos[i];
-                if (a.doc_out) docs[to] = doc[i];
-            } else if (j < o.n && a.freed) {
-                freed[32 * i - to] = slot[i];
+                if (DOCS && a.doc_out) docs[to] = doc[i];
             }
         }
     }
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(NT, 1) kv_evict_kernel(const EvictArgs a, int 
     const int64_t row = (int64_t)b * a.slot_stride;
     const int items = p.bad ? 1 : max(1, min(ITEMS, (p.n + C * NT - 1) / (C * NT)));
     const int j0 = (rank * NT + warp * 32) * items + lane, n = p.bad ? 0 : p.n;
-    Keys keys;
+    Keys<ITEMS, true> keys;
     keys.fetch_weights(a, n, row, j0, items);
     for (int i = tid; i < ALL_BINS / 4; i += NT) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
     if (C > 1) cluster.sync();                           // every CTA runs, and has read the length
@@ -381,7 +382,7 @@ __global__ void __launch_bounds__(256) kv_evict_zero(int4* ws, int n) {
     for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) ws[i] = make_int4(0, 0, 0, 0);
 }
 
-__global__ void __launch_bounds__(NT) kv_evict_count(const EvictArgs a) {
+__global__ void __launch_bounds__(NT, 2) kv_evict_count(const EvictArgs a) {
     __shared__ __align__(16) int hist[BINS];
     const int tid = threadIdx.x, b = blockIdx.y;
     const Plan p = plan_of(a, b);
@@ -424,9 +425,10 @@ __global__ void __launch_bounds__(NT) kv_evict_count(const EvictArgs a) {
     }
 }
 
-__global__ void __launch_bounds__(NT) kv_evict_border(const EvictArgs a) {
+constexpr int HELD = 4096;
+__global__ void __launch_bounds__(NT, 2) kv_evict_border(const EvictArgs a) {
     __shared__ __align__(16) int hist[ALL_BINS - BINS];
-    __shared__ uint32_t held[CHUNK];                     // the first integers of the list
+    __shared__ uint2 held[HELD];                         // the list's first keys
     __shared__ Shared s;
     __shared__ int base, last;
     cg::cluster_group cluster = cg::this_cluster();
@@ -434,6 +436,7 @@ __global__ void __launch_bounds__(NT) kv_evict_border(const EvictArgs a) {
     const Plan p = plan_of(a, b);
     uint32_t u[ITEMS];
     if (!p.bad) chunk_keys(a, b, p, u);
+    for (int i = tid; i < (ALL_BINS - BINS) / 4; i += NT) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (!p.formed && blockIdx.x == 0 && tid == 0) a.border[b] = without_choice(p);
@@ -518,30 +521,38 @@ __global__ void __launch_bounds__(NT) kv_evict_border(const EvictArgs a) {
     if (!known) {
         const int m = __ldcg(&a.done[2 * b + 1]);
         int* bins = hist;
-        for (int i = tid; i < (ALL_BINS - BINS) / 4; i += NT) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
-        __syncthreads();
 #pragma unroll 1
         do {
             const int bits = shift == 32 - BITS0 ? BITS1 : BITS2, above = shift;
             shift -= bits;
-#pragma unroll 4
-            for (int i = tid; i < m; i += NT) {
-                uint32_t x;
-                if (shift > 0 && i < CHUNK) held[i] = x = __ldcg(list + i).x;
-                else x = i < CHUNK ? held[i] : __ldcg(list + i).x;
-                if (x - o.top < 1u << above) atomicAdd(&bins[(x >> shift) & ((1u << bits) - 1u)], 1);
+            for (int first = tid; first < m; first += 4 * NT) {
+                uint2 key[4];                            // (read before any is counted)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int i = first + q * NT;
+                    key[q] = i >= m ? make_uint2(NONE, 0) : shift == 0 && i < HELD ? held[i] : __ldcg(list + i);
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int i = first + q * NT;
+                    if (shift > 0 && i < min(m, HELD)) held[i] = key[q];
+                    if (key[q].x - o.top < 1u << above) atomicAdd(&bins[(key[q].x >> shift) & ((1u << bits) - 1u)], 1);
+                }
             }
             if (bits == BITS1) find_bin<1 << BITS1>(cluster, 1, 1, bins, s, o.want);
             else find_bin<1 << BITS2>(cluster, 1, 2, bins, s, o.want);
             bins += 1 << BITS1;
         } while (!narrow(s, shift, &o.top, &o.want));
-#pragma unroll 4
-        for (int i = tid; i < m; i += NT) {
-            const uint32_t x = i < CHUNK ? held[i] : __ldcg(list + i).x;
-            if (x <= o.top) {
-                const int one = x < o.top ? 1 : 1 << 16, j = __ldcg(list + i).y;
-                atomicAdd(&a.chunk_counts[(int64_t)b * gridDim.x + j / CHUNK], one);
-                atomicAdd(&a.warp_counts[(int64_t)b * gridDim.x * 32 + j / (32 * ITEMS)], one);
+        // those that stay or tie go to the counts; a chunk's keys lie together in the list, and a warp adds them up
+        for (int i = tid; i - lane < m; i += NT) {
+            const uint2 key = i >= m ? make_uint2(NONE, 0) : i < HELD ? held[i] : __ldcg(list + i);
+            const bool mine = key.x <= o.top;
+            const int chunk = mine ? (int)(key.y / CHUNK) : -1;
+            const unsigned group = __match_any_sync(0xffffffffu, chunk), below = __ballot_sync(0xffffffffu, key.x < o.top) & group;
+            if (mine) {
+                atomicAdd(&a.warp_counts[(int64_t)b * gridDim.x * 32 + key.y / (32 * ITEMS)], key.x < o.top ? 1 : 1 << 16);
+                if (lane == __ffs(group) - 1)
+                    atomicAdd(&a.chunk_counts[(int64_t)b * gridDim.x + chunk], __popc(below) | __popc(group & ~below) << 16);
             }
         }
     }
@@ -549,18 +560,20 @@ __global__ void __launch_bounds__(NT) kv_evict_border(const EvictArgs a) {
 }
 
 // A CTA 2048 keys, a warp 256.
-constexpr int TAKE_NT = 256, TAKE_KEYS = TAKE_NT * ITEMS;
-__global__ void __launch_bounds__(TAKE_NT, 4) kv_evict_take(const EvictArgs a) {
+constexpr int TAKE_NT = 256, TAKE_ITEMS = 8, TAKE_KEYS = TAKE_NT * TAKE_ITEMS;
+template <bool DOCS>
+__global__ void __launch_bounds__(TAKE_NT, DOCS ? 4 : 5) kv_evict_take(const EvictArgs a) {
     __shared__ int sums[2][TAKE_NT / 32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.y;
     const int first = blockIdx.x * TAKE_KEYS;
     const int64_t row = (int64_t)b * a.slot_stride;
     const int chunks = (a.slot_stride + CHUNK - 1) / CHUNK, chunk = first / CHUNK;
-    const int me = (first - chunk * CHUNK) / (32 * ITEMS) + warp;   // the warp's place in its chunk
-    const int j0 = first + warp * 32 * ITEMS + lane, n = a.lens[b];
-    Keys keys;
-    keys.fetch_weights(a, n, row, j0, ITEMS);
-    keys.fetch(a, n, row, j0, ITEMS);
+    const int me = (first - chunk * CHUNK) / (32 * ITEMS) + warp * (TAKE_ITEMS / ITEMS);   // of the warp's first keys' counts
+    const int j0 = first + warp * 32 * TAKE_ITEMS + lane, n = a.lens[b];
+    if (first >= n && blockIdx.x > 0) return;            // (the stream's first CTA writes its lengths)
+    Keys<TAKE_ITEMS, DOCS> keys;
+    keys.fetch_weights(a, n, row, j0, TAKE_ITEMS);
+    keys.fetch(a, n, row, j0, TAKE_ITEMS);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Border o = a.border[b];
     // (only here, by the one thread that still reads the length: lens_out may be seq_lens)
@@ -573,7 +586,7 @@ __global__ void __launch_bounds__(TAKE_NT, 4) kv_evict_take(const EvictArgs a) {
         equal += k >> 16;
     }
     if (first >= o.n) return;                            // (a bad length: 0 keys)
-    keys.choose(o, j0, ITEMS);
+    keys.choose(o, j0, TAKE_ITEMS);
     before = __reduce_add_sync(0xffffffffu, before);
     equal = __reduce_add_sync(0xffffffffu, equal);
     if (lane == 0) {
@@ -589,7 +602,7 @@ __global__ void __launch_bounds__(TAKE_NT, 4) kv_evict_take(const EvictArgs a) {
     }
     before += __reduce_add_sync(0xffffffffu, c & 0xffff);
     equal += __reduce_add_sync(0xffffffffu, c >> 16);
-    if (j0 - lane < o.n) keys.write(a, o, row, j0, ITEMS, before, equal);
+    if (j0 - lane < o.n) keys.write(a, o, row, j0, TAKE_ITEMS, before, equal);
 }
 
 // What was to be compacted in place comes back from the workspace (`from`: null where it was not).
@@ -683,7 +696,7 @@ cudaError_t launch_kv_evict_wide(EvictArgs a, int B, bool in_place, void* worksp
         if (a.pos_out && a.pos_out == a.key_pos) from.pos = t.pos_out = reinterpret_cast<int32_t*>(to + 2 * table);
         if (a.doc_out && a.doc_out == a.key_doc) from.doc = t.doc_out = reinterpret_cast<int32_t*>(to + 3 * table);
     }
-    if (e == cudaSuccess) e = launch_dependent(kv_evict_take, take, dim3(TAKE_NT), 0, stream, t);
+    if (e == cudaSuccess) e = launch_dependent(a.doc_out ? kv_evict_take<true> : kv_evict_take<false>, take, dim3(TAKE_NT), 0, stream, t);
     if (e == cudaSuccess && in_place) e = launch_dependent(kv_evict_back, take, dim3(TAKE_NT), 0, stream, a, from);
     return e;
 }
