@@ -341,7 +341,9 @@ size_t mla_verify_fp8_workspace_bytes(int B, int q_len, int H, int max_seq, int 
  * tanh is off by at most 2^-21 of itself.  A row that sees nothing gets out = 0, lse = -inf.  Every other
  * argument, limit and error is that of mla_verify_attn_fp8(); with nsplit = 0 the workspace that it uses is
  * mla_verify_fp8_workspace_bytes() of max_seq = slot_stride, or of min(slot_stride, window - 1 + q_len)
- * with a window and no key_pos.
+ * with a window and no key_pos.  Where documents, or positions and a window, are given and the workspace goes on for
+ * 8 bytes a stream behind that size rounded up to 256 bytes, long streams are first searched for their
+ * longest run of keys that no draft sees, which is then not read.
  */
 int mla_verify_attn_fp8_rules(const void* q, const uint8_t* kv_lat, const float* kv_scale, const void* kv_rope,
                               int64_t n_pool, const int32_t* slot_table, int slot_stride, const int32_t* seq_lens,

@@ -661,6 +661,8 @@ def verify_attn_fp8_rules(q: torch.Tensor, kv_lat: torch.Tensor, kv_scale: torch
             longest = min(stride, window - 1 + q_len) if window > 0 and key_pos is None else stride
             need = workspace_bytes(B, q_len, H, nsplit) if nsplit > 0 else verify_fp8_workspace_bytes(
                 B, q_len, H, longest, num_sms(dev))
+            if key_doc is not None or (key_pos is not None and window > 0):
+                need += 256 + 8 * B                        # room to look for keys that no draft sees
             workspace = _empty(q, (max(need, 256),), torch.uint8, stream)
         _check("mla_verify_attn_fp8_rules", _call("mla_verify_attn_fp8_rules")(
             q.data_ptr(), kv_lat.data_ptr(), kv_scale.data_ptr(), kv_rope.data_ptr(), n_pool, slot_table.data_ptr(),

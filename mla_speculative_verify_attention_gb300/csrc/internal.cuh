@@ -69,14 +69,19 @@ __host__ __device__ inline void split_range(int n, int S, int s, int tile, int* 
 // The keys of a stream that a sliding window leaves visible to some draft, where a key's position is its
 // index: with p = n - q_len, draft 0 sees keys from p - window + 1 on, the others start later, and the
 // first prefix_lens[b] keys stay visible; between them is a gap that no kernel has to read.
-// window 0: all keys.
+// window 0: all keys.  Where a kernel before has looked for gaps (launch_key_gaps), its word holds.
 struct KeySpan {
     int window = 0;
     const int32_t* prefix_lens = nullptr;
+    const int2* gaps = nullptr;
 
     __device__ __forceinline__ void gap(int b, int n, int q_len, int* at, int* len) const {
         *at = *len = 0;
-        if (window > 0) {
+        if (gaps) {
+            const int2 g = __ldcg(gaps + b);
+            *at = g.x;
+            *len = g.y;
+        } else if (window > 0) {
             const int lo = max(0, n - q_len - window + 1);
             *at = prefix_lens ? min(max(__ldg(prefix_lens + b), 0), lo) : 0;
             *len = lo - *at;

@@ -82,12 +82,14 @@ struct ScoreRules {
     const int32_t* key_pos = nullptr;          // [B, slot_stride]; null: a key's index
     const int32_t* prefix_lens = nullptr;      // [B]
     const int32_t* key_doc = nullptr;          // [B, slot_stride]
+    const int2* gaps = nullptr;                // [B], of launch_key_gaps
     int masked = 0;                            // a window, a prefix or documents,
     int spans = 0;                             // and positions or documents given key by key
 
     // The keys that have to be looked at: with given positions any of them may be visible.
     __host__ __device__ __forceinline__ KeySpan span() const {
         KeySpan s;
+        s.gaps = gaps;
         if (!key_pos) {
             s.window = window;
             s.prefix_lens = prefix_lens;
@@ -111,6 +113,13 @@ struct ScoreRules {
         return r;
     }
 };
+
+// Whether keys that no draft sees can lie together without being known from the lengths alone.
+inline bool has_gaps(const ScoreRules& r) { return r.key_doc || (r.key_pos && r.window > 0); }
+// Finds each stream's longest run of keys before the drafts that none of them sees (in whole groups of 32):
+// gaps[b] = its first key, its keys.
+cudaError_t launch_key_gaps(const ScoreRules& r, const int32_t* seq_lens, int B, int q_len, int slot_stride, int2* gaps,
+                            cudaStream_t stream);
 
 // MLA_OK, or what is wrong with the rules' arguments.
 int check_rules(float softcap, const float* slopes, const int32_t* key_pos, int window, const int32_t* prefix_lens,

@@ -896,6 +896,11 @@ cudaError_t launch_verify_fp8(const Fp8Args& a, int n_tiles, int dev, cudaStream
     return launch_one<1, 2, RULES>(a, grid, dev, stream);
 }
 
+// Looking for keys that no draft sees costs 5 us, a tile 1.7: worth it where half of six tiles a CTA go.  (Measured,
+// documents, without and with: 32 streams of 2047 keys x 64 rows, nine tiles a CTA, all keys seen 45.4 and 50.7 us, half
+// 47.8 and 37.6, a tenth 45.2 and 31.6; 8 streams of 46000 keys x 72 rows 148 and 153, 149 and 92, 149 and 38.)
+constexpr int GAP_TILES = 6;
+
 // The checks and launches of a call.
 template <bool RULES>
 int verify_fp8_call(const void* q, const uint8_t* kv_lat, const float* kv_scale, const void* kv_rope, int64_t n_pool,
@@ -931,6 +936,18 @@ int verify_fp8_call(const void* q, const uint8_t* kv_lat, const float* kv_scale,
     a.rules = rules;
     a.debug_stall = take_debug_stall() ? 1 : 0;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    // Looks for the keys that no draft sees, where the workspace has room for the answer behind `used` bytes and
+    // the CTAs have GAP_TILES tiles or more to gain from.
+    auto look_for_gaps = [&](size_t used, int splits) -> bool {
+        if (!RULES || !has_gaps(rules)) return true;
+        used = align256(used);
+        if (!workspace || !aligned(workspace, 8) || used + (size_t)B * sizeof(int2) > ws_bytes) return true;
+        const long long tiles = ((long long)slot_stride + NK - 1) / NK * (a.balanced ? B : 1);
+        if (tiles < (long long)GAP_TILES * splits) return true;
+        int2* const gaps = reinterpret_cast<int2*>(static_cast<char*>(workspace) + used);
+        a.rules.gaps = gaps;
+        return launch_key_gaps(rules, seq_lens, B, q_len, slot_stride, gaps, st) == cudaSuccess;
+    };
     const int slots = nsplit == 0 && workspace && aligned(workspace, 256) ? fp8_balanced_slots(B, n_tiles, num_sms) : 0;
     if (slots) {
         // streams of unequal length: all their keys in equal chunks over one wave of CTAs
@@ -941,12 +958,13 @@ int verify_fp8_call(const void* q, const uint8_t* kv_lat, const float* kv_scale,
             a.nsplit = slots;
             a.part_out = static_cast<float*>(workspace);
             a.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + out_b);
+            if (!look_for_gaps(out_b + (size_t)slots * per_stream * 4, slots)) return MLA_ERR_LAUNCH;
             if (launch_verify_fp8<RULES>(a, n_tiles, dev, st) != cudaSuccess) return MLA_ERR_LAUNCH;
             VerifyArgs c;                              // what the combine reads of a split call
             memset(&c, 0, sizeof c);
             c.seq_lens = seq_lens; c.B = B; c.q_len = q_len; c.H = H; c.slot_stride = slot_stride;
             c.nsplit = a.nsplit; c.bal_G = a.bal_G; c.part_out = a.part_out; c.part_lse = a.part_lse; c.lse = lse;
-            if (launch_combine_balanced_bf16(c, a.out, NK, RULES ? rules.span() : KeySpan{}, st) != cudaSuccess) return MLA_ERR_LAUNCH;
+            if (launch_combine_balanced_bf16(c, a.out, NK, RULES ? a.rules.span() : KeySpan{}, st) != cudaSuccess) return MLA_ERR_LAUNCH;
             return MLA_OK;
         }
     }
@@ -962,6 +980,7 @@ int verify_fp8_call(const void* q, const uint8_t* kv_lat, const float* kv_scale,
         a.part_out = static_cast<float*>(workspace);
         a.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256((size_t)rows * ns * D_V * 4));
     }
+    if (!look_for_gaps(ns > 1 ? mla_verify_workspace_bytes(B, q_len, H, ns) : 0, ns)) return MLA_ERR_LAUNCH;
     if (launch_verify_fp8<RULES>(a, n_tiles, dev, st) != cudaSuccess) return MLA_ERR_LAUNCH;
     if (ns > 1 && launch_combine_bf16(a.part_out, a.part_lse, rows, ns, a.out, lse, st) != cudaSuccess)
         return MLA_ERR_LAUNCH;

@@ -131,6 +131,63 @@ def test_positions_in_any_order(cuda_lib):
     check(cuda_lib, s, lr.Rules(slopes=lr.slopes(8), key_pos=pos, window=40, prefix_lens=np.array([12], np.int32)))
 
 
+def packed(lens, stride, cuts):
+    """Documents one behind the other: stream b's start at the given shares of its keys."""
+    doc = np.zeros((len(lens), stride), np.int32)
+    for b, n in enumerate(lens):
+        for i, c in enumerate(cuts):
+            doc[b, int(c * n):] = i + 1
+    return doc
+
+
+@pytest.mark.parametrize("kind", ["last", "two", "first", "shared", "blocks", "hidden", "seen", "window", "all"])
+@pytest.mark.parametrize("lens,q_len,H,nsplit", [
+    ([900, 37, 640], 3, 2, 1), ([700, 31, 32, 33], 1, 24, 3), ([24000, 20000, 90], 2, 1, 0), ([20000], 1, 2, 20)])
+def test_keys_that_no_draft_sees(cuda_lib, kind, lens, q_len, H, nsplit):
+    """Long runs of keys of other documents or behind the window are left out: at the beginning, between, up to the
+    drafts, in pieces, none and all of them."""
+    s = lr.Step(29 + len(lens), lens, q_len, H)
+    B, st = s.B, s.stride
+    doc, more = packed(lens, st, (0.3, 0.62)), {}
+    if kind == "two":                                     # drafts of the last two documents
+        for b, n in enumerate(lens):
+            doc[b, n - q_len:n - q_len // 2] = 1
+    elif kind == "first":                                 # drafts of the first one, behind another's keys
+        for b, n in enumerate(lens):
+            doc[b, n - q_len:n] = 0
+    elif kind == "shared":
+        doc[:, :70] = -1
+        doc[:, ::611] = -1
+    elif kind == "blocks":
+        doc = np.broadcast_to((np.arange(st, dtype=np.int32) // 32 % 3) * 2, (B, st)).copy()
+    elif kind == "hidden":
+        doc[:] = 5
+        for b, n in enumerate(lens):
+            doc[b, n - q_len:n] = 6
+    elif kind == "seen":
+        doc[:] = 2
+    elif kind in ("window", "all"):
+        more = dict(key_pos=lr.gaps(5, B, st), window=150, prefix_lens=np.full(B, 40, np.int32))
+        if kind == "window":
+            doc = None
+        else:
+            more.update(softcap=20.0, slopes=lr.slopes(H))
+    check(cuda_lib, s, lr.Rules(key_doc=doc, **more), nsplit=nsplit)
+
+
+def test_slots_of_keys_that_no_draft_sees(cuda_lib):
+    """What lies in the middle of a long run of another document's keys is not looked at."""
+    s = lr.Step(31, [9000, 6000], 4, 2)
+    rules = lr.Rules(key_doc=packed([9000, 6000], s.stride, (0.25, 0.75)))
+    want = check(cuda_lib, s, rules, nsplit=2)
+    args = list(s.on("cuda"))
+    table = args[4].clone()
+    table[:, 2500:4200] = -1
+    args[4] = table
+    out, lse = cuda_lib.verify_attn_fp8_rules(*args, SCALE, **rules.on("cuda"), nsplit=2)
+    assert cuda_lib.device_status() == 0 and torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
 def test_wide_table_many_streams_and_a_stream(cuda_lib):
     """More streams than the balanced split takes, a table wider than any, another stream, out and lse given."""
     lens = [4 + 7 * (i % 30) for i in range(70)]
