@@ -366,7 +366,8 @@ int mla_verify_attn_fp8_rules(const void* q, const uint8_t* kv_lat, const float*
  *   counted  uint8 [B, q_len], or NULL: every draft counts (else e.g. only the accepted ones)
  *   weights  fp32 [B, slot_stride], or NULL: zeros;  decay finite
  *   out      fp32 [B, slot_stride], may be `weights`; entries from seq_lens[b] on stay as they were
- *   workspace  device scratch of ws_bytes >= mla_key_weights_workspace_bytes(); NULL where that is 0
+ *   workspace  device scratch of ws_bytes >= mla_key_weights_workspace_bytes(); NULL where that is 0.  8 bytes a
+ *            stream more behind it, as for mla_verify_attn_fp8_rules(), let long streams be searched
  *   q, the cache, table, lengths, masks, rules, limits and errors as for mla_verify_attn_fp8_rules();
  *   of a stream with a bad length nothing is written.  slot_stride is at most MLA_MAX_FP8_KEYS.  Where a wait
  *   expired (MLA_DEV_TIMEOUT), keys without a sum are NaN.
@@ -388,7 +389,7 @@ int mla_key_weights(const void* q, const void* kv_cache, int64_t n_pool, const i
 
 /*
  * Bytes of workspace that mla_key_weights_fp8() and mla_key_weights() need: 0 up to 128 rows (q_len * H), else
- * 4 bytes a key and 128 rows.  Pure host function; 0 where an argument is out of range.
+ * 4 bytes a key and 128 rows.  4-byte aligned (8, to be searched).  Pure host function; 0 where an argument is out of range.
  */
 size_t mla_key_weights_workspace_bytes(int B, int q_len, int H, int slot_stride);
 

@@ -702,8 +702,11 @@ def _key_weights(fn, cache, n_pool, q, slot_table, seq_lens, draft_mask, scale, 
                     out.zero_()
             else:
                 out = weights
-        if workspace is None and q_len * H > 128:
+        hidden = stride >= 1024 and (key_doc is not None or (key_pos is not None and window > 0))
+        if workspace is None and (q_len * H > 128 or hidden):
             need = int(load().mla_key_weights_workspace_bytes(B, q_len, H, stride))
+            if hidden:
+                need += 256 + 8 * B                        # room to look for keys that no draft sees
             workspace = _empty(lse, (max(need, 256),), torch.uint8, stream)
         _check(fn, _call(fn)(
             *(t.data_ptr() for t in cache), n_pool, slot_table.data_ptr(), stride, seq_lens.data_ptr(), mask, bits, B,

@@ -7,7 +7,7 @@ import torch
 import long_ref as lr
 import step_ref as ref
 import workloads as w
-from test_gpu_attn_rules import KINDS, rules_of
+from test_gpu_attn_rules import KINDS, packed, rules_of
 
 pytestmark = pytest.mark.gpu
 SCALE = w.default_scale()
@@ -22,7 +22,7 @@ def true_lse(s, rules):
     return l.astype(np.float32)
 
 
-def check(mv, s, rules, *, counted=None, decay=0.9, weights=True, lse=None, inplace=False, status=0):
+def check(mv, s, rules, *, counted=None, decay=0.9, weights=True, lse=None, inplace=False, status=0, **kw):
     lse = true_lse(s, rules) if lse is None else lse
     g = torch.Generator().manual_seed(5)
     old = torch.rand((s.B, s.stride), generator=g) * 3 if weights else None
@@ -33,7 +33,7 @@ def check(mv, s, rules, *, counted=None, decay=0.9, weights=True, lse=None, inpl
         out, before = dev_old, old
     args = s.on("cuda")
     got = call(mv, s, args, torch.from_numpy(lse).cuda(), weights=dev_old, decay=decay, out=out,
-               counted=None if counted is None else torch.from_numpy(counted).cuda(), **rules.on("cuda"))
+               counted=None if counted is None else torch.from_numpy(counted).cuda(), **rules.on("cuda"), **kw)
     torch.cuda.synchronize()
     assert mv.device_status() == status
     want, tol = lr.key_weights(ref.f64(s.q), s.keys_of, s.seq, s.mask, SCALE, rules, lse.astype(np.float64), counted,
@@ -259,3 +259,26 @@ def test_rows_of_every_size(cuda_lib):
     s.q[0, 1, 3, 100] = float("inf")
     got = call(cuda_lib, s, s.on("cuda"), torch.from_numpy(lse).cuda())
     assert torch.isnan(got[0, :198]).all() and torch.isfinite(got[0, 198:200]).all()   # the keys that draft 1 sees
+
+
+@pytest.mark.parametrize("cache", ["fp8", "bf16"])
+@pytest.mark.parametrize("kind", ["docs", "window", "hidden", "seen"])
+@pytest.mark.parametrize("lens,q_len,H", [([700 - i for i in range(100)], 1, 1), ([3300, 2900], 16, 128), ([9000, 40], 32, 64)])
+def test_keys_that_no_draft_sees(cuda_lib, cache, kind, lens, q_len, H):
+    """Long runs of hidden keys are left out: their former weights decay, with one row tile and with several."""
+    s = lr.Step(41, lens, q_len, H, cache=cache)
+    doc = packed(lens, s.stride, (0.3, 0.7))
+    if kind == "hidden":
+        doc[:] = 3
+        for b, n in enumerate(lens):
+            doc[b, n - q_len:n] = 4
+    elif kind == "seen":
+        doc[:] = 1
+    rules = lr.Rules(key_doc=doc)
+    if kind == "window":
+        rules = lr.Rules(key_pos=lr.gaps(3, s.B, s.stride), window=200, prefix_lens=np.full(s.B, 64, np.int32))
+    need = cuda_lib.load().mla_key_weights_workspace_bytes(s.B, q_len, H, s.stride)
+    room = torch.empty(need + 256 + 8 * s.B, dtype=torch.uint8, device="cuda")
+    for inplace in (False, True):
+        check(cuda_lib, s, rules, inplace=inplace, workspace=room)
+    check(cuda_lib, s, rules, weights=False, workspace=room)
