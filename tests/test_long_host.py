@@ -71,7 +71,7 @@ def test_evict_workspace(lib):
     ws = lib.mla_kv_evict_workspace_bytes
     assert ws(1, 8192, 1, 152) == 0 and ws(1, 16 * 8192, 0, 152) == 0 and ws(64, 16384, 1, 152) == 0
     up = lambda x: (x + 255) // 256 * 256
-    want = lambda B, n, k: up(B * 8258 * 4) + up(B * 24) + up(B * -(-n // 8192) * 4) + up(B * -(-n // 8192) * 128) + k * up(B * n * 4)
+    want = lambda B, n, k: up(B * 8258 * 4) + up(B * 4) + up(B * 24) + up(B * -(-n // 8192) * 4) + up(B * -(-n // 8192) * 128) + k * up(B * n * 4)
     assert ws(64, 16385, 0, 152) == want(64, 16385, 2) and ws(2, 1 << 20, 1, 152) == want(2, 1 << 20, 6)
     assert ws(0, 1 << 20, 0, 152) == ws(65536, 1 << 20, 0, 152) == ws(2, 0, 0, 152) == ws(2, (1 << 30) + 1, 0, 152) == 0
     assert ws(2, 1 << 20, 0, 0) == 0
