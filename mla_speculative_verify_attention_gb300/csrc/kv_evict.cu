@@ -117,10 +117,12 @@ struct Keys {
 #pragma unroll
         for (int i = 0; i < N; ++i) w[i] = i < items && j0 + 32 * i < n ? at[32 * i] : 0.f;
     }
-    __device__ __forceinline__ void fetch(const EvictArgs& a, int n, int64_t row, int j0, int items) {
+    __device__ __forceinline__ void fetch_slots(const EvictArgs& a, int n, int64_t row, int j0, int items) {
         const int32_t* const slots = a.slot + row + j0;
 #pragma unroll
         for (int i = 0; i < N; ++i) slot[i] = i < items && j0 + 32 * i < n ? slots[32 * i] : 0;
+    }
+    __device__ __forceinline__ void fetch(const EvictArgs& a, int n, int64_t row, int j0, int items) {
         if (a.pos_out) {
             const int32_t* const at = a.key_pos + row + j0;
 #pragma unroll
@@ -243,17 +245,11 @@ __device__ __forceinline__ void find_bin(cg::cluster_group& cluster, int C, int 
             v[0] = s.groups[pass][2 * lane];
             v[1] = s.groups[pass][2 * lane + 1];
         } else {
-            int x[MAX_CLUSTER][2];
-#pragma unroll
-            for (int r = 0; r < MAX_CLUSTER; ++r) {
-                const int2 y = r < C ? *reinterpret_cast<const int2*>(cluster.map_shared_rank(&s.groups[pass][2 * lane], r)) : make_int2(0, 0);
-                x[r][0] = y.x;
-                x[r][1] = y.y;
-            }
-#pragma unroll
-            for (int r = 0; r < MAX_CLUSTER; ++r) {
-                v[0] += x[r][0];
-                v[1] += x[r][1];
+#pragma unroll 4
+            for (int r = 0; r < C; ++r) {
+                const int2 y = *reinterpret_cast<const int2*>(cluster.map_shared_rank(&s.groups[pass][2 * lane], r));
+                v[0] += y.x;
+                v[1] += y.y;
             }
         }
         const unsigned hit = __ballot_sync(0xffffffffu, find_in_warp(v, want, &at, &left, &in));
@@ -304,6 +300,7 @@ __global__ void __launch_bounds__(NT, 1) kv_evict_kernel(const EvictArgs a, int 
     const int j0 = (rank * NT + warp * 32) * items + lane, n = p.bad ? 0 : p.n;
     Keys<ITEMS, true> keys;
     keys.fetch_weights(a, n, row, j0, items);
+    keys.fetch_slots(a, n, row, j0, items);
     for (int i = tid; i < ALL_BINS / 4; i += NT) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
     if (C > 1) cluster.sync();                           // every CTA runs, and has read the length
     else __syncthreads();
@@ -573,6 +570,7 @@ __global__ void __launch_bounds__(TAKE_NT, DOCS ? 4 : 5) kv_evict_take(const Evi
     if (first >= n && blockIdx.x > 0) return;            // (the stream's first CTA writes its lengths)
     Keys<TAKE_ITEMS, DOCS> keys;
     keys.fetch_weights(a, n, row, j0, TAKE_ITEMS);
+    keys.fetch_slots(a, n, row, j0, TAKE_ITEMS);
     keys.fetch(a, n, row, j0, TAKE_ITEMS);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Border o = a.border[b];
