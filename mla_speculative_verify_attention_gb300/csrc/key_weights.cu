@@ -24,6 +24,19 @@
 //            shuffles), the four warps' sums in shared memory.  Up to 64 rows stand in TMEM twice, and
 //            a thread takes 8 keys: a warp reaches one quadrant of the lanes only, the one of its own
 //            scheduler, and two of the four schedulers would have nothing to do
+//
+// What bounds it.  Eight streams of 9 x 8 rows, 190 thousand keys: 31.5 us captured, the gather: scattered rows of 512
+// bytes come from HBM at 4.3 TB/s at most, with cp.async from 1 to 16 warps as with bulk copies of a row (through
+// registers 3.4; from L2 8.7, 8.1 and 6.5).  The bf16 cache, 32 streams of 64 rows, 108 MB: 24.3 us, 4.5 TB/s.  64 x 64 rows
+// over 4160 keys: 31.6 us, 6 of them the queries' conversion of a CTA, the rest 33 tiles between products (0.4 us a
+// tile) and score warps.  One tile: 8.3 us.  Forms that were measured and not kept: keys as rows of the products (M = 128
+// keys, Q as the other operand, from shared memory) 33.6, 37.8 (bf16) and 48 us; rows by gathering tensor copies, 69
+// cycles for 128 bytes of four rows; eight score warps 42 us on the first; codes widened to bf16, tiles of 48 keys, the first
+// form here, 50.6.
+//
+// Masks are decided for a warp's keys as a whole from their least and greatest position and document, key by
+// key only where that does not do (8 streams of 46000 keys, documents: 70 us, key by key throughout 95).
+//
 // More than 128 rows: a row tile a CTA, whose sums meet in the workspace (4 bytes a key and row tile; a
 // second small kernel adds them in order).  Sums have a fixed order: equal calls give equal bits.
 #include "../../include/mla_verify.h"
