@@ -23,7 +23,7 @@ __device__ __forceinline__ Run join(const Run& x, const Run& y) {
     return z;
 }
 
-// A cluster (or, of short streams, a CTA) a stream; a warp takes consecutive groups of 32 keys.
+// A cluster (of short streams, or of many, a CTA) a stream; a warp takes consecutive groups of 32 keys.
 __global__ void __launch_bounds__(GAP_NT) key_gaps_kernel(const ScoreRules r, const int32_t* seq_lens, int q_len, int slot_stride,
                                                           int C, int2* gaps) {
     __shared__ Run warps[GAP_NT / 32], ctas[GAP_CLUSTER];
@@ -98,7 +98,9 @@ __global__ void __launch_bounds__(GAP_NT) key_gaps_kernel(const ScoreRules r, co
 
 cudaError_t launch_key_gaps(const ScoreRules& r, const int32_t* seq_lens, int B, int q_len, int slot_stride, int2* gaps,
                             cudaStream_t stream) {
-    const int C = slot_stride > 8192 ? GAP_CLUSTER : 1;
+    // (clusters of eight reach 120 of the SMs at once)
+    int C = slot_stride > 8192 ? GAP_CLUSTER : 1;
+    while (C > 1 && (long long)B * C > 120) C /= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(B * C));
     cfg.blockDim = dim3(GAP_NT);

@@ -175,6 +175,13 @@ def test_keys_that_no_draft_sees(cuda_lib, kind, lens, q_len, H, nsplit):
     check(cuda_lib, s, lr.Rules(key_doc=doc, **more), nsplit=nsplit)
 
 
+@pytest.mark.parametrize("B", [20, 50, 130])
+def test_keys_that_no_draft_sees_of_many_streams(cuda_lib, B):
+    lens = [8200 + 37 * (i % 5) if i % 4 == 0 else 40 + i for i in range(B)]
+    s = lr.Step(37, lens, 1, 1)
+    check(cuda_lib, s, lr.Rules(key_doc=packed(lens, s.stride, (0.2, 0.9))), nsplit=8)
+
+
 def test_slots_of_keys_that_no_draft_sees(cuda_lib):
     """What lies in the middle of a long run of another document's keys is not looked at."""
     s = lr.Step(31, [9000, 6000], 4, 2)
