@@ -247,3 +247,26 @@ def test_captured(cuda_lib):
         torch.cuda.synchronize()
         o, l, t_out, t_lse = lr.attention(ref.f64(s.q), s.keys_of, s.seq, None, SCALE, rules)
         assert np.all(np.abs(ref.f64(out) - o) <= t_out) and np.all(np.abs(ref.f64(lse) - l) <= t_lse)
+
+
+def test_captured_search(cuda_lib):
+    """A captured call looks for hidden keys anew at each replay: other documents, other lengths."""
+    mv = cuda_lib
+    s = lr.Step(53, [900, 700], 3, 4)
+    rules = lr.Rules(key_doc=packed([900, 700], s.stride, (0.4, 0.8)))
+    args, on = s.on("cuda"), rules.on("cuda")
+    call = lambda: mv.verify_attn_fp8_rules(*args, SCALE, **on, nsplit=1)
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = call()
+    for cuts, lens in (((0.4, 0.8), (900, 700)), ((0.1, 0.2), (900, 650)), ((0.9, 0.95), (3, 700)), ((2.0, 2.0), (810, 333))):
+        on["key_doc"].copy_(torch.from_numpy(packed([900, 700], s.stride, cuts)))
+        args[5].copy_(torch.tensor(lens, dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        want = call()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and mv.device_status() == 0
+        s.seq = np.array(lens, np.int32)
+        check(mv, s, lr.Rules(key_doc=packed([900, 700], s.stride, cuts)), nsplit=1)
