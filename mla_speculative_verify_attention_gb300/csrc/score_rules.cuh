@@ -116,7 +116,7 @@ struct ScoreRules {
 
 // Whether keys that no draft sees can lie together without being known from the lengths alone.
 inline bool has_gaps(const ScoreRules& r) { return r.key_doc || (r.key_pos && r.window > 0); }
-// Finds (3 us, a cluster of eight CTAs for long streams) each stream's longest run of keys before the drafts that none of them sees (in whole groups of 32):
+// Finds (a cluster of eight CTAs for long streams) each stream's longest run of keys before the drafts that none of them sees (in whole groups of 32):
 // gaps[b] = its first key, its keys.
 cudaError_t launch_key_gaps(const ScoreRules& r, const int32_t* seq_lens, int B, int q_len, int slot_stride, int2* gaps,
                             cudaStream_t stream);
