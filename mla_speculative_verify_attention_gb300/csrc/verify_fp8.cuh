@@ -664,7 +664,7 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
                         if (before < 64) see = before > 0 ? vis << before | ((1ull << before) - 1) : before > -64 ? vis >> -before : 0;
                     }
                     if (a.rules.masked) {
-                        // the tile's keys as a whole, and one by one only where that does not decide
+                        // the tile's keys as a whole, and each of them only where that does not decide
                         int4 span;
                         if (a.rules.spans) {
                             const int4 part = M.key_span[st * WIDE_WARPS + (lane & (WIDE_WARPS - 1))];
@@ -680,15 +680,25 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
                             if (none) see = 0;
                         } else {
                             see = 0;
-                            // lane l holds keys l and 32 + (l & 15)
+                            // lane l looks at keys l and 32 + (l & 15), for one draft of the warp's rows after the other
                             const int v0 = k0 + lane, v1 = k0 + 32 + (lane & 15);
                             const int pos0 = key_pos(v0), pos1 = key_pos(v1), doc0 = key_doc(v0), doc1 = key_doc(v1);
+                            unsigned todo = __ballot_sync(0xffffffffu, row_ok);
 #pragma unroll 1
-                            for (int k = 0; k < NK; ++k) {
-                                const int kp = __shfl_sync(0xffffffffu, k < 32 ? pos0 : pos1, k & 31);
-                                const int kd = __shfl_sync(0xffffffffu, k < 32 ? doc0 : doc1, k & 31);
-                                const int j = k0 + k - p;    // draft index, < 0: before the drafts
-                                see |= (uint64_t)rule.sees(j < 0 || ((vis >> (j & 63)) & 1ull), kp, kd) << k;
+                            while (todo) {
+                                const int lead = __ffs(todo) - 1;
+                                RowRule one;
+                                one.lo = __shfl_sync(0xffffffffu, rule.lo, lead);
+                                one.prefix = __shfl_sync(0xffffffffu, rule.prefix, lead);
+                                one.doc = __shfl_sync(0xffffffffu, rule.doc, lead);
+                                const uint64_t drafts = __shfl_sync(0xffffffffu, vis, lead);
+                                const int j0 = v0 - p, j1 = v1 - p;   // draft indices, < 0: before the drafts
+                                const uint64_t lower = __ballot_sync(0xffffffffu, one.sees(j0 < 0 || ((drafts >> (j0 & 63)) & 1ull), pos0, doc0));
+                                const uint64_t upper = __ballot_sync(0xffffffffu, one.sees(j1 < 0 || ((drafts >> (j1 & 63)) & 1ull), pos1, doc1));
+                                const int its = __shfl_sync(0xffffffffu, t, lead);   // (by every lane: not behind row_ok)
+                                const bool mine = row_ok && t == its;
+                                if (mine) see = lower | (upper & 0xffffull) << 32;
+                                todo &= ~__ballot_sync(0xffffffffu, mine);
                             }
                         }
                     }
