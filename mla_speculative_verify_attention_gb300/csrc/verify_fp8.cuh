@@ -46,8 +46,9 @@
 // (score_rules.cuh).  The bias's part that belongs to the row, slope x (row's position - the stream's last), is added
 // to the log-sum-exp instead of to every key.  The gather leaves the positions' distances and, a warp, the
 // least and greatest position and document of its six keys; from those a row knows most tiles to be seen whole or
-// not at all, and only others are looked at key by key.  Rules cost the softmax 0.5 to 1 us a tile (32 streams of 64
-// rows, nine tiles a CTA: none 39 us a call, a bias 43, a cap 47, documents 46) and a first pass through their code.
+// not at all; of others a lane looks at a key for one draft after the other.  Rules cost the softmax up to 0.6 us a tile
+// (32 streams of 64 rows, nine tiles a CTA: none 39 us a call, a bias 41, a cap 47, documents of which half are
+// hidden 41) and a first pass through their code.
 //
 // Warps (512 threads): 0 issues A and C, 1 issues O^T (whole warp, one elected lane), 4-7 Q,
 // softmax and epilogue (TMEM lane quadrant = warp % 4), 8-15 gather and widening (six keys of
