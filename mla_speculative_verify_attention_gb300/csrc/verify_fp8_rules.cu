@@ -29,13 +29,14 @@ __global__ void __launch_bounds__(GAP_NT) key_gaps_kernel(const ScoreRules r, co
     __shared__ Run warps[GAP_NT / 32], ctas[GAP_CLUSTER];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const cg::cluster_group cluster = cg::this_cluster();
+    cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.x / C, rank = blockIdx.x % C;
     const int n = seq_lens[b];
-    if (n < q_len || n > slot_stride) {
+    if (n < q_len || n > slot_stride) {                  // (the cluster as a whole)
         if (rank == 0 && tid == 0) gaps[b] = make_int2(0, 0);
         return;
     }
+    if (C > 1) cluster.barrier_arrive();                 // this CTA runs: the wait is where another's memory is written
     const int64_t row = (int64_t)b * slot_stride;
     const int p = n - q_len;
     // documents and window of all drafts together
@@ -86,6 +87,7 @@ __global__ void __launch_bounds__(GAP_NT) key_gaps_kernel(const ScoreRules r, co
     Run all = {};
     if (warp == 0) all = reduce(warps[lane], 32);
     if (C > 1) {
+        cluster.barrier_wait();                          // every CTA of the cluster runs
         if (tid == 0) *cluster.map_shared_rank(&ctas[rank], 0) = all;
         cluster.sync();
         if (rank > 0) return;
