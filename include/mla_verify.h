@@ -330,7 +330,7 @@ size_t mla_verify_fp8_workspace_bytes(int B, int q_len, int H, int max_seq, int 
  *     key j is visible to draft t  iff  ( (draft mask and window) or pos(j) < prefix_lens[b] )
  *                                       and ( doc(j) == doc(j_t) or doc(j) < 0 )
  *     draft mask  j < seq_lens[b] - q_len, or the mask's bit of draft j;   window  pos(j_t) - pos(j) < window
- *   softcap     finite, >= 0 (0: no cap)
+ *   softcap     finite, >= 0 (0: no cap; above 2.358e38, 2^128 ln 2, it counts as that)
  *   slopes      fp32 [H], or NULL: no bias.  A positive slope favours near keys.
  *   key_pos     int32 [B, slot_stride], any order (mla_kv_evict() leaves a table whose positions have gaps),
  *               or NULL.  Positions that a bias compares are less than 2^31 apart.

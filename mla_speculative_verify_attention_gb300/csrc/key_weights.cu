@@ -524,8 +524,7 @@ __global__ void __launch_bounds__(NT, 1) key_weights_kernel(const WeightArgs a) 
         const float off = -lse * LOG2E;
         RowRule rule;
         if (RULES) rule = a.rules.row(b, t, row_ok ? (row0 + r) % a.H : 0, p + gap, a.slot_stride, false);
-        const float cap_in = RULES && a.rules.softcap > 0.f ? c2 / (a.rules.softcap * LOG2E) : 0.f;
-        const float cap_out = RULES ? a.rules.softcap * LOG2E : 0.f;
+        const float in = RULES && a.rules.softcap > 0.f ? cap_in(c2, a.rules.softcap) : 0.f;
         const bool any_live = __any_sync(0xffffffffu, live);
         constexpr uint32_t ALL_KEYS = (1u << KW) - 1u;
         int ring = set;
@@ -586,9 +585,10 @@ __global__ void __launch_bounds__(NT, 1) key_weights_kernel(const WeightArgs a) 
                 for (int k = 0; k < KW; ++k) {
                     const float x = __uint_as_float(va[k]), y = __uint_as_float(vl[k]), z = __uint_as_float(vc[k]);
                     const float dot = FP8 ? fmaf(fmaf(y, 0.0625f, x), ks[k], z) : x + y + z;
-                    e[k] = RULES && a.rules.softcap > 0.f ? dot * cap_in : fmaf(dot, c2, off);
+                    e[k] = RULES && a.rules.softcap > 0.f ? dot * in : fmaf(dot, c2, off);
                 }
                 if (RULES && a.rules.softcap > 0.f) {
+                    const float out = cap_out(c2, a.rules.softcap, in);   // (held over the tiles: 35.7 instead of 35.2 us)
                     float top = 0.f;
 #pragma unroll
                     for (int k = 0; k < KW; ++k) top = fmaxf(top, fabsf(e[k]));
@@ -596,14 +596,14 @@ __global__ void __launch_bounds__(NT, 1) key_weights_kernel(const WeightArgs a) 
                     if (__all_sync(0xffffffffu, top <= 1.f)) {
 #pragma unroll
                         for (int k = 0; k < KW; k += 2) {
-                            const float2 y = fma2(tanh_near(make_float2(e[k], e[k + 1])), both(cap_out), both(off));
+                            const float2 y = fma2(tanh_near(make_float2(e[k], e[k + 1])), both(out), both(off));
                             e[k] = y.x;
                             e[k + 1] = y.y;
                         }
                     } else {
 #pragma unroll
                         for (int k = 0; k < KW; k += 2) {
-                            const float2 y = fma2(tanh2(make_float2(e[k], e[k + 1])), both(cap_out), both(off));
+                            const float2 y = fma2(tanh2(make_float2(e[k], e[k + 1])), both(out), both(off));
                             e[k] = y.x;
                             e[k + 1] = y.y;
                         }

@@ -6,6 +6,7 @@
 // A draft's position and document are those of its own key.
 #pragma once
 
+#include <float.h>
 #include <limits.h>
 #include <stdint.h>
 
@@ -57,6 +58,20 @@ __device__ __forceinline__ float2 tanh2(float2 u) {
     const float2 near = tanh_near(u);
     return make_float2(fabsf(u.x) <= 1.f ? near.x : tanh_far(u.x), fabsf(u.y) <= 1.f ? near.y : tanh_far(u.y));
 }
+
+// A row's capped scores in log2 units are cap_out tanh(cap_in x), where c2 x are the uncapped ones.  Under the largest
+// caps cap_in would lose its bits below 2^-126: there tanh is its argument for every x below 2^88, and so it is with
+// PLAIN_IN.  Under the smallest ones cap_in stays finite: a score of 0 is 0.
+constexpr float PLAIN_IN = 0x1p-100f;
+__device__ __forceinline__ float cap_in(float c2, float softcap) {
+    const float in = c2 / (softcap * 1.4426950408889634f);
+    return fabsf(in) < 0x1p-126f ? PLAIN_IN : fminf(fmaxf(in, -FLT_MAX), FLT_MAX);
+}
+__device__ __forceinline__ float cap_out(float c2, float softcap, float in) {
+    return in == PLAIN_IN ? c2 * 0x1p100f : softcap * 1.4426950408889634f;
+}
+// Caps are at most this: in log2 units they are below 2^128.
+constexpr float MAX_CAP = 0x1.62e4p127f;
 
 // One query row's part of the rules.
 struct RowRule {

@@ -545,8 +545,8 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
         const int plain_end = min(p, k_end);             // keys below this need no mask (of drafts)
         RowRule rule;
         if (RULES) rule = a.rules.row(b, t, row_ok ? (row0 + r) % a.H : 0, p + gap, a.slot_stride, bad_len);
-        const float cap_in = RULES && a.rules.softcap > 0.f ? c2 / (a.rules.softcap * LOG2E) : 0.f;
-        const float cap_out = RULES ? a.rules.softcap * LOG2E : 0.f;
+        const float in = RULES && a.rules.softcap > 0.f ? cap_in(c2, a.rules.softcap) : 0.f;
+        const float capped = RULES && a.rules.softcap > 0.f ? cap_out(c2, a.rules.softcap, in) : 0.f;
         // The bias is slope (key's distance from the stream's last position - the row's): the second part, the same
         // for all of the row's keys, waits for the log-sum-exp.  Where it is large (bits would be lost beside it), or
         // the distances are no fp32 numbers, the warp takes the differences of positions instead.
@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
                         float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                         for (int k = 0; k < NK; k += 2) {
-                            put(k, mul2(pair(k), both(cap_in)));
+                            put(k, mul2(pair(k), both(in)));
                             top[k & 2] = fmaxf(top[k & 2], fabsf(x[k]));
                             top[(k & 2) + 1] = fmaxf(top[(k & 2) + 1], fabsf(x[k + 1]));
                         }
@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(NT, 1) verify_fp8_kernel(const Fp8Args a) {
 #pragma unroll
                             for (int k = 0; k < NK; k += 2) put(k, tanh2(pair(k)));
                         }
-                        gain = cap_out;
+                        gain = capped;
                     }
 #pragma unroll
                     for (int k = 0; k < NK; k += 4) {

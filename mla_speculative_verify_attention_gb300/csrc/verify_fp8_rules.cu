@@ -125,7 +125,7 @@ int check_rules(float softcap, const float* slopes, const int32_t* key_pos, int 
     if (!aligned(slopes, 4) || !aligned(key_pos, 4) || !aligned(prefix_lens, 4) || !aligned(key_doc, 4))
         return MLA_ERR_ALIGN;
     ScoreRules r;
-    r.softcap = softcap; r.window = window; r.slopes = slopes; r.key_pos = key_pos; r.prefix_lens = prefix_lens;
+    r.softcap = fminf(softcap, MAX_CAP); r.window = window; r.slopes = slopes; r.key_pos = key_pos; r.prefix_lens = prefix_lens;
     r.key_doc = key_doc;
     r.masked = window > 0 || prefix_lens || key_doc;
     r.spans = r.masked && (key_pos || key_doc);
