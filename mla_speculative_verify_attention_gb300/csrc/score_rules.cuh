@@ -47,12 +47,12 @@ __device__ __forceinline__ float2 tanh_near(float2 u) {
     s = fma2(s, w, both(-0.33332985639572144f));
     return fma2(mul2(w, s), u, u);
 }
-// Farther out 1 - 2 / (e^2u + 1): the quotient, at most 0.24 there, is off by 1.5 2^-22 of itself.
+// Farther out 1 - 2 / (e^2|u| + 1) with u's sign: the quotient, at most 0.24 there, is off by 1.5 2^-22 of itself.
 __device__ __forceinline__ float tanh_far(float u) {
-    const float e = ex2(u * 2.8853900817779268f) + 1.f;
+    const float e = ex2(fabsf(u) * 2.8853900817779268f) + 1.f;
     float q;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(e));
-    return fmaf(-2.f, q, 1.f);
+    return copysignf(fmaf(-2.f, q, 1.f), u);
 }
 __device__ __forceinline__ float2 tanh2(float2 u) {
     const float2 near = tanh_near(u);

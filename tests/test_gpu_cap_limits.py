@@ -1,4 +1,5 @@
-"""Caps at the ends of their range: rows that see a single key, whose log-sum-exp is the capped score itself."""
+"""Caps at the ends of their range, and the cap's symmetry: rows that see a single key, whose log-sum-exp is the
+capped score itself."""
 import numpy as np
 import pytest
 import torch
@@ -73,3 +74,15 @@ def test_key_weights(cuda_lib, cap, beside):
     for got in (mv.key_weights_fp8(q, lat, scale, rope, table, seq, None, 1.0, lse, softcap=cap),
                 mv.key_weights(q, kv, table, seq, None, 1.0, lse, softcap=cap)):
         assert np.all(np.abs(ref.f64(got)[:, 0] - 1) <= tol * 1.01), ref.f64(got)
+
+
+def test_capped_scores_are_odd(cuda_lib):
+    """cap tanh(-z / cap) is the negative of cap tanh(z / cap), bit for bit, beyond the cap as within it.  (In log2
+    units these are between 39 and 57 in size: the 7 that the log-sum-exp takes off and adds back are exact.)"""
+    a = np.array([i / 4 for i in range(148, 256)] + [i / 2 for i in range(128, 256)] + list(range(128, 256, 3)))
+    for scale in (1.0, 1.01, 1.7):
+        cap = 37.0
+        up, down = capped(cuda_lib, a, cap, scale), capped(cuda_lib, -a, cap, scale)
+        assert np.array_equal(up, -down), int((up != -down).sum())
+        want = cap * np.tanh(float(np.float32(scale)) * a / cap)
+        assert np.all(np.abs(up - want) <= bound(want))
