@@ -9,6 +9,7 @@
 #include <float.h>
 #include <limits.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "internal.cuh"
 
@@ -22,17 +23,25 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t bits_of(float2 x) {
+    uint64_t v;
+    memcpy(&v, &x, sizeof v);
+    return v;
+}
+__device__ __forceinline__ float2 pair_of(uint64_t v) {
+    float2 x;
+    memcpy(&x, &v, sizeof x);
+    return x;
+}
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(reinterpret_cast<uint64_t&>(d))
-        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
-    return d;
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits_of(a)), "l"(bits_of(b)), "l"(bits_of(c)));
+    return pair_of(d);
 }
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<uint64_t&>(d))
-        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
-    return d;
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits_of(a)), "l"(bits_of(b)));
+    return pair_of(d);
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
