@@ -389,7 +389,9 @@ int mla_key_weights(const void* q, const void* kv_cache, int64_t n_pool, const i
 
 /*
  * Bytes of workspace that mla_key_weights_fp8() and mla_key_weights() need: 0 up to 128 rows (q_len * H), else
- * 4 bytes a key and 128 rows.  4-byte aligned (8, to be searched).  Pure host function; 0 where an argument is out of range.
+ * 4 bytes a key and 128 rows.  4-byte aligned.  Pure host function; 0 where an argument is out of range.
+ * Room for the search for hidden keys is not counted: a workspace of this size rounded up to 256 bytes, and 8 bytes
+ * a stream behind it, 8-byte aligned, lets long streams be searched (a call without it reads the hidden keys too).
  */
 size_t mla_key_weights_workspace_bytes(int B, int q_len, int H, int slot_stride);
 

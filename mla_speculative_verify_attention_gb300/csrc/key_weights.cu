@@ -820,7 +820,9 @@ extern "C" int mla_key_weights(const void* q, const void* kv_cache, int64_t n_po
 }
 
 extern "C" size_t mla_key_weights_workspace_bytes(int B, int q_len, int H, int slot_stride) {
-    if (B <= 0 || q_len < 1 || q_len > MLA_MAX_Q_LEN || H < 1 || H > MLA_MAX_HEADS || slot_stride < 1) return 0;
+    if (B <= 0 || B > 65535 || q_len < 1 || q_len > MLA_MAX_Q_LEN || H < 1 || H > MLA_MAX_HEADS || slot_stride < q_len ||
+        slot_stride > MLA_MAX_FP8_KEYS)
+        return 0;
     int n_tiles, R_step;
     weight_tiling(q_len * H, &n_tiles, &R_step);
     return n_tiles > 1 ? (size_t)n_tiles * B * slot_stride * 4 : 0;
