@@ -103,7 +103,8 @@ __device__ __forceinline__ void store4(__nv_bfloat16* dst, const float4& v) {
         make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
-template <int Z, typename Out>
+// SPAN: with hidden keys (else the plan's code is without them: 0.2 us of 38.3 on 32 decode streams of 64 heads).
+template <int Z, typename Out, bool SPAN>
 __global__ void __launch_bounds__(CB_THREADS) combine_kernel(const float* __restrict__ part_out,
                                                              const float* __restrict__ part_lse, int S_all,
                                                              long long n_items, Out* __restrict__ out,
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(CB_THREADS) combine_kernel(const float* __rest
     long long po = row * (long long)S_all * D_V;
     if (bal.on) {
         const BalancedPlan P = balanced_plan(bal.seq_lens, bal.B, bal.q_len, bal.slot_stride, bal.G,
-                                             bal.unit, bal.least, bal.span);
+                                             bal.unit, bal.least, SPAN ? bal.span : KeySpan{});
         const int b = (int)(row / bal.rows), r = (int)(row % bal.rows);
         int first, count;
         balanced_stream(P, b, &first, &count);
@@ -202,12 +203,12 @@ __global__ void __launch_bounds__(CB_THREADS) combine_kernel(const float* __rest
     }
 }
 
-template <int Z, typename Out>
+template <int Z, bool SPAN, typename Out>
 cudaError_t launch_combine_z(const float* part_out, const float* part_lse, long long n_rows, int S, Out* out,
                              float* lse, const CombineBalanced& bal, cudaStream_t stream) {
     const long long items = n_rows * (D_V / CB_DIMS);
     const long long per_cta = CB_WARPS / Z;
-    return launch_dependent(combine_kernel<Z, Out>, dim3((unsigned)((items + per_cta - 1) / per_cta)),
+    return launch_dependent(combine_kernel<Z, Out, SPAN>, dim3((unsigned)((items + per_cta - 1) / per_cta)),
                             dim3(CB_THREADS), 0, stream, part_out, part_lse, S, items, out, lse, bal);
 }
 
@@ -217,15 +218,15 @@ cudaError_t launch_combine_z(const float* part_out, const float* part_lse, long 
 // 58.3, 1 warp 58.1); one beside a bf16 output, whose streams are often short of splits
 // (32 streams of 64 rows, five splits each: 2 warps 44.5 us per call, 1 warp 38.9; eight
 // streams of 19 splits 75.7 and 75.9)).
-template <typename Out>
+template <bool SPAN = false, typename Out>
 cudaError_t launch_combine_any(const float* part_out, const float* part_lse, long long n_rows, int S, Out* out,
                                float* lse, const CombineBalanced& bal, cudaStream_t stream) {
     if (n_rows <= 0) return cudaSuccess;
     const int per = bal.on ? (sizeof(Out) == 4 ? 2 : 1) * 16 : S;
-    if (per <= 16) return launch_combine_z<1>(part_out, part_lse, n_rows, S, out, lse, bal, stream);
-    if (per <= 32) return launch_combine_z<2>(part_out, part_lse, n_rows, S, out, lse, bal, stream);
-    if (per <= 64) return launch_combine_z<4>(part_out, part_lse, n_rows, S, out, lse, bal, stream);
-    return launch_combine_z<8>(part_out, part_lse, n_rows, S, out, lse, bal, stream);
+    if (per <= 16) return launch_combine_z<1, SPAN>(part_out, part_lse, n_rows, S, out, lse, bal, stream);
+    if (per <= 32) return launch_combine_z<2, SPAN>(part_out, part_lse, n_rows, S, out, lse, bal, stream);
+    if (per <= 64) return launch_combine_z<4, SPAN>(part_out, part_lse, n_rows, S, out, lse, bal, stream);
+    return launch_combine_z<8, SPAN>(part_out, part_lse, n_rows, S, out, lse, bal, stream);
 }
 
 }  // namespace
@@ -255,7 +256,10 @@ cudaError_t combine_balanced(const VerifyArgs& a, Out* out, int unit, int least,
     bal.rows = a.q_len * a.H;
     bal.unit = unit;
     bal.least = least;
-    return launch_combine_any(a.part_out, a.part_lse, (long long)a.B * bal.rows, a.nsplit, out, a.lse, bal, stream);
+    const long long rows = (long long)a.B * bal.rows;
+    if constexpr (sizeof(Out) == 2)                      // (only the attention under rules has hidden keys)
+        if (span.window > 0 || span.gaps) return launch_combine_any<true>(a.part_out, a.part_lse, rows, a.nsplit, out, a.lse, bal, stream);
+    return launch_combine_any(a.part_out, a.part_lse, rows, a.nsplit, out, a.lse, bal, stream);
 }
 }  // namespace
 
