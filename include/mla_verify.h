@@ -338,8 +338,10 @@ size_t mla_verify_fp8_workspace_bytes(int B, int q_len, int H, int max_seq, int 
  *   prefix_lens int32 [B], or NULL: no prefix.  Prefix keys are visible both ways: a draft whose own
  *               position is in the prefix is seen by every draft of its stream.
  *   key_doc     int32 [B, slot_stride], or NULL: one document.  A negative number is shared by all.
- * tanh is off by at most 2^-21 of itself.  A row that sees nothing gets out = 0, lse = -inf.  Every other
- * argument, limit and error is that of mla_verify_attn_fp8(); with nsplit = 0 the workspace that it uses is
+ * tanh is off by at most 2^-21 of itself, and odd.  Under slopes a score is held with up to 64 (in log2 units) of
+ * the draft's own distance from the stream's last position until its row's lse, which rounds it by up to 2^-18.
+ * A row that sees nothing gets out = 0, lse = -inf.  Every other argument, limit and error is that of
+ * mla_verify_attn_fp8(); with nsplit = 0 the workspace that it uses is
  * mla_verify_fp8_workspace_bytes() of max_seq = slot_stride, or of min(slot_stride, window - 1 + q_len)
  * with a window and no key_pos.  Where documents, or positions and a window, are given and the workspace goes on for
  * 8 bytes a stream behind that size rounded up to 256 bytes, long streams are first searched for their

@@ -9,13 +9,13 @@
 // Streams of up to 8192 keys a CTA: a cluster of up to sixteen CTAs a stream, in one kernel; a thread keeps its
 // eight integers in registers.  Everything is read before anything is written, so tables may be compacted
 // in place.
-// One stream of 4105 keys takes 8.9 us captured: dependent reads, counts and barriers.
+// One stream of 4105 keys takes 7.3 to 8.9 us captured: dependent reads, counts and barriers.
 // Longer ones: all SMs share the streams out in chunks of 8192 keys.  One kernel adds the histograms up in the
 // workspace; the next counts what stays for sure and lists the keys of the border's bin, of which each
 // stream's last CTA to finish finds the border and adds those that stay to the counts; the third takes the
-// keys.  A table that is compacted in place passes through the workspace.  64 streams of up to 46 thousand keys take
-// 26.0 us, two of a million 28.1, three dependent kernels of which each starts during the one before it; the bytes alone
-// would take 3.2 and 4.1. 
+// keys.  64 streams of up to 46 thousand keys take 25.6 us, two of a million 27.5, dependent kernels of which each
+// starts during the one before it; the bytes alone would take 3.2 and 4.1.  A table that is compacted in place passes
+// through the workspace and comes back by one kernel more: 36.9 and 35.7 us (behind the copies that restore the tables).
 #include "../../include/mla_verify.h"
 #include "internal.cuh"
 

@@ -44,7 +44,8 @@
 //
 // The RULES form (mla_verify_attn_fp8_rules): x goes through the cap and the bias in log2 units before log2 s_j is added
 // (score_rules.cuh).  The bias's part that belongs to the row, slope x (row's position - the stream's last), is added
-// to the log-sum-exp instead of to every key.  The gather leaves the positions' distances and, a warp, the
+// to the log-sum-exp instead of to every key (up to 64 in size: half a step of such a sum is 2^-18; where it is larger the
+// differences of positions are taken).  The gather leaves the positions' distances and, a warp, the
 // least and greatest position and document of its six keys; from those a row knows most tiles to be seen whole or
 // not at all; of others a lane looks at a key for one draft after the other.  Rules cost the softmax up to 0.6 us a tile
 // (32 streams of 64 rows, nine tiles a CTA: none 39 us a call, a bias 41, a cap 47, documents of which half are
