@@ -132,3 +132,30 @@ def test_key_weights_captured(cuda_lib, lens, q_len, H, cache):
         torch.cuda.synchronize()
         assert np.array_equal(ref.f64(out), counts(c, lr.Rules(key_doc=doc), H, c.table.shape[1])), kind
         assert mv.device_status() == 0
+
+
+def test_bad_lengths(cuda_lib):
+    """Streams of bad lengths between others that are searched: reported and left alone, the others exact."""
+    mv = cuda_lib
+    q_len, H = 2, 4
+    c = Counted(q_len, H, [9000, 8500, 8700, 400], seed=8, mask=True)
+    doc = docs("last", c)[0]
+    rules = lr.Rules(key_doc=doc)
+    want = counts(c, rules, H, c.table.shape[1])
+    seq, call = weights_call(mv, "fp8", c, H)
+    seq[1], seq[2] = 1, 9001
+    want[1:3] = -1
+    out = torch.full(c.table.shape, -1.0, device="cuda")
+    on = rules.on("cuda")
+    call(out, on)
+    assert np.array_equal(ref.f64(out), want) and mv.device_status(clear=True) == 2
+    q = torch.zeros((c.B, q_len, H, 576), dtype=torch.bfloat16, device="cuda")
+    for nsplit in (1, 0):
+        o, lse = (ref.f64(x) for x in mv.verify_attn_fp8_rules(q, cuda(c.lat), cuda(c.scale), cuda(c.rope).to(torch.bfloat16),
+                                                               cuda(c.table), seq, cuda(c.mask), 1.0, nsplit=nsplit, **on))
+        assert mv.device_status(clear=True) == 2
+        assert np.isnan(lse[1:3]).all() and np.all(o[1:3] == 0)
+        for b in (0, 3):
+            for t, see in enumerate(expected_rows(c, rules)[b]):
+                s = c.table[b, :c.seq[b]][see]
+                assert c.agree(o[b, t], lse[b, t], *c.expected(s)), (b, t, nsplit)
